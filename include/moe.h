@@ -392,6 +392,89 @@ int moe_forward_mx(const uint16_t* x, const uint16_t* router_w, const float* rou
                    void* workspace, size_t workspace_bytes,
                    const moe_event_t* stage_events, moe_stream_t stream);
 
+/*
+ * Router with expert groups: scores, a selection bias, group-limited top-k.
+ *   l[t,e] = x[t] . Wr[e] (fp64 sums; moe_route_groups), or the caller's fp32 logits
+ *            (moe_route_logits: row t at logits + t * ld, ld >= E)
+ *   s[t,e] = sigmoid(l) (MOE_SCORE_SIGMOID) or softmax over the E experts (MOE_SCORE_SOFTMAX)
+ *   c[t,e] = s + select_bias[e] (select_bias fp32 [E], finite, or NULL); it selects only
+ *   The experts form n_group groups of E / n_group consecutive ids (1 <= n_group <= 64,
+ *   dividing E).  A group's score is the sum of its group_top (1 or 2) largest c; the
+ *   topk_group groups with the largest scores stay, ties to the lower group.
+ *   topk_ids [M, top_k] int32 out: the largest c in the groups that stay, descending, ties to
+ *            the lower id (top_k <= topk_group * E / n_group); ids are those of the exact sums.
+ *            Without a bias the logits are compared, which order as the scores do.
+ *   topk_w   [M, top_k] fp32 out: s of the picks (without the bias), divided by their sum if
+ *            renormalize is not 0 (a sum of 0 gives weights 0), times scale (finite).
+ * An expert whose logit is -inf (masked) or NaN has no score: weight 0, nothing added to its
+ * group's score, picked only after every scored expert of the groups that stay, in id order;
+ * a group without a scored expert ranks last.  A token whose experts are all masked gets
+ * weights 0.  Every row of topk_ids holds distinct experts.
+ * n_group = topk_group = group_top = 1 routes without groups.
+ *   workspace: >= moe_route_groups_workspace_bytes(M, E) bytes (0 for invalid sizes), 16-byte
+ *   aligned; moe_route_logits needs none, and only 4-byte alignment of its pointers.
+ */
+enum { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 };
+size_t moe_route_groups_workspace_bytes(int32_t M, int32_t E);
+int moe_route_groups(const uint16_t* x, const uint16_t* router_w, const float* select_bias,
+                     int32_t M, int32_t H, int32_t E, int32_t top_k,
+                     int32_t score, int32_t n_group, int32_t topk_group, int32_t group_top,
+                     int32_t renormalize, float scale,
+                     int32_t* topk_ids, float* topk_w,
+                     void* workspace, size_t workspace_bytes, moe_stream_t stream);
+int moe_route_logits(const float* logits, int64_t ld, const float* select_bias,
+                     int32_t M, int32_t E, int32_t top_k,
+                     int32_t score, int32_t n_group, int32_t topk_group, int32_t group_top,
+                     int32_t renormalize, float scale,
+                     int32_t* topk_ids, float* topk_w, moe_stream_t stream);
+
+/*
+ * 8-bit integer rows and their matrix product.
+ * moe_i8_quantize: v [rows, K] bf16 -> codes [rows, K] int8 and scales [rows] fp32: with a the
+ *   row's largest magnitude, scale = a / 127 and code = 127 v / a rounded to nearest, ties to
+ *   even (exactly); a row of zeros gets scale 0 and codes 0; a row with a NaN or an infinity
+ *   gets a scale that is not finite and codes 0, so that what is computed from it is not
+ *   finite.  Weights [N, K] quantized so have a scale per output channel, tokens [M, K] one
+ *   per token.  K % 16 == 0, 16 <= K <= 131072; v and codes 16-byte, scales 4-byte aligned.
+ * moe_i8_matmul: out[m, n] = a_scales[m] * w_scales[n] * sum_k a[m, k] * w[n, k] for a [M, K]
+ *   and w [N, K] int8 (K as above); the sums are exact (int32), the scaling fp32.  out [M, N]
+ *   is bf16, or fp32 with out_f32 = 1.  M >= 0 and N >= 1 are any.  a, w, w_scales and out
+ *   16-byte, a_scales 4-byte aligned.  The workspace holds moe_i8_matmul_workspace_bytes
+ *   bytes, 256-byte aligned (it may be NULL where that is 0); its contents are not kept.
+ */
+int moe_i8_quantize(const uint16_t* v, int64_t rows, int32_t K, int8_t* codes, float* scales,
+                    moe_stream_t stream);
+size_t moe_i8_matmul_workspace_bytes(int32_t M, int32_t N, int32_t K);
+int moe_i8_matmul(const int8_t* a, const float* a_scales, const int8_t* w, const float* w_scales,
+                  int32_t M, int32_t N, int32_t K, void* out, int32_t out_f32,
+                  void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/*
+ * moe_forward with int8 expert weights (moe_i8_quantize: w13_codes [E, 2I, H] + w13_scales
+ * [E, 2I], w2_codes [E, H, I] + w2_scales [E, H]) and the router of moe_route_groups in place
+ * of step 1.  x is quantized row by row (a scale per token); the up GEMM runs on the codes,
+ * SwiGLU in fp32; act is rounded to bf16 and quantized row by row (a scale per token and
+ * pick); the down GEMM runs on the codes; finalize as in moe_forward.  Other arguments,
+ * stage events (quantizing x counts to step 1, quantizing act to step 4) and outputs are
+ * those of moe_forward.  H % 16 == 0 and I % 16 == 0, I <= 131072; codes and their scales
+ * 16-byte aligned; workspace of moe_i8_workspace_bytes bytes (0 for invalid sizes), 256-byte
+ * aligned.
+ */
+size_t moe_i8_workspace_bytes(int32_t M, int32_t H, int32_t E, int32_t I, int32_t top_k,
+                              int32_t block);
+int moe_forward_i8(const uint16_t* x, const uint16_t* router_w, const float* select_bias,
+                   const int8_t* w13_codes, const float* w13_scales,
+                   const int8_t* w2_codes, const float* w2_scales,
+                   const uint16_t* residual, const uint16_t* norm_w, float eps,
+                   int32_t M, int32_t H, int32_t E, int32_t I, int32_t top_k, int32_t block,
+                   int32_t score, int32_t n_group, int32_t topk_group, int32_t group_top,
+                   int32_t renormalize, float scale,
+                   uint16_t* out, uint16_t* residual_out,
+                   int32_t* topk_ids_out, float* topk_w_out,
+                   int32_t* sorted_ids_out, int32_t* block_expert_out, int32_t* num_padded_out,
+                   void* workspace, size_t workspace_bytes,
+                   const moe_event_t* stage_events, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -24,6 +24,9 @@ __all__ = [
     "moe_prepared_w2_bytes", "moe_prepare_weights", "moe_forward_prepared",
     "moe_mx4_weight_bytes", "moe_mx4_quantize", "moe_mx4_dequantize", "moe_forward_mx4",
     "moe_mx_prepared_bytes", "moe_mx_prepare_weights", "moe_forward_mx_prepared",
+    "moe_route_groups_workspace_bytes", "moe_route_groups", "moe_route_logits",
+    "SCORE_SIGMOID", "SCORE_SOFTMAX", "moe_i8_quantize", "moe_i8_matmul_workspace_bytes",
+    "moe_i8_matmul", "moe_i8_workspace_bytes", "moe_forward_i8",
     "HipEvent",
 ]
 
@@ -87,6 +90,21 @@ _PROTOS = {
     "moe_mx_dequantize": (ctypes.c_int, [_p, _p, ctypes.c_int64, _i32, _p, _p]),
     "moe_forward_mx": (ctypes.c_int, [_p, _p, _p, _p, _p, _p, _p, _p, _p, ctypes.c_float,
                                       _i32, _i32, _i32, _i32, _i32, _i32,
+                                      _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p, _p]),
+    "moe_route_groups_workspace_bytes": (_sz, [_i32, _i32]),
+    "moe_route_groups": (ctypes.c_int, [_p, _p, _p, _i32, _i32, _i32, _i32,
+                                        _i32, _i32, _i32, _i32, _i32, ctypes.c_float,
+                                        _p, _p, _p, _sz, _p]),
+    "moe_route_logits": (ctypes.c_int, [_p, ctypes.c_int64, _p, _i32, _i32, _i32,
+                                        _i32, _i32, _i32, _i32, _i32, ctypes.c_float,
+                                        _p, _p, _p]),
+    "moe_i8_quantize": (ctypes.c_int, [_p, ctypes.c_int64, _i32, _p, _p, _p]),
+    "moe_i8_matmul_workspace_bytes": (_sz, [_i32, _i32, _i32]),
+    "moe_i8_matmul": (ctypes.c_int, [_p, _p, _p, _p, _i32, _i32, _i32, _p, _i32, _p, _sz, _p]),
+    "moe_i8_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32]),
+    "moe_forward_i8": (ctypes.c_int, [_p, _p, _p, _p, _p, _p, _p, _p, _p, ctypes.c_float,
+                                      _i32, _i32, _i32, _i32, _i32, _i32,
+                                      _i32, _i32, _i32, _i32, _i32, ctypes.c_float,
                                       _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p, _p]),
 }
 EXPORTED_SYMBOLS = tuple(_PROTOS)
@@ -679,6 +697,156 @@ def moe_forward_mx(x, router_w, router_bias, w13_codes, w13_scales, w2_codes, w2
         top_k, block, _ptr(out), _ptr(residual_out), _ptr(topk_ids_out), _ptr(topk_w_out),
         _ptr(sorted_ids_out), _ptr(block_expert_out), _ptr(num_padded_out), _ptr(workspace),
         workspace.numel(), ev, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------------------
+# Grouped expert routing, int8 rows and products, the layer on int8 expert weights
+# ---------------------------------------------------------------------------------------
+SCORE_SIGMOID, SCORE_SOFTMAX = 0, 1   # MOE_SCORE_* of include/moe.h
+
+
+def moe_route_groups_workspace_bytes(M: int, E: int) -> int:
+    return int(load_library().moe_route_groups_workspace_bytes(M, E))
+
+
+def _need_bias(select_bias, E: int):
+    if select_bias is not None:
+        _need(select_bias, "select_bias", torch.float32, (E,))
+
+
+def moe_route_groups(x, router_w, select_bias, top_k: int, topk_ids, topk_w, workspace,
+                     score: int = SCORE_SIGMOID, n_group: int = 1, topk_group: int = 1,
+                     group_top: int = 1, renormalize: bool = True, scale: float = 1.0,
+                     stream=None):
+    """Route x [M, H] by router_w [E, H] with sigmoid or softmax scores, a selection bias
+    (fp32 [E] or None) and expert groups; weights from the unbiased scores."""
+    M, H = x.shape
+    E = router_w.shape[0]
+    _need(x, "x", torch.bfloat16)
+    _need(router_w, "router_w", torch.bfloat16, (E, H))
+    _need_bias(select_bias, E)
+    _need(topk_ids, "topk_ids", torch.int32, (M, top_k))
+    _need(topk_w, "topk_w", torch.float32, (M, top_k))
+    _need(workspace, "workspace", torch.uint8)
+    _check("moe_route_groups", load_library().moe_route_groups(
+        _ptr(x), _ptr(router_w), _ptr(select_bias), M, H, E, top_k, score, n_group, topk_group,
+        group_top, int(bool(renormalize)), float(scale), _ptr(topk_ids), _ptr(topk_w),
+        _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+def moe_route_logits(logits, select_bias, top_k: int, topk_ids, topk_w,
+                     score: int = SCORE_SIGMOID, n_group: int = 1, topk_group: int = 1,
+                     group_top: int = 1, renormalize: bool = True, scale: float = 1.0,
+                     stream=None):
+    """moe_route_groups from fp32 logits [M, E], whose rows may lie further apart than E (a
+    slice of the columns of a wider tensor)."""
+    M, E = logits.shape
+    if not isinstance(logits, torch.Tensor) or logits.dtype != torch.float32:
+        raise TypeError("logits must be a float32 tensor")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a device (GPU) tensor")
+    if (E > 1 and logits.stride(1) != 1) or (M > 1 and logits.stride(0) < E):
+        raise ValueError("logits must have contiguous rows that do not overlap")
+    _need_bias(select_bias, E)
+    _need(topk_ids, "topk_ids", torch.int32, (M, top_k))
+    _need(topk_w, "topk_w", torch.float32, (M, top_k))
+    _check("moe_route_logits", load_library().moe_route_logits(
+        _ptr(logits), logits.stride(0) if M > 1 else E, _ptr(select_bias), M, E, top_k, score,
+        n_group, topk_group, group_top, int(bool(renormalize)), float(scale), _ptr(topk_ids),
+        _ptr(topk_w), _stream(stream)))
+
+
+def moe_i8_quantize(v, codes, scales, stream=None):
+    """v [..., K] bf16 -> codes [..., K] int8 and scales [...] fp32, a scale for each row."""
+    _need(v, "v", torch.bfloat16)
+    K = v.shape[-1]
+    _need(codes, "codes", torch.int8, tuple(v.shape))
+    _need(scales, "scales", torch.float32, tuple(v.shape[:-1]))
+    _check("moe_i8_quantize", load_library().moe_i8_quantize(
+        _ptr(v), scales.numel(), K, _ptr(codes), _ptr(scales), _stream(stream)))
+
+
+def moe_i8_matmul_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(load_library().moe_i8_matmul_workspace_bytes(M, N, K))
+
+
+def moe_i8_matmul(a, a_scales, w, w_scales, out, workspace=None, stream=None):
+    """out [M, N] (bf16 or fp32) = (a [M, K] int8, a scale for each row) times (w [N, K] int8,
+    a scale for each row) transposed."""
+    M, K = a.shape
+    N = w.shape[0]
+    _need(a, "a", torch.int8)
+    _need(a_scales, "a_scales", torch.float32, (M,))
+    _need(w, "w", torch.int8, (N, K))
+    _need(w_scales, "w_scales", torch.float32, (N,))
+    f32 = isinstance(out, torch.Tensor) and out.dtype == torch.float32
+    _need(out, "out", torch.float32 if f32 else torch.bfloat16, (M, N))
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8)
+    _check("moe_i8_matmul", load_library().moe_i8_matmul(
+        _ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales), M, N, K, _ptr(out), int(f32),
+        _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream)))
+
+
+def moe_i8_workspace_bytes(M: int, H: int, E: int, I: int, top_k: int, block: int) -> int:
+    return int(load_library().moe_i8_workspace_bytes(M, H, E, I, top_k, block))
+
+
+def moe_forward_i8(x, router_w, select_bias, w13_codes, w13_scales, w2_codes, w2_scales, residual,
+                   norm_w, eps: float, top_k: int, block: int, out, workspace, residual_out=None,
+                   topk_ids_out=None, topk_w_out=None, sorted_ids_out=None, block_expert_out=None,
+                   num_padded_out=None, score: int = SCORE_SIGMOID, n_group: int = 1,
+                   topk_group: int = 1, group_top: int = 1, renormalize: bool = True,
+                   scale: float = 1.0, stage_events: Optional[Sequence["HipEvent"]] = None,
+                   stream=None):
+    """The layer on int8 expert weights (moe_i8_quantize of W13 [E, 2I, H] and W2 [E, H, I])
+    with the router of moe_route_groups."""
+    M, H = x.shape
+    E, two_i, _ = w13_codes.shape
+    I = two_i // 2
+    _need(x, "x", torch.bfloat16)
+    _need(router_w, "router_w", torch.bfloat16, (E, H))
+    _need_bias(select_bias, E)
+    _need(w13_codes, "w13_codes", torch.int8, (E, 2 * I, H))
+    _need(w13_scales, "w13_scales", torch.float32, (E, 2 * I))
+    _need(w2_codes, "w2_codes", torch.int8, (E, H, I))
+    _need(w2_scales, "w2_scales", torch.float32, (E, H))
+    _need(residual, "residual", torch.bfloat16, (M, H))
+    _need(norm_w, "norm_w", torch.bfloat16, (H,))
+    _need(out, "out", torch.bfloat16, (M, H))
+    _need(workspace, "workspace", torch.uint8)
+    if residual_out is not None:
+        _need(residual_out, "residual_out", torch.bfloat16, (M, H))
+    if topk_ids_out is not None:
+        _need(topk_ids_out, "topk_ids_out", torch.int32, (M, top_k))
+    if topk_w_out is not None:
+        _need(topk_w_out, "topk_w_out", torch.float32, (M, top_k))
+    if sorted_ids_out is not None or block_expert_out is not None:
+        cap = moe_align_capacity(M, top_k, E, block)
+        if sorted_ids_out is not None:
+            _need(sorted_ids_out, "sorted_ids_out", torch.int32)
+            if sorted_ids_out.numel() < cap:
+                raise ValueError("sorted_ids_out smaller than the plan capacity")
+        if block_expert_out is not None:
+            _need(block_expert_out, "block_expert_out", torch.int32)
+            if block_expert_out.numel() < cap // block:
+                raise ValueError("block_expert_out smaller than capacity / block")
+    if num_padded_out is not None:
+        _need(num_padded_out, "num_padded_out", torch.int32)
+        if num_padded_out.numel() < 1:
+            raise ValueError("num_padded_out must hold one entry")
+    ev = None
+    if stage_events is not None:
+        if len(stage_events) != 6:
+            raise ValueError("stage_events must hold 6 events")
+        ev = (ctypes.c_void_p * 6)(*[e.handle for e in stage_events])
+    _check("moe_forward_i8", load_library().moe_forward_i8(
+        _ptr(x), _ptr(router_w), _ptr(select_bias), _ptr(w13_codes), _ptr(w13_scales),
+        _ptr(w2_codes), _ptr(w2_scales), _ptr(residual), _ptr(norm_w), float(eps), M, H, E, I,
+        top_k, block, score, n_group, topk_group, group_top, int(bool(renormalize)), float(scale),
+        _ptr(out), _ptr(residual_out), _ptr(topk_ids_out), _ptr(topk_w_out), _ptr(sorted_ids_out),
+        _ptr(block_expert_out), _ptr(num_padded_out), _ptr(workspace), workspace.numel(), ev,
+        _stream(stream)))
 
 
 # ---------------------------------------------------------------------------------------

@@ -14,6 +14,29 @@ constexpr int kRouteScratchPerPair = 32;
 hipError_t launch_route(const uint16_t* x, const uint16_t* wr, const float* bias, int M, int H,
                         int E, int top_k, int32_t* ids, float* w, double* keys, hipStream_t s);
 
+// fp64 keys [M, E] = x . Wr^T by dot products.
+hipError_t launch_router_keys(const uint16_t* x, const uint16_t* wr, int M, int H, int E,
+                              double* keys, hipStream_t s);
+
+// Router with expert groups (route_groups.hip).
+struct GroupRule {
+  int softmax;      // scores: softmax over the experts, else sigmoid
+  int n_group;      // 1 .. 64
+  int per;          // experts per group, E / n_group
+  int topk_group;   // groups that stay
+  int group_top;    // 1 or 2: largest scores that make a group's
+  int renorm;       // weights divided by their sum over the picks
+  float scale;
+};
+// From hidden states (scratch of kRouteScratchPerPair bytes per (token, expert)), or from
+// fp32 logits with a row stride of ld values.
+hipError_t launch_route_groups(const uint16_t* x, const uint16_t* wr, const float* bias, int M,
+                               int H, int E, int top_k, const GroupRule& rule, int32_t* ids,
+                               float* w, void* scratch, hipStream_t s);
+hipError_t launch_route_logits(const float* logits, int64_t ld, const float* bias, int M, int E,
+                               int top_k, const GroupRule& rule, int32_t* ids, float* w,
+                               hipStream_t s);
+
 // Expert-major plan of the flat ids [n]; sentinel = n.  When `tiles` is not null the
 // kernel also lists the row tiles of height tile_rows holding real entries
 // ({first plan row, real rows}) and their count; at most tile_capacity(n, E, tile_rows).
@@ -162,6 +185,32 @@ hipError_t launch_expert_down_frag_mx(const uint16_t* act, const uint8_t* w2c, c
                                      int max_tiles, int tile_rows, bool stream_weights, int H,
                                      int I, int top_k, int block, uint16_t* y, float* y0,
                                      hipStream_t s);
+
+// int8 rows (i8_quant.hip): bf16 [rows, K] (K % 8 == 0) -> codes and the scale of each row;
+// with `plan` (sorted ids) only rows below *num_padded whose id is in [0, n_ids).
+hipError_t launch_i8_rows(const uint16_t* v, int64_t rows, int K, const int32_t* plan,
+                          const int32_t* num_padded, int n_ids, int8_t* codes, float* scales,
+                          hipStream_t s);
+
+// int8 products (i8_gemm.hip); K % 16 == 0.  Dense: out [M, N] (bf16, or fp32 with f32) =
+// a_scale[m] w_scale[n] sum_k a[m,k] w[n,k].
+hipError_t launch_i8_matmul(const int8_t* a, const float* a_scale, const int8_t* w,
+                            const float* w_scale, int M, int N, int K, void* out, bool f32,
+                            hipStream_t s);
+// Grouped over the tiles (height tile_rows, 64 or 128) of a plan: up + SwiGLU -> act bf16
+// [capacity, I] from the tokens' codes [M, H]; down from act's codes [capacity, I] to the
+// split rows y / y0 of moe_forward.
+hipError_t launch_i8_up(const int8_t* x, const float* x_scale, const int8_t* w13,
+                        const float* w13_scale, const int32_t* sorted_ids,
+                        const int32_t* block_expert, const int2* tiles, const int32_t* num_tiles,
+                        int max_tiles, int tile_rows, bool stream_weights, int H, int I, int top_k,
+                        int block, uint16_t* act, hipStream_t s);
+hipError_t launch_i8_down(const int8_t* act, const float* act_scale, const int8_t* w2,
+                          const float* w2_scale, const int32_t* sorted_ids,
+                          const int32_t* block_expert, const int2* tiles,
+                          const int32_t* num_tiles, int max_tiles, int tile_rows,
+                          bool stream_weights, int H, int I, int top_k, int block, uint16_t* y,
+                          float* y0, hipStream_t s);
 
 // Weighted top-k combine + residual add + RMSNorm over fp32 rows of y, or over moe_forward's
 // split rows (first picks in fp32 in y0, the others in bf16 in y).

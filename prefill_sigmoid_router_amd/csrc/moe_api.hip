@@ -674,3 +674,229 @@ int moe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows,
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------------------------------
+// Grouped expert routing, int8 rows and products, the layer on int8 expert weights
+// ---------------------------------------------------------------------------------------
+namespace {
+
+constexpr int kMaxGroups = 64;
+constexpr int kMaxI8K = 131072;   // 127^2 * kMaxI8K < 2^31: int32 sums are exact
+
+bool make_rule(int32_t E, int32_t top_k, int32_t score, int32_t n_group, int32_t topk_group,
+               int32_t group_top, int32_t renormalize, float scale, moe::GroupRule* rule) {
+  if (E < 1 || E > kMaxE || (score != MOE_SCORE_SIGMOID && score != MOE_SCORE_SOFTMAX)) return false;
+  if (n_group < 1 || n_group > kMaxGroups || E % n_group != 0) return false;
+  const int per = E / n_group;
+  if (topk_group < 1 || topk_group > n_group || group_top < 1 || group_top > 2 || group_top > per)
+    return false;
+  if (top_k < 1 || top_k > topk_group * per || !isfinite(scale)) return false;
+  *rule = moe::GroupRule{score == MOE_SCORE_SOFTMAX, n_group, per, topk_group, group_top,
+                         renormalize != 0, scale};
+  return true;
+}
+
+// Workspace layout of moe_forward_i8: the routed-MoE layer's regions, the int8 tokens and
+// the int8 act with their scales.
+struct I8Layout {
+  Layout base;
+  size_t xq, xs, aq, as, total;
+};
+
+I8Layout i8_layout_of(int32_t M, int32_t H, int32_t E, int32_t I, int32_t top_k, int32_t block) {
+  I8Layout L;
+  L.base = layout_of(M, H, E, I, top_k, block);
+  const size_t cap = capacity_of(M, top_k, E, block);
+  size_t off = round_up(L.base.total, kAlign);
+  L.xq = off;  off += round_up((size_t)M * H, kAlign);
+  L.xs = off;  off += round_up((size_t)M * sizeof(float), kAlign);
+  L.aq = off;  off += round_up(cap * (size_t)I, kAlign);
+  L.as = off;  off += round_up(cap * sizeof(float), kAlign);
+  L.total = off;
+  return L;
+}
+
+bool i8_sizes_ok(int32_t M, int32_t H, int32_t E, int32_t I, int32_t top_k) {
+  return sizes_ok(M, H, E, I, top_k) && H % 16 == 0 && I <= kMaxI8K;
+}
+
+// Token-tile height of the grouped int8 GEMMs: 64 rows below 64 expected tokens per expert.
+int i8_tile_rows(int32_t M, int32_t E, int32_t top_k) {
+  return (int64_t)M * top_k / E < 64 ? 64 : 128;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_route_groups_workspace_bytes(int32_t M, int32_t E) {
+  return moe_route_workspace_bytes(M, E);
+}
+
+int moe_route_groups(const uint16_t* x, const uint16_t* router_w, const float* select_bias,
+                     int32_t M, int32_t H, int32_t E, int32_t top_k, int32_t score,
+                     int32_t n_group, int32_t topk_group, int32_t group_top, int32_t renormalize,
+                     float scale, int32_t* topk_ids, float* topk_w, void* workspace,
+                     size_t workspace_bytes, moe_stream_t stream) {
+  moe::GroupRule rule;
+  if (!make_rule(E, top_k, score, n_group, topk_group, group_top, renormalize, scale, &rule))
+    return MOE_ERR_INVALID_ARG;
+  if (M < 0 || H < 8 || H > kMaxH || H % 8 != 0 || (int64_t)M * top_k >= ((int64_t)1 << 31))
+    return MOE_ERR_INVALID_ARG;
+  if (M == 0) return MOE_OK;
+  if (!x || !router_w || !topk_ids || !topk_w || !aligned(x, 16) || !aligned(router_w, 16) ||
+      !aligned(topk_ids, 4) || !aligned(topk_w, 4) || (select_bias && !aligned(select_bias, 4)))
+    return MOE_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 16) ||
+      workspace_bytes < moe_route_groups_workspace_bytes(M, E))
+    return MOE_ERR_WORKSPACE;
+  return hip_status(moe::launch_route_groups(x, router_w, select_bias, M, H, E, top_k, rule,
+                                             topk_ids, topk_w, workspace, (hipStream_t)stream));
+}
+
+int moe_route_logits(const float* logits, int64_t ld, const float* select_bias, int32_t M,
+                     int32_t E, int32_t top_k, int32_t score, int32_t n_group, int32_t topk_group,
+                     int32_t group_top, int32_t renormalize, float scale, int32_t* topk_ids,
+                     float* topk_w, moe_stream_t stream) {
+  moe::GroupRule rule;
+  if (!make_rule(E, top_k, score, n_group, topk_group, group_top, renormalize, scale, &rule))
+    return MOE_ERR_INVALID_ARG;
+  if (M < 0 || ld < E || ld > ((int64_t)1 << 32) || (int64_t)M * top_k >= ((int64_t)1 << 31))
+    return MOE_ERR_INVALID_ARG;
+  if (M == 0) return MOE_OK;
+  if (!logits || !topk_ids || !topk_w || !aligned(logits, 4) || !aligned(topk_ids, 4) ||
+      !aligned(topk_w, 4) || (select_bias && !aligned(select_bias, 4)))
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_route_logits(logits, ld, select_bias, M, E, top_k, rule, topk_ids,
+                                             topk_w, (hipStream_t)stream));
+}
+
+int moe_i8_quantize(const uint16_t* v, int64_t rows, int32_t K, int8_t* codes, float* scales,
+                    moe_stream_t stream) {
+  if (rows < 0 || K < 16 || K % 16 != 0 || K > kMaxI8K || rows > ((int64_t)1 << 40) / K)
+    return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!v || !codes || !scales || !aligned(v, 16) || !aligned(codes, 16) || !aligned(scales, 4))
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_i8_rows(v, rows, K, nullptr, nullptr, 0, codes, scales,
+                                        (hipStream_t)stream));
+}
+
+size_t moe_i8_matmul_workspace_bytes(int32_t M, int32_t N, int32_t K) {
+  (void)M;
+  (void)N;
+  (void)K;
+  return 0;
+}
+
+int moe_i8_matmul(const int8_t* a, const float* a_scales, const int8_t* w, const float* w_scales,
+                  int32_t M, int32_t N, int32_t K, void* out, int32_t out_f32, void* workspace,
+                  size_t workspace_bytes, moe_stream_t stream) {
+  if (M < 0 || N < 1 || K < 16 || K % 16 != 0 || K > kMaxI8K || (out_f32 != 0 && out_f32 != 1))
+    return MOE_ERR_INVALID_ARG;
+  if (M == 0) return MOE_OK;
+  if (!a || !a_scales || !w || !w_scales || !out || !aligned(a, 16) || !aligned(a_scales, 4) ||
+      !aligned(w, 16) || !aligned(w_scales, 16) || !aligned(out, 16))
+    return MOE_ERR_INVALID_ARG;
+  const size_t need = moe_i8_matmul_workspace_bytes(M, N, K);
+  if (need > 0 && (!workspace || !aligned(workspace, kAlign) || workspace_bytes < need))
+    return MOE_ERR_WORKSPACE;
+  return hip_status(moe::launch_i8_matmul(a, a_scales, w, w_scales, M, N, K, out, out_f32 == 1,
+                                          (hipStream_t)stream));
+}
+
+size_t moe_i8_workspace_bytes(int32_t M, int32_t H, int32_t E, int32_t I, int32_t top_k,
+                              int32_t block) {
+  if (!i8_sizes_ok(M, H, E, I, top_k) || !gemm_block_ok(block)) return 0;
+  return i8_layout_of(M, H, E, I, top_k, block).total;
+}
+
+int moe_forward_i8(const uint16_t* x, const uint16_t* router_w, const float* select_bias,
+                   const int8_t* w13_codes, const float* w13_scales, const int8_t* w2_codes,
+                   const float* w2_scales, const uint16_t* residual, const uint16_t* norm_w,
+                   float eps, int32_t M, int32_t H, int32_t E, int32_t I, int32_t top_k,
+                   int32_t block, int32_t score, int32_t n_group, int32_t topk_group,
+                   int32_t group_top, int32_t renormalize, float scale, uint16_t* out,
+                   uint16_t* residual_out, int32_t* topk_ids_out, float* topk_w_out,
+                   int32_t* sorted_ids_out, int32_t* block_expert_out, int32_t* num_padded_out,
+                   void* workspace, size_t workspace_bytes, const moe_event_t* stage_events,
+                   moe_stream_t stream) {
+  moe::GroupRule rule;
+  if (!i8_sizes_ok(M, H, E, I, top_k) || !(eps > 0.0f) || !isfinite(eps) ||
+      !make_rule(E, top_k, score, n_group, topk_group, group_top, renormalize, scale, &rule))
+    return MOE_ERR_INVALID_ARG;
+  if (!gemm_block_ok(block)) return MOE_ERR_UNSUPPORTED;
+  if (M == 0) return MOE_OK;
+  if (!x || !router_w || !w13_codes || !w13_scales || !w2_codes || !w2_scales || !residual ||
+      !norm_w || !out)
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(router_w, 16) || !aligned(w13_codes, 16) ||
+      !aligned(w13_scales, 16) || !aligned(w2_codes, 16) || !aligned(w2_scales, 16) ||
+      !aligned(residual, 16) || !aligned(norm_w, 16) || !aligned(out, 16) ||
+      (residual_out && !aligned(residual_out, 16)) || (select_bias && !aligned(select_bias, 4)) ||
+      (topk_ids_out && !aligned(topk_ids_out, 4)) || (topk_w_out && !aligned(topk_w_out, 4)) ||
+      (sorted_ids_out && !aligned(sorted_ids_out, 4)) ||
+      (block_expert_out && !aligned(block_expert_out, 4)) ||
+      (num_padded_out && !aligned(num_padded_out, 4)))
+    return MOE_ERR_INVALID_ARG;
+  const size_t cap = capacity_of(M, top_k, E, block);
+  if (cap >= ((size_t)1 << 31)) return MOE_ERR_INVALID_ARG;
+  const I8Layout L = i8_layout_of(M, H, E, I, top_k, block);
+  if (!workspace || !aligned(workspace, kAlign) || workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
+
+  char* ws = static_cast<char*>(workspace);
+  const Layout& B = L.base;
+  int32_t* ids = topk_ids_out ? topk_ids_out : reinterpret_cast<int32_t*>(ws + B.ids);
+  float* w = topk_w_out ? topk_w_out : reinterpret_cast<float*>(ws + B.w);
+  int32_t* sorted = sorted_ids_out ? sorted_ids_out : reinterpret_cast<int32_t*>(ws + B.sorted);
+  int32_t* bexp = block_expert_out ? block_expert_out : reinterpret_cast<int32_t*>(ws + B.bexp);
+  int32_t* npad = num_padded_out ? num_padded_out : reinterpret_cast<int32_t*>(ws + B.npad);
+  int2* tiles = reinterpret_cast<int2*>(ws + B.tiles);
+  int32_t* ntiles = reinterpret_cast<int32_t*>(ws + B.ntiles);
+  uint16_t* act = reinterpret_cast<uint16_t*>(ws + B.act);
+  uint16_t* y = reinterpret_cast<uint16_t*>(ws + B.y);
+  float* y0 = reinterpret_cast<float*>(ws + B.y0);
+  int8_t* xq = reinterpret_cast<int8_t*>(ws + L.xq);
+  float* xs = reinterpret_cast<float*>(ws + L.xs);
+  int8_t* aq = reinterpret_cast<int8_t*>(ws + L.aq);
+  float* as = reinterpret_cast<float*>(ws + L.as);
+  hipStream_t s = (hipStream_t)stream;
+
+  const int n = M * top_k;
+  const int trows = i8_tile_rows(M, E, top_k);
+  const bool stream_w = stream_weights(M, E, top_k, trows);
+  const int max_tiles = moe::tile_capacity(n, E, trows);
+  auto mark = [&](int i) -> bool {
+    return !stage_events || hipEventRecord((hipEvent_t)stage_events[i], s) == hipSuccess;
+  };
+  if (!mark(0)) return MOE_ERR_HIP;
+  if (moe::launch_route_groups(x, router_w, select_bias, M, H, E, top_k, rule, ids, w, ws + B.keys,
+                               s) != hipSuccess ||
+      moe::launch_i8_rows(x, M, H, nullptr, nullptr, 0, xq, xs, s) != hipSuccess)
+    return MOE_ERR_HIP;
+  if (!mark(1)) return MOE_ERR_HIP;
+  if (moe::launch_align(ids, n, E, block, sorted, bexp, npad, trows, tiles, ntiles, s, nullptr) !=
+      hipSuccess)
+    return MOE_ERR_HIP;
+  if (!mark(2)) return MOE_ERR_HIP;
+  if (moe::launch_i8_up(xq, xs, w13_codes, w13_scales, sorted, bexp, tiles, ntiles, max_tiles,
+                        trows, stream_w, H, I, top_k, block, act, s) != hipSuccess)
+    return MOE_ERR_HIP;
+  if (!mark(3)) return MOE_ERR_HIP;
+  if (moe::launch_i8_rows(act, (int64_t)cap, I, sorted, npad, n, aq, as, s) != hipSuccess ||
+      moe::launch_i8_down(aq, as, w2_codes, w2_scales, sorted, bexp, tiles, ntiles, max_tiles,
+                          trows, stream_w, H, I, top_k, block, y, y0, s) != hipSuccess)
+    return MOE_ERR_HIP;
+  if (!mark(4)) return MOE_ERR_HIP;
+  const hipError_t fin_err =
+      M < moe::kFinSlicesMaxTokens
+          ? moe::launch_finalize_slices(y, y0, w, residual, norm_w, eps, M, H, top_k, out,
+                                        residual_out, reinterpret_cast<float*>(ws + B.fin), s)
+          : moe::launch_finalize(y, y0, w, residual, norm_w, eps, M, H, top_k, out, residual_out,
+                                 s);
+  if (fin_err != hipSuccess) return MOE_ERR_HIP;
+  if (!mark(5)) return MOE_ERR_HIP;
+  return MOE_OK;
+}
+
+}  // extern "C"

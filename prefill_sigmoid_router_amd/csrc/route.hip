@@ -521,6 +521,12 @@ static hipError_t launch_topk(const double* keys, const float* bias, int M, int 
   return hipGetLastError();
 }
 
+hipError_t launch_router_keys(const uint16_t* x, const uint16_t* wr, int M, int H, int E,
+                              double* keys, hipStream_t s) {
+  return M <= 16 ? launch_keys<2, 4, 4>(x, wr, M, H, E, keys, s)
+                 : launch_keys<4, 4, 2>(x, wr, M, H, E, keys, s);
+}
+
 hipError_t launch_route(const uint16_t* x, const uint16_t* wr, const float* bias, int M, int H,
                         int E, int top_k, int32_t* ids, float* w, double* keys, hipStream_t s) {
   hipError_t err;
@@ -549,8 +555,7 @@ hipError_t launch_route(const uint16_t* x, const uint16_t* wr, const float* bias
 #undef MOE_SELECT
     return hipGetLastError();
   }
-  if (M <= 16) err = launch_keys<2, 4, 4>(x, wr, M, H, E, keys, s);
-  else err = launch_keys<4, 4, 2>(x, wr, M, H, E, keys, s);
+  err = launch_router_keys(x, wr, M, H, E, keys, s);
   if (err != hipSuccess) return err;
   if (per_thread <= 1) return launch_topk<1>(keys, bias, M, E, top_k, ids, w, s);
   if (per_thread <= 2) return launch_topk<2>(keys, bias, M, E, top_k, ids, w, s);
