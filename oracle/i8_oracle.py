@@ -9,8 +9,7 @@ logits are compared); weights are s of the picks, divided by their sum if renorm
 scale.  Experts with a logit of -inf or NaN have no score: weight 0, last in their groups.
 
 int8 rows: a = max |v|, scale a / 127, code = 127 v / a rounded to nearest even (Fractions:
-exact).  A product is the exact integer sum times both scales.  The layer rounds act to
-bf16 before it quantizes its rows.
+exact).  A product is the exact integer sum times both scales.  The layer quantizes x and act row by row.
 """
 from __future__ import annotations
 
@@ -105,7 +104,7 @@ def layer(x_bits, ids, weights, w13, w13_scale, w2, w2_scale, residual_bits, nor
     for e in np.unique(ids):
         t, j = np.nonzero(ids == e)
         h = matmul(xq[t], xs[t], w13[e], w13_scale[e])
-        act = round_bf16(h[:, :I] / (1.0 + np.exp(-h[:, :I])) * h[:, I:])
+        act = h[:, :I] / (1.0 + np.exp(-h[:, :I])) * h[:, I:]
         aq, a_s = quantize(act)
         y[t * k + j] = matmul(aq, a_s, w2[e], w2_scale[e])
     out, z = finalize(y, weights, residual_bits, norm_w_bits, eps)

@@ -10,7 +10,7 @@
 // publishes them.  Only a partial last chunk goes through registers (zero-filled).
 //
 // UP: tokens gathered through the plan, gate and up rows of 32 WN act columns, SwiGLU, act
-// in bf16.  DOWN: act rows of the plan, results to the split y rows.  DENSE: plain rows.
+// as block floats (below).  DOWN: act rows of the plan, results to the split y rows.  DENSE: plain rows.
 #include "device_common.h"
 #include "launchers.h"
 #include "tiled_common.h"
@@ -40,7 +40,8 @@ struct I8Args {
   const int2* tiles;
   const int32_t* num_tiles;
   int n_ntiles, M, K, ncols, top_k, block;   // ncols: act columns (UP), output columns
-  uint16_t* act;
+  int16_t* act;
+  uint8_t* act_exps;
   uint16_t* y;
   float* y0;
   void* out;
@@ -207,25 +208,50 @@ __global__ __launch_bounds__(64 * WN * WM) void i8_gemm_kernel(I8Args p) {
       const int r = 16 * (wm * C::MTW + s) + li;
       if (s >= my_active || r >= nlive) continue;
       if (UP) {
+        // act leaves as block floats: the wave's 32 columns of a row share a power of two
+        // (byte E: value = int16 * 2^(E - 140), the largest below 2^14), because rounding
+        // act to bf16 first moves one int8 code in ten by one (the layer's output 0.6 % off
+        // in relative L2 instead of 0.2 %) and fp32 is twice the bytes.
         const float xs = p.tok_scale[p.sorted_ids[start + r] / p.top_k];
+        float a[2][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int n = col0 + wn * 32 + h * 16 + 4 * lg;
-          if (n < p.ncols) {
-            const float4 g = *reinterpret_cast<const float4*>(ws + n);
-            const float4 u = *reinterpret_cast<const float4*>(ws + p.ncols + n);
-            float a[4];
-            const float gs[4] = {g.x, g.y, g.z, g.w}, us[4] = {u.x, u.y, u.z, u.w};
+          const bool in = n < p.ncols;
+          const float4 g = *reinterpret_cast<const float4*>(ws + (in ? n : 0));
+          const float4 u = *reinterpret_cast<const float4*>(ws + p.ncols + (in ? n : 0));
+          const float gs[4] = {g.x, g.y, g.z, g.w}, us[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              a[q] = silu_f32((float)acc[h][s][q] * (xs * gs[q])) *
-                     ((float)acc[2 + h][s][q] * (xs * us[q]));
-            uint2 v;
-            v.x = pack_bf16x2(a[0], a[1]);
-            v.y = pack_bf16x2(a[2], a[3]);
-            *reinterpret_cast<uint2*>(p.act + (size_t)(start + r) * p.ncols + n) = v;
+          for (int q = 0; q < 4; ++q) {
+            const float v = silu_f32((float)acc[h][s][q] * (xs * gs[q])) *
+                            ((float)acc[2 + h][s][q] * (xs * us[q]));
+            a[h][q] = in ? v : 0.0f;
           }
         }
+        uint32_t m = 0;   // magnitudes' bits order as they do, infinities and NaN last
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) m = max(m, __float_as_uint(a[h][q]) & 0x7fffffffu);
+        // lanes of the same row (lg = 0 .. 3) are all live or all not
+        m = max(m, (uint32_t)__shfl_xor((int)m, 16, kWave));
+        m = max(m, (uint32_t)__shfl_xor((int)m, 32, kWave));
+        const uint32_t E = max(m >> 23, 14u);
+        const float mult = E == 255u ? 0.0f : __uint_as_float((267u - E) << 23);   // 2^(140 - E)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int n = col0 + wn * 32 + h * 16 + 4 * lg;
+          int c[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) c[q] = E == 255u ? 0 : (int)rintf(a[h][q] * mult);
+          if (n < p.ncols)
+            *reinterpret_cast<uint2*>(p.act + (size_t)(start + r) * p.ncols + n) =
+                uint2{(uint32_t)(c[0] & 0xffff) | (uint32_t)c[1] << 16,
+                      (uint32_t)(c[2] & 0xffff) | (uint32_t)c[3] << 16};
+        }
+        const int b = (col0 >> 5) + wn;
+        if (lg == 0 && 32 * b < p.ncols)
+          p.act_exps[(size_t)(start + r) * ((p.ncols + 31) >> 5) + b] = (uint8_t)E;
       } else {
         const float xs = p.tok_scale[start + r];
 #pragma unroll
@@ -322,10 +348,11 @@ hipError_t launch_i8_up(const int8_t* x, const float* x_scale, const int8_t* w13
                         const float* w13_scale, const int32_t* sorted_ids,
                         const int32_t* block_expert, const int2* tiles, const int32_t* num_tiles,
                         int max_tiles, int tile_rows, bool stream_weights, int H, int I, int top_k,
-                        int block, uint16_t* act, hipStream_t s) {
+                        int block, int16_t* act, uint8_t* act_exps, hipStream_t s) {
   I8Args p = grouped(x, x_scale, w13, w13_scale, sorted_ids, block_expert, tiles, num_tiles, H, I,
                      top_k, block);
   p.act = act;
+  p.act_exps = act_exps;
   if (tile_rows == 64)
     return stream_weights ? launch<64, 4, 1, 3, kUp, false, kStreamPolicy>(p, max_tiles, s)
                           : launch<64, 4, 1, 3, kUp, false, 0>(p, max_tiles, s);

@@ -40,20 +40,15 @@ __device__ __forceinline__ uint2 codes8(u32x4 v, float a) {
 
 // Rows of LANES threads each (a wave or the workgroup); KEEP chunks of 8 values per thread
 // stay in registers between the maximum and the codes, later ones are read again.
-// `plan` (sorted ids of a plan of num_padded rows, real entries below n_ids): rows that hold
-// no real entry are skipped.
 template <int LANES, int KEEP>
-__global__ __launch_bounds__(kQThreads) void i8_rows_kernel(
-    const uint16_t* __restrict__ v, int64_t row0, int64_t rows, int K,
-    const int32_t* __restrict__ plan,
-    const int32_t* __restrict__ num_padded, int n_ids, int8_t* __restrict__ codes,
-    float* __restrict__ scales) {
+__global__ __launch_bounds__(kQThreads) void i8_rows_kernel(const uint16_t* __restrict__ v,
+                                                            int64_t row0, int64_t rows, int K,
+                                                            int8_t* __restrict__ codes,
+                                                            float* __restrict__ scales) {
   __shared__ uint32_t part[kQThreads / kWave];
   const int lane = threadIdx.x % LANES;
   const int64_t row = row0 + (int64_t)blockIdx.x * (kQThreads / LANES) + threadIdx.x / LANES;
-  bool on = row < rows;
-  if (on && plan) on = row < *num_padded && (uint32_t)plan[row] < (uint32_t)n_ids;
-  if (LANES == kQThreads && !on) return;   // uniform: the workgroup is the row
+  const bool on = row < rows;   // uniform over a row's threads
   const uint16_t* src = v + row * K;
   const int nchunk = K >> 3;
   u32x4 keep[KEEP];
@@ -92,11 +87,87 @@ __global__ __launch_bounds__(kQThreads) void i8_rows_kernel(
         zero ? uint2{0u, 0u} : codes8(ld16(src + (size_t)ch * 8), top);
 }
 
+// Rows of a plan (one wave each) from the block floats of the up GEMM: 32 values share the
+// byte E, value = int16 * 2^(E - 140); E = 255 marks a block that is not finite.  Rows that
+// hold no real entry are skipped.  The row's maximum and the codes come from the stored
+// values, whose rounding (2^-14 of the block's largest value at most) moves a code by one
+// only where 127 v / a lies within 127 * 2^-14 of a border.
+__global__ __launch_bounds__(kQThreads) void i8_act_kernel(
+    const int16_t* __restrict__ act, const uint8_t* __restrict__ exps, int I, int nblocks,
+    const int32_t* __restrict__ plan, const int32_t* __restrict__ num_padded, int n_ids,
+    int8_t* __restrict__ codes, float* __restrict__ scales) {
+  constexpr int KEEP = 4;       // 8-value chunks per lane kept in registers (I <= 2048)
+  const int lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * (kQThreads / kWave) + (threadIdx.x >> 6);
+  if (row >= *num_padded || (uint32_t)plan[row] >= (uint32_t)n_ids) return;
+  const int16_t* src = act + row * I;
+  const uint8_t* es = exps + row * nblocks;
+  const int nchunk = I >> 3;
+  auto unit = [](uint32_t e) { return __uint_as_float((e - 13u) << 23); };   // 2^(e - 140)
+  auto largest = [](u32x4 v) {
+    int m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = max(m, max(abs((int)(int16_t)v[j]), abs((int)v[j] >> 16)));
+    return (float)m;
+  };
+  u32x4 keep[KEEP];
+  uint32_t e[KEEP];
+  float top = 0.0f;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i) {
+    const int ch = lane + kWave * i;
+    const bool in = ch < nchunk;
+    keep[i] = in ? ld16(src + (size_t)ch * 8) : u32x4{0, 0, 0, 0};
+    e[i] = in ? es[ch >> 2] : 14u;
+  }
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i) {
+    bad |= e[i] == 255u;
+    top = fmaxf(top, largest(keep[i]) * unit(e[i]));
+  }
+  for (int ch = lane + kWave * KEEP; ch < nchunk; ch += kWave) {
+    const uint32_t ex = es[ch >> 2];
+    bad |= ex == 255u;
+    top = fmaxf(top, largest(ld16(src + (size_t)ch * 8)) * unit(ex));
+  }
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, kWave));
+  bad = __any(bad);
+  if (lane == 0) scales[row] = bad ? __uint_as_float(0x7fc00000u) : top / 127.0f;
+  const bool zero = bad || top == 0.0f;
+  auto put = [&](int ch, u32x4 v, uint32_t ex) {
+    const float u = unit(ex);
+    uint32_t c[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      c[2 * j] = code_of((float)(int16_t)v[j] * u, top);
+      c[2 * j + 1] = code_of((float)((int)v[j] >> 16) * u, top);
+    }
+    const uint2 out = {c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24,
+                       c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24};
+    *reinterpret_cast<uint2*>(codes + row * I + (size_t)ch * 8) = zero ? uint2{0u, 0u} : out;
+  };
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i)
+    if (lane + kWave * i < nchunk) put(lane + kWave * i, keep[i], e[i]);
+  for (int ch = lane + kWave * KEEP; ch < nchunk; ch += kWave)
+    put(ch, ld16(src + (size_t)ch * 8), es[ch >> 2]);
+}
+
 }  // namespace
 
-hipError_t launch_i8_rows(const uint16_t* v, int64_t rows, int K, const int32_t* plan,
-                          const int32_t* num_padded, int n_ids, int8_t* codes, float* scales,
-                          hipStream_t s) {
+hipError_t launch_i8_act(const int16_t* act, const uint8_t* exps, int64_t rows, int I,
+                         const int32_t* plan, const int32_t* num_padded, int n_ids, int8_t* codes,
+                         float* scales, hipStream_t s) {
+  const dim3 grid((unsigned)((rows + 3) / 4));
+  hipLaunchKernelGGL(i8_act_kernel, grid, dim3(kQThreads), 0, s, act, exps, I, (I + 31) / 32, plan,
+                     num_padded, n_ids, codes, scales);
+  return hipGetLastError();
+}
+
+hipError_t launch_i8_rows(const uint16_t* v, int64_t rows, int K, int8_t* codes,
+                          float* scales, hipStream_t s) {
   // a wave per row up to 2048 values (4 chunks a lane), a workgroup per longer row
   const bool wave_rows = K <= 2048;
   const int per = wave_rows ? kQThreads / kWave : 1;
@@ -106,10 +177,10 @@ hipError_t launch_i8_rows(const uint16_t* v, int64_t rows, int K, const int32_t*
     const dim3 grid((unsigned)((n + per - 1) / per));
     if (wave_rows)
       hipLaunchKernelGGL((i8_rows_kernel<kWave, 4>), grid, dim3(kQThreads), 0, s, v, r0, rows, K,
-                         plan, num_padded, n_ids, codes, scales);
+                         codes, scales);
     else
       hipLaunchKernelGGL((i8_rows_kernel<kQThreads, 4>), grid, dim3(kQThreads), 0, s, v, r0, rows,
-                         K, plan, num_padded, n_ids, codes, scales);
+                         K, codes, scales);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }

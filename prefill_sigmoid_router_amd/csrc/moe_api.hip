@@ -700,7 +700,7 @@ bool make_rule(int32_t E, int32_t top_k, int32_t score, int32_t n_group, int32_t
 // the int8 act with their scales.
 struct I8Layout {
   Layout base;
-  size_t xq, xs, aq, as, total;
+  size_t xq, xs, ae, aq, as, total;
 };
 
 I8Layout i8_layout_of(int32_t M, int32_t H, int32_t E, int32_t I, int32_t top_k, int32_t block) {
@@ -710,6 +710,7 @@ I8Layout i8_layout_of(int32_t M, int32_t H, int32_t E, int32_t I, int32_t top_k,
   size_t off = round_up(L.base.total, kAlign);
   L.xq = off;  off += round_up((size_t)M * H, kAlign);
   L.xs = off;  off += round_up((size_t)M * sizeof(float), kAlign);
+  L.ae = off;  off += round_up(cap * (size_t)((I + 31) / 32), kAlign);
   L.aq = off;  off += round_up(cap * (size_t)I, kAlign);
   L.as = off;  off += round_up(cap * sizeof(float), kAlign);
   L.total = off;
@@ -778,8 +779,7 @@ int moe_i8_quantize(const uint16_t* v, int64_t rows, int32_t K, int8_t* codes, f
   if (rows == 0) return MOE_OK;
   if (!v || !codes || !scales || !aligned(v, 16) || !aligned(codes, 16) || !aligned(scales, 4))
     return MOE_ERR_INVALID_ARG;
-  return hip_status(moe::launch_i8_rows(v, rows, K, nullptr, nullptr, 0, codes, scales,
-                                        (hipStream_t)stream));
+  return hip_status(moe::launch_i8_rows(v, rows, K, codes, scales, (hipStream_t)stream));
 }
 
 size_t moe_i8_matmul_workspace_bytes(int32_t M, int32_t N, int32_t K) {
@@ -853,7 +853,8 @@ int moe_forward_i8(const uint16_t* x, const uint16_t* router_w, const float* sel
   int32_t* npad = num_padded_out ? num_padded_out : reinterpret_cast<int32_t*>(ws + B.npad);
   int2* tiles = reinterpret_cast<int2*>(ws + B.tiles);
   int32_t* ntiles = reinterpret_cast<int32_t*>(ws + B.ntiles);
-  uint16_t* act = reinterpret_cast<uint16_t*>(ws + B.act);
+  int16_t* act = reinterpret_cast<int16_t*>(ws + B.act);
+  uint8_t* ae = reinterpret_cast<uint8_t*>(ws + L.ae);
   uint16_t* y = reinterpret_cast<uint16_t*>(ws + B.y);
   float* y0 = reinterpret_cast<float*>(ws + B.y0);
   int8_t* xq = reinterpret_cast<int8_t*>(ws + L.xq);
@@ -872,7 +873,7 @@ int moe_forward_i8(const uint16_t* x, const uint16_t* router_w, const float* sel
   if (!mark(0)) return MOE_ERR_HIP;
   if (moe::launch_route_groups(x, router_w, select_bias, M, H, E, top_k, rule, ids, w, ws + B.keys,
                                s) != hipSuccess ||
-      moe::launch_i8_rows(x, M, H, nullptr, nullptr, 0, xq, xs, s) != hipSuccess)
+      moe::launch_i8_rows(x, M, H, xq, xs, s) != hipSuccess)
     return MOE_ERR_HIP;
   if (!mark(1)) return MOE_ERR_HIP;
   if (moe::launch_align(ids, n, E, block, sorted, bexp, npad, trows, tiles, ntiles, s, nullptr) !=
@@ -880,10 +881,10 @@ int moe_forward_i8(const uint16_t* x, const uint16_t* router_w, const float* sel
     return MOE_ERR_HIP;
   if (!mark(2)) return MOE_ERR_HIP;
   if (moe::launch_i8_up(xq, xs, w13_codes, w13_scales, sorted, bexp, tiles, ntiles, max_tiles,
-                        trows, stream_w, H, I, top_k, block, act, s) != hipSuccess)
+                        trows, stream_w, H, I, top_k, block, act, ae, s) != hipSuccess)
     return MOE_ERR_HIP;
   if (!mark(3)) return MOE_ERR_HIP;
-  if (moe::launch_i8_rows(act, (int64_t)cap, I, sorted, npad, n, aq, as, s) != hipSuccess ||
+  if (moe::launch_i8_act(act, ae, (int64_t)cap, I, sorted, npad, n, aq, as, s) != hipSuccess ||
       moe::launch_i8_down(aq, as, w2_codes, w2_scales, sorted, bexp, tiles, ntiles, max_tiles,
                           trows, stream_w, H, I, top_k, block, y, y0, s) != hipSuccess)
     return MOE_ERR_HIP;
