@@ -11,6 +11,8 @@
 //
 // UP: tokens gathered through the plan, gate and up rows of 32 WN act columns, SwiGLU, act
 // as block floats (below).  DOWN: act rows of the plan, results to the split y rows.  DENSE: plain rows.
+#include <type_traits>
+
 #include "device_common.h"
 #include "launchers.h"
 #include "tiled_common.h"
@@ -46,6 +48,54 @@ struct I8Args {
   float* y0;
   void* out;
 };
+
+// act leaves the up product as block floats: the wave's 32 columns of a row share a power
+// of two (byte E: value = int16 * 2^(E - 140), the largest below 2^14), because rounding act
+// to bf16 first moves one int8 code in ten by one (the layer's output 0.6 % off in relative
+// L2 instead of 0.2 %) and fp32 is twice the bytes.  Plan row `row`, columns c0 .. c0 + 31:
+// this lane's g0 / g1 (gate) and u0 / u1 (up) hold columns c0 + 4 lg and c0 + 16 + 4 lg.  The
+// four lanes of a row call it together.
+__device__ __forceinline__ void store_act(const I8Args& p, const float* ws, int row, int c0, int lg,
+                                          i32x4 g0, i32x4 g1, i32x4 u0, i32x4 u1) {
+  const float xs = p.tok_scale[p.sorted_ids[row] / p.top_k];
+  float a[2][4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int n = c0 + h * 16 + 4 * lg;
+    const bool in = n < p.ncols;
+    const float4 g = *reinterpret_cast<const float4*>(ws + (in ? n : 0));
+    const float4 u = *reinterpret_cast<const float4*>(ws + p.ncols + (in ? n : 0));
+    const float gs[4] = {g.x, g.y, g.z, g.w}, us[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float v = silu_f32((float)(h ? g1 : g0)[q] * (xs * gs[q])) *
+                      ((float)(h ? u1 : u0)[q] * (xs * us[q]));
+      a[h][q] = in ? v : 0.0f;
+    }
+  }
+  uint32_t m = 0;   // magnitudes' bits order as they do, infinities and NaN last
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) m = max(m, __float_as_uint(a[h][q]) & 0x7fffffffu);
+  m = max(m, (uint32_t)__shfl_xor((int)m, 16, kWave));
+  m = max(m, (uint32_t)__shfl_xor((int)m, 32, kWave));
+  const uint32_t E = max(m >> 23, 14u);
+  const float mult = E == 255u ? 0.0f : __uint_as_float((267u - E) << 23);   // 2^(140 - E)
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int n = c0 + h * 16 + 4 * lg;
+    int c[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) c[q] = E == 255u ? 0 : (int)rintf(a[h][q] * mult);
+    if (n < p.ncols)
+      *reinterpret_cast<uint2*>(p.act + (size_t)row * p.ncols + n) =
+          uint2{(uint32_t)(c[0] & 0xffff) | (uint32_t)c[1] << 16,
+                (uint32_t)(c[2] & 0xffff) | (uint32_t)c[3] << 16};
+  }
+  if (lg == 0 && c0 < p.ncols)
+    p.act_exps[(size_t)row * ((p.ncols + 31) >> 5) + (c0 >> 5)] = (uint8_t)E;
+}
 
 template <int BM, int WN, int WM>
 struct I8Cfg {
@@ -208,50 +258,7 @@ __global__ __launch_bounds__(64 * WN * WM) void i8_gemm_kernel(I8Args p) {
       const int r = 16 * (wm * C::MTW + s) + li;
       if (s >= my_active || r >= nlive) continue;
       if (UP) {
-        // act leaves as block floats: the wave's 32 columns of a row share a power of two
-        // (byte E: value = int16 * 2^(E - 140), the largest below 2^14), because rounding
-        // act to bf16 first moves one int8 code in ten by one (the layer's output 0.6 % off
-        // in relative L2 instead of 0.2 %) and fp32 is twice the bytes.
-        const float xs = p.tok_scale[p.sorted_ids[start + r] / p.top_k];
-        float a[2][4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int n = col0 + wn * 32 + h * 16 + 4 * lg;
-          const bool in = n < p.ncols;
-          const float4 g = *reinterpret_cast<const float4*>(ws + (in ? n : 0));
-          const float4 u = *reinterpret_cast<const float4*>(ws + p.ncols + (in ? n : 0));
-          const float gs[4] = {g.x, g.y, g.z, g.w}, us[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float v = silu_f32((float)acc[h][s][q] * (xs * gs[q])) *
-                            ((float)acc[2 + h][s][q] * (xs * us[q]));
-            a[h][q] = in ? v : 0.0f;
-          }
-        }
-        uint32_t m = 0;   // magnitudes' bits order as they do, infinities and NaN last
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) m = max(m, __float_as_uint(a[h][q]) & 0x7fffffffu);
-        // lanes of the same row (lg = 0 .. 3) are all live or all not
-        m = max(m, (uint32_t)__shfl_xor((int)m, 16, kWave));
-        m = max(m, (uint32_t)__shfl_xor((int)m, 32, kWave));
-        const uint32_t E = max(m >> 23, 14u);
-        const float mult = E == 255u ? 0.0f : __uint_as_float((267u - E) << 23);   // 2^(140 - E)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int n = col0 + wn * 32 + h * 16 + 4 * lg;
-          int c[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) c[q] = E == 255u ? 0 : (int)rintf(a[h][q] * mult);
-          if (n < p.ncols)
-            *reinterpret_cast<uint2*>(p.act + (size_t)(start + r) * p.ncols + n) =
-                uint2{(uint32_t)(c[0] & 0xffff) | (uint32_t)c[1] << 16,
-                      (uint32_t)(c[2] & 0xffff) | (uint32_t)c[3] << 16};
-        }
-        const int b = (col0 >> 5) + wn;
-        if (lg == 0 && 32 * b < p.ncols)
-          p.act_exps[(size_t)(start + r) * ((p.ncols + 31) >> 5) + b] = (uint8_t)E;
+        store_act(p, ws, start + r, col0 + wn * 32, lg, acc[0][s], acc[1][s], acc[2][s], acc[3][s]);
       } else {
         const float xs = p.tok_scale[start + r];
 #pragma unroll
@@ -304,6 +311,305 @@ hipError_t launch(I8Args& a, long token_tiles, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Grouped products over whole 128-wide chunks (K % 128 == 0).
+//
+// 256 weight rows (UP: 128 act columns) per workgroup of 8 waves, 4 along the weight rows and
+// 2 along the tokens, against up to ROWS token rows of an expert at once, so that its weights
+// are read once.  The workgroup walks its items as one stream of steps (a chunk of an item
+// each, rounded up to a multiple of D; the added steps compute nothing): in step c it
+//   copies the tokens of step c + D into a ring of D + 1 LDS stages,
+//   moves the weights of step c + 1 from registers into one of two LDS stages and
+//   loads those of step c + 1 + D into the registers they leave,
+//   multiplies chunk c.
+// The copies of the next item's first D + 1 steps start in the last steps of the present
+// one.  Weights and tokens return in order, so both run D steps ahead; the registers hold
+// the weights in flight because the LDS cannot hold both rings (two LDS rings: tokens one
+// step ahead, whose L2 latency then set the pace).  Without the stream each item paid about
+// 12 us of latencies: item data, first chunks, scales (M=2048, H=7168, I=2048, E=256, 29
+// items a workgroup in the down product).
+template <int ROWS_, int D_>
+struct Ring {
+  static constexpr int ROWS = ROWS_, D = D_;
+  static constexpr int MTW = ROWS / 32;           // token row tiles per wave
+  static constexpr int TPW = ROWS / 64;           // token pieces (8 rows) per wave per chunk
+  static constexpr int PW = 4;                    // weight pieces per wave per chunk
+  static constexpr int WSTAGE = 256 * 128, TSTAGE = ROWS * 128;
+  static constexpr int LDS = 2 * WSTAGE + (D + 1) * TSTAGE;
+  static_assert(D % 2 == 0, "a step's weight stage is its parity");
+  static_assert(LDS <= 160 * 1024, "the rings must fit the LDS");
+  static_assert(PW + (D - 1) * (TPW + PW) <= 63, "the copies in flight must fit the vmcnt counter");
+};
+
+#ifdef __HIP_DEVICE_COMPILE__   // the host pass knows no buffer descriptors
+// Buffer descriptor of raw bytes from a wave-uniform pointer on, without a bound.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const int8_t* base) {
+  const uint64_t b = (uint64_t)base;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)b);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc((void*)((uint64_t)hi << 32 | lo), 0, -1, 0x00020000);
+}
+
+struct GroupedItem {
+  int start, nlive, e, col0;
+};
+
+template <Mode MODE, typename R, int WPOL>
+__device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char* lds) {
+  constexpr bool UP = MODE == kUp;
+  constexpr int D = R::D, PW = R::PW, TPW = R::TPW, MTW = R::MTW;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int li = lane & 15, lg = lane >> 4;
+  const int wn = wave & 3, wm = wave >> 2;
+  const int K = p.K;
+  unsigned char* const tlds = lds + 2 * R::WSTAGE;
+
+  TiledWalk walk(*p.num_tiles, p.n_ntiles);
+  auto next_item = [&](GroupedItem& it) -> bool {
+    int ntile, ti;
+    if (!walk.next(ntile, ti)) return false;
+    const int l = ntile * walk.ntiles_live + ti;   // expert by expert: its N tiles share its
+    ti = l / p.n_ntiles;                           // token rows through the XCD's L2
+    const int2 tile = p.tiles[ti];
+    it.start = tile.x;
+    it.nlive = tile.y;
+    it.e = p.block_expert[tile.x / p.block];
+    it.col0 = (l % p.n_ntiles) * (UP ? 128 : 256);
+    return true;
+  };
+
+  // A piece is 8 rows x 128 bytes; slot l % 8 of row r (in its 16-row tile) holds the 16-byte
+  // part (l % 8) ^ (r / 2): fragment reads then meet no bank twice, whichever 16 lanes the
+  // LDS serves together.  Weight rows past the last column repeat it; they and token rows
+  // past nlive are never stored.  Buffer loads: scalar base and step offset, a 32-bit offset
+  // a lane.  (Beside copies of the global_load_lds form the compiler waits for everything in
+  // flight.)
+  const int rr = lane >> 3;
+  const int part[2] = {16 * ((lane & 7) ^ (rr >> 1)), 16 * ((lane & 7) ^ (4 + (rr >> 1)))};
+  struct Src {
+    __amdgpu_buffer_rsrc_t w, t;
+    uint32_t woff[PW], toff[TPW];
+  };
+  auto sources = [&](const GroupedItem& it, Src& q) {
+    const int wcol = it.col0 + (UP ? 32 * wn : 32 * wave);   // the wave's first weight row
+    const size_t row0 = (size_t)it.e * (UP ? 2 * p.ncols : p.ncols) + (UP && wm ? p.ncols : 0) +
+                        min(wcol, p.ncols - 1);
+    q.w = buffer_of(p.w + row0 * K);
+    q.t = buffer_of(UP ? p.tok : p.tok + (size_t)it.start * K);
+#pragma unroll
+    for (int i = 0; i < PW; ++i)
+      q.woff[i] = (uint32_t)max(0, min(8 * i + rr, p.ncols - 1 - wcol)) * (uint32_t)K + part[i & 1];
+#pragma unroll
+    for (int i = 0; i < TPW; ++i) {
+      const int pc = wave * TPW + i;
+      const int r = min(pc * 8 + rr, it.nlive - 1);
+      const uint32_t row = UP ? (uint32_t)p.sorted_ids[it.start + r] / (uint32_t)p.top_k : r;
+      q.toff[i] = row * (uint32_t)K + part[pc & 1];
+    }
+  };
+
+  const int nch = K / kKC;
+  const int steps = (nch + D - 1) / D * D;
+  u32x4 wreg[D][PW];
+  int tput = 0;   // token stage that the next copy fills
+  int tget = 0;   // token stage of the present step
+  auto load_w = [&](const Src& q, int c, u32x4 (&dst)[PW]) {
+    const int off = min(c, nch - 1) * kKC;
+#pragma unroll
+    for (int i = 0; i < PW; ++i)
+      dst[i] = __builtin_amdgcn_raw_buffer_load_b128(q.w, q.woff[i], off, WPOL);
+  };
+  auto put_w = [&](int stage, const u32x4 (&v)[PW]) {
+    unsigned char* base = lds + stage * R::WSTAGE + wave * PW * 1024 + lane * 16;
+#pragma unroll
+    for (int i = 0; i < PW; ++i) *reinterpret_cast<u32x4*>(base + i * 1024) = v[i];
+  };
+  auto copy_t = [&](const Src& q, int c) {
+    const int off = min(c, nch - 1) * kKC;
+    unsigned char* base = tlds + tput * R::TSTAGE + wave * TPW * 1024;
+    tput = tput == D ? 0 : tput + 1;
+#pragma unroll
+    for (int i = 0; i < TPW; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(q.t, (lds_void*)(base + i * 1024), 16, q.toff[i],
+                                               off, 0, 0);
+  };
+  const int frag_off = (li >> 3) * 1024 + (li & 7) * 128;
+  auto frag = [&](const unsigned char* tile, int ks) -> u32x4 {
+    return *reinterpret_cast<const u32x4*>(tile + frag_off + (((lg + 4 * ks) ^ (li >> 1)) * 16));
+  };
+  // weight tiles of this wave: UP gate 2 wn, 2 wn + 1 and the up tiles of the same columns
+  auto wtile = [&](int j) { return UP ? (j < 2 ? 2 * wn + j : 8 + 2 * wn + j - 2) : 4 * wn + j; };
+
+  i32x4 acc[4][MTW];
+  auto clear = [&] {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int s = 0; s < MTW; ++s) acc[j][s] = i32x4{0, 0, 0, 0};
+  };
+  // Products of a step, token tile by token tile (both K halves of one: 8 MFMAs) up to the
+  // item's last, each tile's fragments read while the tile before is multiplied; `between`
+  // runs after the first tile, whose products cover its waits.
+  auto compute = [&](const GroupedItem& it, int c, auto between) {
+    const unsigned char* wb = lds + (c & 1) * R::WSTAGE;
+    const unsigned char* tb = tlds + (tget * R::TSTAGE + wm * 2048);
+    tget = tget == D ? 0 : tget + 1;
+    const int active = c < nch ? (((it.nlive + 15) >> 4) - wm + 1) >> 1 : 0;
+    u32x4 wa[2][4], xb[2][2];
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) wa[ks][j] = frag(wb + wtile(j) * 2048, ks);
+      xb[0][ks] = frag(tb, ks);
+    }
+#pragma unroll
+    for (int s = 0; s < MTW; ++s) {
+      if (s + 1 < MTW) {
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) xb[(s + 1) & 1][ks] = frag(tb + (s + 1) * 4096, ks);
+      }
+      __builtin_amdgcn_sched_barrier(0);   // keeps the reads ahead
+      if (s < active) {
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[j][s] = mfma_i8(wa[ks][j], xb[s & 1][ks], acc[j][s]);
+      }
+      if (s == 0) between();
+      else if (s + 1 < MTW && s >= active) break;
+    }
+  };
+  // the next step's tokens have to be in LDS: all but the copies issued after them
+  auto publish = [&] {
+    wait_vmcnt<PW + (D - 1) * (TPW + PW)>();
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  };
+  auto store = [&](const GroupedItem& it) {
+    const float* ws = p.w_scale + (size_t)it.e * (UP ? 2 * p.ncols : p.ncols);
+#pragma unroll
+    for (int s = 0; s < MTW; ++s) {
+      const int r = 16 * (2 * s + wm) + li;
+      if (r >= it.nlive) continue;
+      const int row = it.start + r;
+      if (UP) {
+        store_act(p, ws, row, it.col0 + wn * 32, lg, acc[0][s], acc[1][s], acc[2][s], acc[3][s]);
+      } else {
+        const float xs = p.tok_scale[row];
+        const YRow yr = y_row(p.sorted_ids[row], p.top_k, p.ncols);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int n = it.col0 + wn * 64 + j * 16 + 4 * lg;
+          if (n < p.ncols) {
+            const float4 g = *reinterpret_cast<const float4*>(ws + n);
+            store_y4(p.y, p.y0, yr, n, (float)acc[j][s][0] * (xs * g.x),
+                     (float)acc[j][s][1] * (xs * g.y), (float)acc[j][s][2] * (xs * g.z),
+                     (float)acc[j][s][3] * (xs * g.w));
+          }
+        }
+      }
+    }
+  };
+
+  GroupedItem cur, nxt;
+  if (!next_item(cur)) return;
+  Src qc, qn;
+  sources(cur, qc);
+  {
+    u32x4 first[PW];
+    load_w(qc, 0, first);
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      copy_t(qc, d);
+      load_w(qc, 1 + d, wreg[d]);
+    }
+    put_w(0, first);
+  }
+  clear();
+  publish();   // (the first stage of weights too: older than the tokens)
+  for (;;) {
+    nxt = cur;
+    const bool more = next_item(nxt);   // without another item the last copies are repeats
+    sources(nxt, qn);
+    int c = 0;
+    for (; c + 2 * D < steps; c += D) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        copy_t(qc, c + d + D);
+        compute(cur, c + d, [&] {
+          put_w((d + 1) & 1, wreg[d]);
+          load_w(qc, c + d + 1 + D, wreg[d]);
+        });
+        publish();
+      }
+    }
+    // the last 2 D steps reach into the next item
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      copy_t(qc, c + d + D);
+      compute(cur, c + d, [&] {
+        put_w((d + 1) & 1, wreg[d]);
+        if (d + 1 < D) load_w(qc, c + d + 1 + D, wreg[d]);
+        else load_w(qn, 0, wreg[d]);
+      });
+      publish();
+    }
+    c += D;
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      copy_t(qn, d);
+      compute(cur, c + d, [&] {
+        put_w((d + 1) & 1, wreg[d]);
+        load_w(qn, d + 1, wreg[d]);
+      });
+      publish();
+    }
+    store(cur);
+    if (!more) break;
+    clear();
+    cur = nxt;
+    qc = qn;
+  }
+  wait_vmcnt<0>();   // copies into LDS that are still in flight end with the workgroup
+}
+#endif
+
+constexpr int kGroupedLds = 160 * 1024;
+
+template <Mode MODE, typename R, int WPOL>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void i8_grouped_kernel(
+    I8Args p) {
+  __shared__ __align__(16) unsigned char lds[R::LDS];
+#ifdef __HIP_DEVICE_COMPILE__
+  grouped_products<MODE, R, WPOL>(p, lds);
+#endif
+}
+
+using RingFew = Ring<64, 4>;
+using RingMid = Ring<128, 4>;
+using RingMany = Ring<256, 2>;
+
+template <Mode MODE, typename R, int WPOL>
+hipError_t launch_grouped(I8Args& a, long token_tiles, hipStream_t s) {
+  const int per = MODE == kUp ? 128 : 256;
+  a.n_ntiles = (a.ncols + per - 1) / per;
+  // one workgroup per CU, whatever its LDS would allow: 512 threads of up to 256 registers
+  const long grid = walk_grid(token_tiles * a.n_ntiles, kGroupedLds);
+  hipLaunchKernelGGL((i8_grouped_kernel<MODE, R, WPOL>), dim3((unsigned)grid), dim3(512), 0, s, a);
+  return hipGetLastError();
+}
+
+template <Mode MODE>
+hipError_t launch_expert(I8Args& a, long tiles, int tile_rows, hipStream_t s) {
+  // the stream needs 2 D whole chunks per item
+  if (a.K % kKC == 0 && a.K / kKC > 4) {
+    if (tile_rows == 64) return launch_grouped<MODE, RingFew, kStreamPolicy>(a, tiles, s);
+    if (tile_rows == 128) return launch_grouped<MODE, RingMid, kStreamPolicy>(a, tiles, s);
+    return launch_grouped<MODE, RingMany, kStreamPolicy>(a, tiles, s);
+  }
+  if (tile_rows == 64) return launch<64, 4, 1, 3, MODE, false, kStreamPolicy>(a, tiles, s);
+  if (tile_rows == 128) return launch<128, 8, 1, 2, MODE, false, 0>(a, tiles, s);
+  return launch<256, 4, 2, 2, MODE, false, 0>(a, tiles, s);
+}
+
 }  // namespace
 
 hipError_t launch_i8_matmul(const int8_t* a, const float* a_scale, const int8_t* w,
@@ -347,32 +653,25 @@ static I8Args grouped(const int8_t* tok, const float* tok_scale, const int8_t* w
 hipError_t launch_i8_up(const int8_t* x, const float* x_scale, const int8_t* w13,
                         const float* w13_scale, const int32_t* sorted_ids,
                         const int32_t* block_expert, const int2* tiles, const int32_t* num_tiles,
-                        int max_tiles, int tile_rows, bool stream_weights, int H, int I, int top_k,
+                        int max_tiles, int tile_rows, int H, int I, int top_k,
                         int block, int16_t* act, uint8_t* act_exps, hipStream_t s) {
   I8Args p = grouped(x, x_scale, w13, w13_scale, sorted_ids, block_expert, tiles, num_tiles, H, I,
                      top_k, block);
   p.act = act;
   p.act_exps = act_exps;
-  if (tile_rows == 64)
-    return stream_weights ? launch<64, 4, 1, 3, kUp, false, kStreamPolicy>(p, max_tiles, s)
-                          : launch<64, 4, 1, 3, kUp, false, 0>(p, max_tiles, s);
-  return launch<128, 8, 1, 2, kUp, false, 0>(p, max_tiles, s);
+  return launch_expert<kUp>(p, max_tiles, tile_rows, s);
 }
 
 hipError_t launch_i8_down(const int8_t* act, const float* act_scale, const int8_t* w2,
                           const float* w2_scale, const int32_t* sorted_ids,
                           const int32_t* block_expert, const int2* tiles,
-                          const int32_t* num_tiles, int max_tiles, int tile_rows,
-                          bool stream_weights, int H, int I, int top_k, int block, uint16_t* y,
+                          const int32_t* num_tiles, int max_tiles, int tile_rows, int H, int I, int top_k, int block, uint16_t* y,
                           float* y0, hipStream_t s) {
   I8Args p = grouped(act, act_scale, w2, w2_scale, sorted_ids, block_expert, tiles, num_tiles, I,
                      H, top_k, block);
   p.y = y;
   p.y0 = y0;
-  if (tile_rows == 64)
-    return stream_weights ? launch<64, 8, 1, 2, kDown, false, kStreamPolicy>(p, max_tiles, s)
-                          : launch<64, 8, 1, 2, kDown, false, 0>(p, max_tiles, s);
-  return launch<128, 8, 1, 2, kDown, false, 0>(p, max_tiles, s);
+  return launch_expert<kDown>(p, max_tiles, tile_rows, s);
 }
 
 }  // namespace moe

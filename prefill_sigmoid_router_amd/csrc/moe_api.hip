@@ -723,7 +723,8 @@ bool i8_sizes_ok(int32_t M, int32_t H, int32_t E, int32_t I, int32_t top_k) {
 
 // Token-tile height of the grouped int8 GEMMs: 64 rows below 64 expected tokens per expert.
 int i8_tile_rows(int32_t M, int32_t E, int32_t top_k) {
-  return (int64_t)M * top_k / E < 64 ? 64 : 128;
+  const int64_t per_expert = (int64_t)M * top_k / E;
+  return per_expert < 32 ? 64 : per_expert < 96 ? 128 : 256;
 }
 
 }  // namespace
@@ -865,7 +866,6 @@ int moe_forward_i8(const uint16_t* x, const uint16_t* router_w, const float* sel
 
   const int n = M * top_k;
   const int trows = i8_tile_rows(M, E, top_k);
-  const bool stream_w = stream_weights(M, E, top_k, trows);
   const int max_tiles = moe::tile_capacity(n, E, trows);
   auto mark = [&](int i) -> bool {
     return !stage_events || hipEventRecord((hipEvent_t)stage_events[i], s) == hipSuccess;
@@ -881,12 +881,12 @@ int moe_forward_i8(const uint16_t* x, const uint16_t* router_w, const float* sel
     return MOE_ERR_HIP;
   if (!mark(2)) return MOE_ERR_HIP;
   if (moe::launch_i8_up(xq, xs, w13_codes, w13_scales, sorted, bexp, tiles, ntiles, max_tiles,
-                        trows, stream_w, H, I, top_k, block, act, ae, s) != hipSuccess)
+                        trows, H, I, top_k, block, act, ae, s) != hipSuccess)
     return MOE_ERR_HIP;
   if (!mark(3)) return MOE_ERR_HIP;
   if (moe::launch_i8_act(act, ae, (int64_t)cap, I, sorted, npad, n, aq, as, s) != hipSuccess ||
       moe::launch_i8_down(aq, as, w2_codes, w2_scales, sorted, bexp, tiles, ntiles, max_tiles,
-                          trows, stream_w, H, I, top_k, block, y, y0, s) != hipSuccess)
+                          trows, H, I, top_k, block, y, y0, s) != hipSuccess)
     return MOE_ERR_HIP;
   if (!mark(4)) return MOE_ERR_HIP;
   const hipError_t fin_err =
