@@ -411,6 +411,7 @@ int moe_forward_mx(const uint16_t* x, const uint16_t* router_w, const float* rou
  * a group without a scored expert ranks last.  A token whose experts are all masked gets
  * weights 0.  Every row of topk_ids holds distinct experts.
  * n_group = topk_group = group_top = 1 routes without groups.
+ * M is at most 2^24.
  *   workspace: >= moe_route_groups_workspace_bytes(M, E) bytes (0 for invalid sizes), 16-byte
  *   aligned; moe_route_logits needs none, and only 4-byte alignment of its pointers.
  */
@@ -456,8 +457,8 @@ int moe_i8_matmul(const int8_t* a, const float* a_scales, const int8_t* w, const
  * SwiGLU in fp32; act is quantized row by row (a scale per token and pick; between the two
  * it is held to 2^-14 of the largest of 32 neighbours); the down GEMM runs on the codes; finalize as in moe_forward.  Other arguments,
  * stage events (quantizing x counts to step 1, quantizing act to step 4) and outputs are
- * those of moe_forward.  H % 16 == 0 and I % 16 == 0, I <= 131072; codes and their scales
- * 16-byte aligned; workspace of moe_i8_workspace_bytes bytes (0 for invalid sizes), 256-byte
+ * those of moe_forward.  H % 16 == 0 and I % 16 == 0, I <= 131072, M at most 2^24 and
+ * M * H below 2^32 (MOE_ERR_UNSUPPORTED otherwise); codes and their scales 16-byte aligned; workspace of moe_i8_workspace_bytes bytes (0 for invalid sizes), 256-byte
  * aligned.
  */
 size_t moe_i8_workspace_bytes(int32_t M, int32_t H, int32_t E, int32_t I, int32_t top_k,

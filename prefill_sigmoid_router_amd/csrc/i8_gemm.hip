@@ -4,8 +4,8 @@
 //
 // Workgroup tile: BM token rows x 64 WN weight rows, K in chunks of 128 values (one
 // 128-byte line per row).  Both operands are copied global -> LDS in 1 KiB pieces of 8 rows
-// x one line; inside a row the 16-byte pieces are XOR-swizzled so that an MFMA fragment (16
-// rows x 64 K values, 16 per lane) is one conflict-free ds_read_b128.  A ring of S stages
+// x one line, whose 16-byte parts are XOR-swizzled so that an MFMA fragment (16 rows x 64 K
+// values, 16 per lane) is one conflict-free ds_read_b128.  A ring of S stages
 // keeps S - 1 chunks in flight; each wave waits for its own copies and a bare barrier
 // publishes them.  Only a partial last chunk goes through registers (zero-filled).
 //
@@ -41,6 +41,7 @@ struct I8Args {
   const int32_t* block_expert;
   const int2* tiles;
   const int32_t* num_tiles;
+  int act_rows;   // rows of a 128-column block of act
   int n_ntiles, M, K, ncols, top_k, block;   // ncols: act columns (UP), output columns
   int16_t* act;
   uint8_t* act_exps;
@@ -49,52 +50,93 @@ struct I8Args {
   void* out;
 };
 
-// act leaves the up product as block floats: the wave's 32 columns of a row share a power
-// of two (byte E: value = int16 * 2^(E - 140), the largest below 2^14), because rounding act
-// to bf16 first moves one int8 code in ten by one (the layer's output 0.6 % off in relative
-// L2 instead of 0.2 %) and fp32 is twice the bytes.  Plan row `row`, columns c0 .. c0 + 31:
-// this lane's g0 / g1 (gate) and u0 / u1 (up) hold columns c0 + 4 lg and c0 + 16 + 4 lg.  The
-// four lanes of a row call it together.
-__device__ __forceinline__ void store_act(const I8Args& p, const float* ws, int row, int c0, int lg,
-                                          i32x4 g0, i32x4 g1, i32x4 u0, i32x4 u1) {
-  const float xs = p.tok_scale[p.sorted_ids[row] / p.top_k];
-  float a[2][4];
+// LDS rows are one 128-byte line of a chunk each; 16-byte slot q of row r holds the part
+// q ^ f(r) of the line, with f chosen so that the 16 rows of a fragment read (which also
+// differ in r % 2) meet no bank twice.  Token fragments are 16 consecutive rows.  Weight
+// fragment j of a wave's 32 (UP: gate, and as many up) or 64 rows holds rows
+// SPAN (i / 4) + 4 j + i % 4, i = 0 .. 15, SPAN = 8 or 16: a lane's results of all the
+// fragments then are SPAN consecutive columns, stored 16 bytes at a time.
+__device__ __forceinline__ int token_swizzle(int r) { return (r >> 1) & 7; }
+template <int SPAN>
+__device__ __forceinline__ int weight_swizzle(int r) {
+  return ((r >> 1) & 1) | ((r / SPAN) & 3) << 1;
+}
+
+__device__ __forceinline__ void load16(const float* src, float (&w)[16]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float4 g = reinterpret_cast<const float4*>(src)[j];
+    w[4 * j] = g.x;
+    w[4 * j + 1] = g.y;
+    w[4 * j + 2] = g.z;
+    w[4 * j + 3] = g.w;
+  }
+}
+__device__ __forceinline__ void store16(float* dst, const float (&v)[16]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    reinterpret_cast<float4*>(dst)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+}
+__device__ __forceinline__ void store16(uint16_t* dst, const float (&v)[16]) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    u32x4 u;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) u[q] = pack_bf16x2(v[8 * j + 2 * q], v[8 * j + 2 * q + 1]);
+    st16(dst + 8 * j, u);
+  }
+}
+
+__device__ __forceinline__ float silu_fast(float z) {   // both steps within 2 units in the last place
+  return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+}
+
+// act of this lane's 8 columns from c on: silu(gate) * up of the scaled sums, 0 past the last
+// column.  ws: the gate rows' scales, the up rows' p.ncols behind them.
+__device__ __forceinline__ void scaled_act(i32x4 g0, i32x4 g1, i32x4 u0, i32x4 u1, float xs,
+                                           const float* ws, int c, int ncols, float (&a)[8]) {
+  const bool in = c < ncols;
+  const float4* g4 = reinterpret_cast<const float4*>(ws + (in ? c : 0));
+  const float4* u4 = reinterpret_cast<const float4*>(ws + ncols + (in ? c : 0));
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int n = c0 + h * 16 + 4 * lg;
-    const bool in = n < p.ncols;
-    const float4 g = *reinterpret_cast<const float4*>(ws + (in ? n : 0));
-    const float4 u = *reinterpret_cast<const float4*>(ws + p.ncols + (in ? n : 0));
-    const float gs[4] = {g.x, g.y, g.z, g.w}, us[4] = {u.x, u.y, u.z, u.w};
+    const float4 gw = g4[h], uw = u4[h];
+    const float gs[4] = {gw.x, gw.y, gw.z, gw.w}, us[4] = {uw.x, uw.y, uw.z, uw.w};
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const float v = silu_f32((float)(h ? g1 : g0)[q] * (xs * gs[q])) *
+      const float v = silu_fast((float)(h ? g1 : g0)[q] * (xs * gs[q])) *
                       ((float)(h ? u1 : u0)[q] * (xs * us[q]));
-      a[h][q] = in ? v : 0.0f;
+      a[4 * h + q] = in ? v : 0.0f;
     }
   }
+}
+
+// act leaves the up product as block floats: 32 columns of a row share a power of two (byte
+// E: value = int16 * 2^(E - 140), the largest below 2^14), because rounding act to bf16 first
+// moves one int8 code in ten by one (the layer's output 0.6 % off in relative L2 instead of
+// 0.2 %) and fp32 is twice the bytes.  Four lanes (lane / 16) hold the 32 columns, 8 each;
+// they call it together.  a: act of this lane's columns, 0 past the last; c: its first column.
+// Layout [ceil(I / 128)][rows][128]: what a workgroup writes is one piece of memory.
+__device__ __forceinline__ void store_act(const I8Args& p, int row, int c, const float (&a)[8]) {
   uint32_t m = 0;   // magnitudes' bits order as they do, infinities and NaN last
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) m = max(m, __float_as_uint(a[h][q]) & 0x7fffffffu);
+  for (int q = 0; q < 8; ++q) m = max(m, __float_as_uint(a[q]) & 0x7fffffffu);
   m = max(m, (uint32_t)__shfl_xor((int)m, 16, kWave));
   m = max(m, (uint32_t)__shfl_xor((int)m, 32, kWave));
   const uint32_t E = max(m >> 23, 14u);
   const float mult = E == 255u ? 0.0f : __uint_as_float((267u - E) << 23);   // 2^(140 - E)
+  uint32_t v[4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int n = c0 + h * 16 + 4 * lg;
-    int c[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) c[q] = E == 255u ? 0 : (int)rintf(a[h][q] * mult);
-    if (n < p.ncols)
-      *reinterpret_cast<uint2*>(p.act + (size_t)row * p.ncols + n) =
-          uint2{(uint32_t)(c[0] & 0xffff) | (uint32_t)c[1] << 16,
-                (uint32_t)(c[2] & 0xffff) | (uint32_t)c[3] << 16};
+  for (int q = 0; q < 4; ++q) {
+    const int lo = E == 255u ? 0 : (int)rintf(a[2 * q] * mult);
+    const int hi = E == 255u ? 0 : (int)rintf(a[2 * q + 1] * mult);
+    v[q] = (uint32_t)(lo & 0xffff) | (uint32_t)hi << 16;
   }
-  if (lg == 0 && c0 < p.ncols)
-    p.act_exps[(size_t)row * ((p.ncols + 31) >> 5) + (c0 >> 5)] = (uint8_t)E;
+  const size_t block_row = (size_t)(c >> 7) * p.act_rows + row;
+  if (c < p.ncols)   // nontemporal: 60 us less of 1,660 beside the weights' stream
+    __builtin_nontemporal_store(u32x4{v[0], v[1], v[2], v[3]},
+                                reinterpret_cast<u32x4*>(p.act + block_row * 128 + (c & 127)));
+  if ((c & 31) == 0 && c < p.ncols) p.act_exps[block_row * 4 + ((c >> 5) & 3)] = (uint8_t)E;
 }
 
 template <int BM, int WN, int WM>
@@ -126,6 +168,7 @@ __global__ __launch_bounds__(64 * WN * WM) void i8_gemm_kernel(I8Args p) {
   static_assert((S - 2) * C::PPW <= 63, "the copies in flight must fit the vmcnt counter");
   static_assert(S * C::PIECES * 1024 <= 160 * 1024, "the ring must fit the LDS");
   __shared__ __align__(16) unsigned char lds[S * C::PIECES * 1024];
+  constexpr int SPAN = UP ? 8 : 16;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int li = lane & 15, lg = lane >> 4;
   const int wn = wave % WN, wm = wave / WN;
@@ -148,43 +191,32 @@ __global__ __launch_bounds__(64 * WN * WM) void i8_gemm_kernel(I8Args p) {
     const int col0 = UP ? ntile * 32 * WN : ntile * 64 * WN;
     const size_t wrow0 = MODE == kDense ? 0 : (size_t)e * (UP ? 2 * p.ncols : p.ncols);
 
-    // piece f of a chunk: rows 8h .. 8h + 7 (h = f % 2) of row tile f / 2 (weight tiles
-    // first); lane l copies 16 bytes of row 8h + l / 8 into slot l % 8, which holds K piece
-    // (l % 8) ^ (row % 8) ^ h.  Rows without data point at a valid row; their results are
-    // never stored.
+    // piece f of a chunk: LDS rows 8f .. 8f + 7 (weight rows first); lane l copies slot l % 8
+    // of row 8f + l / 8.  Rows without data point at a valid row; their results are never
+    // stored.
     const int8_t* src[C::PPW];
     bool on[C::PPW];
     int q16[C::PPW];
 #pragma unroll
     for (int i = 0; i < C::PPW; ++i) {
       const int f = wave * C::PPW + i;
-      const int rt = f >> 1, h = f & 1;
-      const int rr = 8 * h + (lane >> 3);
-      q16[i] = 16 * ((lane & 7) ^ (lane >> 3) ^ h);
-      if (rt < C::WT) {
-        int col, row;
-        if (UP) {
-          const bool up = rt >= C::WT / 2;
-          col = col0 + (up ? rt - C::WT / 2 : rt) * 16 + rr;
-          row = up ? p.ncols + col : col;
-        } else {
-          row = col = col0 + rt * 16 + rr;
-        }
+      const int lr = 8 * f + (lane >> 3);
+      if (lr < 64 * WN) {
+        q16[i] = 16 * ((lane & 7) ^ weight_swizzle<SPAN>(lr));
+        const bool up = UP && lr >= 32 * WN;
+        const int col = col0 + (up ? lr - 32 * WN : lr);
+        const int row = up ? p.ncols + col : col;
         on[i] = col < p.ncols;
         src[i] = p.w + (wrow0 + (on[i] ? row : 0)) * K + q16[i];
       } else {
-        const int r = 16 * (rt - C::WT) + rr;
+        const int r = lr - 64 * WN;
+        q16[i] = 16 * ((lane & 7) ^ token_swizzle(r));
         on[i] = r < nlive;
         int row = start + (on[i] ? r : 0);
         if (UP) row = p.sorted_ids[row] / p.top_k;
         src[i] = p.tok + (size_t)row * K + q16[i];
       }
     }
-    int wtile[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      wtile[j] = UP ? ((j < 2) ? 2 * wn + j : C::WT / 2 + 2 * wn + j - 2) : 4 * wn + j;
-
     const int nch = (K + kKC - 1) / kKC;
     const int ndma = K / kKC;   // whole chunks
     auto issue = [&](int c) {
@@ -210,11 +242,15 @@ __global__ __launch_bounds__(64 * WN * WM) void i8_gemm_kernel(I8Args p) {
         }
       }
     };
-    const int frag_off = (li >> 3) * 1024 + (li & 7) * 128;
-    auto frag = [&](int c, int t, int ks) -> u32x4 {
-      const int q = (lg + 4 * ks) ^ (li & 7) ^ (li >> 3);
-      return *reinterpret_cast<const u32x4*>(lds + (size_t)(c % S) * C::PIECES * 1024 + t * 2048 +
-                                             frag_off + q * 16);
+    const int wrow = (UP ? 32 : 64) * wn + SPAN * (li >> 2) + (li & 3);
+    const int wslot = weight_swizzle<SPAN>(wrow), tslot = token_swizzle(li);
+    auto frag = [&](int c, int row, int slot) -> u32x4 {
+      return *reinterpret_cast<const u32x4*>(lds + (size_t)(c % S) * C::PIECES * 1024 + row * 128 +
+                                             slot * 16);
+    };
+    auto wfrag = [&](int c, int j, int ks) {
+      const int row = UP ? wrow + 4 * (j & 1) + (j >> 1) * 32 * WN : wrow + 4 * j;
+      return frag(c, row, (lg + 4 * ks) ^ wslot);
     };
 
     i32x4 acc[4][C::MTW];
@@ -238,11 +274,11 @@ __global__ __launch_bounds__(64 * WN * WM) void i8_gemm_kernel(I8Args p) {
         for (int ks = 0; ks < 2; ++ks) {
           u32x4 wa[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) wa[j] = frag(c, wtile[j], ks);
+          for (int j = 0; j < 4; ++j) wa[j] = wfrag(c, j, ks);
 #pragma unroll
           for (int s = 0; s < C::MTW; ++s) {
             if (s < my_active) {
-              const u32x4 xb = frag(c, C::WT + wm * C::MTW + s, ks);
+              const u32x4 xb = frag(c, 64 * WN + 16 * (wm * C::MTW + s) + li, (lg + 4 * ks) ^ tslot);
 #pragma unroll
               for (int j = 0; j < 4; ++j) acc[j][s] = mfma_i8(wa[j], xb, acc[j][s]);
             }
@@ -251,48 +287,46 @@ __global__ __launch_bounds__(64 * WN * WM) void i8_gemm_kernel(I8Args p) {
       }
     }
 
-    // lane (li, lg) holds weight rows 4 lg .. 4 lg + 3 of each weight tile, token row li
+    // lane (li, lg) holds token row li of each token tile and SPAN columns from n0 on
     const float* ws = p.w_scale + wrow0;
+    const int n0 = col0 + (UP ? 32 : 64) * wn + SPAN * lg;
 #pragma unroll
     for (int s = 0; s < C::MTW; ++s) {
       const int r = 16 * (wm * C::MTW + s) + li;
       if (s >= my_active || r >= nlive) continue;
+      const int row = start + r;
       if (UP) {
-        store_act(p, ws, start + r, col0 + wn * 32, lg, acc[0][s], acc[1][s], acc[2][s], acc[3][s]);
-      } else {
-        const float xs = p.tok_scale[start + r];
+        float a[8];
+        const float xs = p.tok_scale[p.sorted_ids[row] / p.top_k];
+        scaled_act(acc[0][s], acc[1][s], acc[2][s], acc[3][s], xs, ws, n0, p.ncols, a);
+        store_act(p, row, n0, a);
+      } else if (n0 < p.ncols) {
+        const float xs = p.tok_scale[row];
+        const i32x4 v4[4] = {acc[0][s], acc[1][s], acc[2][s], acc[3][s]};
+        float v[16];
+        if (MODE == kDown || (n0 + 15 < p.ncols && p.ncols % 8 == 0)) {
+          float w[16];
+          load16(ws + n0, w);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int n = col0 + wn * 64 + j * 16 + 4 * lg;
+          for (int q = 0; q < 16; ++q) v[q] = (float)v4[q >> 2][q & 3] * (xs * w[q]);
           if (MODE == kDown) {
-            if (n < p.ncols) {
-              const float4 g = *reinterpret_cast<const float4*>(ws + n);
-              store_y4(p.y, p.y0, y_row(p.sorted_ids[start + r], p.top_k, p.ncols), n,
-                       (float)acc[j][s][0] * (xs * g.x), (float)acc[j][s][1] * (xs * g.y),
-                       (float)acc[j][s][2] * (xs * g.z), (float)acc[j][s][3] * (xs * g.w));
-            }
+            const YRow yr = y_row(p.sorted_ids[row], p.top_k, p.ncols);
+            if (yr.first) store16(p.y0 + yr.off + n0, v);
+            else store16(p.y + yr.off + n0, v);
+          } else if (F32) {
+            store16(static_cast<float*>(p.out) + (size_t)row * p.ncols + n0, v);
           } else {
-            const size_t o = (size_t)(start + r) * p.ncols + n;
-            if (n + 3 < p.ncols && p.ncols % 4 == 0) {
-              const float4 g = *reinterpret_cast<const float4*>(ws + n);
-              const float4 v =
-                  make_float4((float)acc[j][s][0] * (xs * g.x), (float)acc[j][s][1] * (xs * g.y),
-                              (float)acc[j][s][2] * (xs * g.z), (float)acc[j][s][3] * (xs * g.w));
-              if (F32)
-                *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o) = v;
-              else
-                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + o) =
-                    uint2{pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
-            } else {
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                if (n + q < p.ncols) {
-                  const float v = (float)acc[j][s][q] * (xs * ws[n + q]);
-                  if (F32) static_cast<float*>(p.out)[o + q] = v;
-                  else static_cast<uint16_t*>(p.out)[o + q] = (uint16_t)f32_to_bf16_rne(v);
-                }
-            }
+            store16(static_cast<uint16_t*>(p.out) + (size_t)row * p.ncols + n0, v);
           }
+        } else {
+          const size_t o = (size_t)row * p.ncols + n0;
+#pragma unroll
+          for (int q = 0; q < 16; ++q)
+            if (n0 + q < p.ncols) {
+              const float f = (float)v4[q >> 2][q & 3] * (xs * ws[n0 + q]);
+              if (F32) static_cast<float*>(p.out)[o + q] = f;
+              else static_cast<uint16_t*>(p.out)[o + q] = (uint16_t)f32_to_bf16_rne(f);
+            }
         }
       }
     }
@@ -377,14 +411,13 @@ __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char*
     return true;
   };
 
-  // A piece is 8 rows x 128 bytes; slot l % 8 of row r (in its 16-row tile) holds the 16-byte
-  // part (l % 8) ^ (r / 2): fragment reads then meet no bank twice, whichever 16 lanes the
-  // LDS serves together.  Weight rows past the last column repeat it; they and token rows
-  // past nlive are never stored.  Buffer loads: scalar base and step offset, a 32-bit offset
+  // A piece is 8 LDS rows (UP: 128 gate rows, then 128 up rows); lane l copies slot l % 8 of
+  // row l / 8.  Weight rows past the last column repeat it; they and token rows past nlive
+  // are never stored.  Buffer loads: scalar base and step offset, a 32-bit offset
   // a lane.  (Beside copies of the global_load_lds form the compiler waits for everything in
   // flight.)
   const int rr = lane >> 3;
-  const int part[2] = {16 * ((lane & 7) ^ (rr >> 1)), 16 * ((lane & 7) ^ (4 + (rr >> 1)))};
+  constexpr int SPAN = UP ? 8 : 16;
   struct Src {
     __amdgpu_buffer_rsrc_t w, t;
     uint32_t woff[PW], toff[TPW];
@@ -397,13 +430,14 @@ __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char*
     q.t = buffer_of(UP ? p.tok : p.tok + (size_t)it.start * K);
 #pragma unroll
     for (int i = 0; i < PW; ++i)
-      q.woff[i] = (uint32_t)max(0, min(8 * i + rr, p.ncols - 1 - wcol)) * (uint32_t)K + part[i & 1];
+      q.woff[i] = (uint32_t)max(0, min(8 * i + rr, p.ncols - 1 - wcol)) * (uint32_t)K +
+                  16 * ((lane & 7) ^ weight_swizzle<SPAN>(32 * wave + 8 * i + rr));
 #pragma unroll
     for (int i = 0; i < TPW; ++i) {
-      const int pc = wave * TPW + i;
-      const int r = min(pc * 8 + rr, it.nlive - 1);
+      const int lr = (wave * TPW + i) * 8 + rr;
+      const int r = min(lr, it.nlive - 1);
       const uint32_t row = UP ? (uint32_t)p.sorted_ids[it.start + r] / (uint32_t)p.top_k : r;
-      q.toff[i] = row * (uint32_t)K + part[pc & 1];
+      q.toff[i] = row * (uint32_t)K + 16 * ((lane & 7) ^ token_swizzle(lr));
     }
   };
 
@@ -432,12 +466,17 @@ __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char*
       __builtin_amdgcn_raw_ptr_buffer_load_lds(q.t, (lds_void*)(base + i * 1024), 16, q.toff[i],
                                                off, 0, 0);
   };
-  const int frag_off = (li >> 3) * 1024 + (li & 7) * 128;
-  auto frag = [&](const unsigned char* tile, int ks) -> u32x4 {
-    return *reinterpret_cast<const u32x4*>(tile + frag_off + (((lg + 4 * ks) ^ (li >> 1)) * 16));
+  const int wrow = (UP ? 32 : 64) * wn + SPAN * (li >> 2) + (li & 3);
+  const int woff16 = wrow * 128 + 16 * (lg ^ weight_swizzle<SPAN>(wrow));
+  const int toff16 = (16 * wm + li) * 128 + 16 * (lg ^ token_swizzle(li));
+  auto at = [&](const unsigned char* q) { return *reinterpret_cast<const u32x4*>(q); };
+  // fragments of K half ks: slot lg + 4 ks, that is byte 64 ks flipped
+  auto wfrag = [&](const unsigned char* stage, int j, int ks) {
+    return at(stage + (woff16 ^ (64 * ks)) + (UP ? 512 * (j & 1) + 16384 * (j >> 1) : 512 * j));
   };
-  // weight tiles of this wave: UP gate 2 wn, 2 wn + 1 and the up tiles of the same columns
-  auto wtile = [&](int j) { return UP ? (j < 2 ? 2 * wn + j : 8 + 2 * wn + j - 2) : 4 * wn + j; };
+  auto tfrag = [&](const unsigned char* stage, int s, int ks) {
+    return at(stage + (toff16 ^ (64 * ks)) + 4096 * s);
+  };
 
   i32x4 acc[4][MTW];
   auto clear = [&] {
@@ -451,21 +490,21 @@ __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char*
   // runs after the first tile, whose products cover its waits.
   auto compute = [&](const GroupedItem& it, int c, auto between) {
     const unsigned char* wb = lds + (c & 1) * R::WSTAGE;
-    const unsigned char* tb = tlds + (tget * R::TSTAGE + wm * 2048);
+    const unsigned char* tb = tlds + tget * R::TSTAGE;
     tget = tget == D ? 0 : tget + 1;
     const int active = c < nch ? (((it.nlive + 15) >> 4) - wm + 1) >> 1 : 0;
     u32x4 wa[2][4], xb[2][2];
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) wa[ks][j] = frag(wb + wtile(j) * 2048, ks);
-      xb[0][ks] = frag(tb, ks);
+      for (int j = 0; j < 4; ++j) wa[ks][j] = wfrag(wb, j, ks);
+      xb[0][ks] = tfrag(tb, 0, ks);
     }
 #pragma unroll
     for (int s = 0; s < MTW; ++s) {
       if (s + 1 < MTW) {
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) xb[(s + 1) & 1][ks] = frag(tb + (s + 1) * 4096, ks);
+        for (int ks = 0; ks < 2; ++ks) xb[(s + 1) & 1][ks] = tfrag(tb, s + 1, ks);
       }
       __builtin_amdgcn_sched_barrier(0);   // keeps the reads ahead
       if (s < active) {
@@ -485,26 +524,38 @@ __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char*
   };
   auto store = [&](const GroupedItem& it) {
     const float* ws = p.w_scale + (size_t)it.e * (UP ? 2 * p.ncols : p.ncols);
+    const int n0 = it.col0 + (UP ? 32 : 64) * wn + SPAN * lg;
+    int id[MTW];   // every load of a kind before its first use: one latency, not one per row
+    float xs[MTW];
 #pragma unroll
     for (int s = 0; s < MTW; ++s) {
-      const int r = 16 * (2 * s + wm) + li;
-      if (r >= it.nlive) continue;
-      const int row = it.start + r;
-      if (UP) {
-        store_act(p, ws, row, it.col0 + wn * 32, lg, acc[0][s], acc[1][s], acc[2][s], acc[3][s]);
-      } else {
-        const float xs = p.tok_scale[row];
-        const YRow yr = y_row(p.sorted_ids[row], p.top_k, p.ncols);
+      const int row = it.start + min(16 * (2 * s + wm) + li, it.nlive - 1);
+      id[s] = p.sorted_ids[row];
+      if (!UP) xs[s] = p.tok_scale[row];
+    }
+    if (UP) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int n = it.col0 + wn * 64 + j * 16 + 4 * lg;
-          if (n < p.ncols) {
-            const float4 g = *reinterpret_cast<const float4*>(ws + n);
-            store_y4(p.y, p.y0, yr, n, (float)acc[j][s][0] * (xs * g.x),
-                     (float)acc[j][s][1] * (xs * g.y), (float)acc[j][s][2] * (xs * g.z),
-                     (float)acc[j][s][3] * (xs * g.w));
-          }
-        }
+      for (int s = 0; s < MTW; ++s) xs[s] = p.tok_scale[id[s] / p.top_k];
+#pragma unroll
+      for (int s = 0; s < MTW; ++s) {
+        const int r = 16 * (2 * s + wm) + li;
+        if (r >= it.nlive) continue;
+        float a[8];
+        scaled_act(acc[0][s], acc[1][s], acc[2][s], acc[3][s], xs[s], ws, n0, p.ncols, a);
+        store_act(p, it.start + r, n0, a);
+      }
+    } else if (n0 < p.ncols) {
+      float w[16];
+      load16(ws + n0, w);
+#pragma unroll
+      for (int s = 0; s < MTW; ++s) {
+        if (16 * (2 * s + wm) + li >= it.nlive) continue;
+        float v[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) v[q] = (float)acc[q >> 2][s][q & 3] * (xs[s] * w[q]);
+        const YRow yr = y_row(id[s], p.top_k, p.ncols);
+        if (yr.first) store16(p.y0 + yr.off + n0, v);
+        else store16(p.y + yr.off + n0, v);
       }
     }
   };
@@ -654,11 +705,13 @@ hipError_t launch_i8_up(const int8_t* x, const float* x_scale, const int8_t* w13
                         const float* w13_scale, const int32_t* sorted_ids,
                         const int32_t* block_expert, const int2* tiles, const int32_t* num_tiles,
                         int max_tiles, int tile_rows, int H, int I, int top_k,
-                        int block, int16_t* act, uint8_t* act_exps, hipStream_t s) {
+                        int block, int16_t* act, uint8_t* act_exps, int act_rows,
+                        hipStream_t s) {
   I8Args p = grouped(x, x_scale, w13, w13_scale, sorted_ids, block_expert, tiles, num_tiles, H, I,
                      top_k, block);
   p.act = act;
   p.act_exps = act_exps;
+  p.act_rows = act_rows;
   return launch_expert<kUp>(p, max_tiles, tile_rows, s);
 }
 

@@ -93,15 +93,15 @@ __global__ __launch_bounds__(kQThreads) void i8_rows_kernel(const uint16_t* __re
 // values, whose rounding (2^-14 of the block's largest value at most) moves a code by one
 // only where 127 v / a lies within 127 * 2^-14 of a border.
 __global__ __launch_bounds__(kQThreads) void i8_act_kernel(
-    const int16_t* __restrict__ act, const uint8_t* __restrict__ exps, int I, int nblocks,
+    const int16_t* __restrict__ act, const uint8_t* __restrict__ exps, int64_t rows, int I,
     const int32_t* __restrict__ plan, const int32_t* __restrict__ num_padded, int n_ids,
     int8_t* __restrict__ codes, float* __restrict__ scales) {
   constexpr int KEEP = 4;       // 8-value chunks per lane kept in registers (I <= 2048)
   const int lane = threadIdx.x & 63;
   const int64_t row = (int64_t)blockIdx.x * (kQThreads / kWave) + (threadIdx.x >> 6);
   if (row >= *num_padded || (uint32_t)plan[row] >= (uint32_t)n_ids) return;
-  const int16_t* src = act + row * I;
-  const uint8_t* es = exps + row * nblocks;
+  auto value8 = [&](int ch) { return act + ((ch >> 4) * rows + row) * 128 + (ch & 15) * 8; };
+  auto exp8 = [&](int ch) { return exps[((ch >> 4) * rows + row) * 4 + ((ch >> 2) & 3)]; };
   const int nchunk = I >> 3;
   auto unit = [](uint32_t e) { return __uint_as_float((e - 13u) << 23); };   // 2^(e - 140)
   auto largest = [](u32x4 v) {
@@ -118,8 +118,8 @@ __global__ __launch_bounds__(kQThreads) void i8_act_kernel(
   for (int i = 0; i < KEEP; ++i) {
     const int ch = lane + kWave * i;
     const bool in = ch < nchunk;
-    keep[i] = in ? ld16(src + (size_t)ch * 8) : u32x4{0, 0, 0, 0};
-    e[i] = in ? es[ch >> 2] : 14u;
+    keep[i] = in ? ld16(value8(ch)) : u32x4{0, 0, 0, 0};
+    e[i] = in ? exp8(ch) : 14u;
   }
 #pragma unroll
   for (int i = 0; i < KEEP; ++i) {
@@ -127,9 +127,9 @@ __global__ __launch_bounds__(kQThreads) void i8_act_kernel(
     top = fmaxf(top, largest(keep[i]) * unit(e[i]));
   }
   for (int ch = lane + kWave * KEEP; ch < nchunk; ch += kWave) {
-    const uint32_t ex = es[ch >> 2];
+    const uint32_t ex = exp8(ch);
     bad |= ex == 255u;
-    top = fmaxf(top, largest(ld16(src + (size_t)ch * 8)) * unit(ex));
+    top = fmaxf(top, largest(ld16(value8(ch))) * unit(ex));
   }
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, kWave));
@@ -152,7 +152,7 @@ __global__ __launch_bounds__(kQThreads) void i8_act_kernel(
   for (int i = 0; i < KEEP; ++i)
     if (lane + kWave * i < nchunk) put(lane + kWave * i, keep[i], e[i]);
   for (int ch = lane + kWave * KEEP; ch < nchunk; ch += kWave)
-    put(ch, ld16(src + (size_t)ch * 8), es[ch >> 2]);
+    put(ch, ld16(value8(ch)), exp8(ch));
 }
 
 }  // namespace
@@ -161,7 +161,7 @@ hipError_t launch_i8_act(const int16_t* act, const uint8_t* exps, int64_t rows, 
                          const int32_t* plan, const int32_t* num_padded, int n_ids, int8_t* codes,
                          float* scales, hipStream_t s) {
   const dim3 grid((unsigned)((rows + 3) / 4));
-  hipLaunchKernelGGL(i8_act_kernel, grid, dim3(kQThreads), 0, s, act, exps, I, (I + 31) / 32, plan,
+  hipLaunchKernelGGL(i8_act_kernel, grid, dim3(kQThreads), 0, s, act, exps, rows, I, plan,
                      num_padded, n_ids, codes, scales);
   return hipGetLastError();
 }

@@ -18,6 +18,13 @@ hipError_t launch_route(const uint16_t* x, const uint16_t* wr, const float* bias
 hipError_t launch_router_keys(const uint16_t* x, const uint16_t* wr, int M, int H, int E,
                               double* keys, hipStream_t s);
 
+// fp32 partial logits `parts` x [M, E] and, behind them (*absdot), the sums of |x| |w|, which
+// bound a part's error by nround 2^-23 times the sum (1 + 2^-9); in the scratch of
+// launch_route.
+hipError_t launch_router_logits(const uint16_t* x, const uint16_t* wr, int M, int H, int E,
+                                float* logits, float** absdot, int* parts, int* nround,
+                                hipStream_t s);
+
 // Router with expert groups (route_groups.hip).
 struct GroupRule {
   int softmax;      // scores: softmax over the experts, else sigmoid
@@ -187,8 +194,9 @@ hipError_t launch_expert_down_frag_mx(const uint16_t* act, const uint8_t* w2c, c
                                      hipStream_t s);
 
 // int8 rows (i8_quant.hip): bf16 [rows, K] (K % 8 == 0) -> codes and the scale of each row;
-// and from the block floats [rows, I] of the up GEMM (bytes exps [rows, ceil(I / 32)]), for
-// the plan rows below *num_padded whose id is in [0, n_ids).
+// and from the block floats of the up GEMM (int16 [ceil(I / 128)][rows][128], bytes
+// [ceil(I / 128)][rows][4], one per 32 values), for the plan rows below *num_padded whose id
+// is in [0, n_ids).
 hipError_t launch_i8_rows(const uint16_t* v, int64_t rows, int K, int8_t* codes, float* scales,
                           hipStream_t s);
 hipError_t launch_i8_act(const int16_t* act, const uint8_t* exps, int64_t rows, int I,
@@ -201,13 +209,14 @@ hipError_t launch_i8_matmul(const int8_t* a, const float* a_scale, const int8_t*
                             const float* w_scale, int M, int N, int K, void* out, bool f32,
                             hipStream_t s);
 // Grouped over the tiles (height tile_rows, 64, 128 or 256) of a plan: up + SwiGLU -> act as
-// block floats [capacity, I] from the tokens' codes [M, H]; down from act's codes [capacity, I] to the
+// block floats (act_rows = capacity rows) from the tokens' codes [M, H]; down from act's codes [capacity, I] to the
 // split rows y / y0 of moe_forward.
 hipError_t launch_i8_up(const int8_t* x, const float* x_scale, const int8_t* w13,
                         const float* w13_scale, const int32_t* sorted_ids,
                         const int32_t* block_expert, const int2* tiles, const int32_t* num_tiles,
                         int max_tiles, int tile_rows, int H, int I, int top_k,
-                        int block, int16_t* act, uint8_t* act_exps, hipStream_t s);
+                        int block, int16_t* act, uint8_t* act_exps, int act_rows,
+                        hipStream_t s);
 hipError_t launch_i8_down(const int8_t* act, const float* act_scale, const int8_t* w2,
                           const float* w2_scale, const int32_t* sorted_ids,
                           const int32_t* block_expert, const int2* tiles,

@@ -681,6 +681,7 @@ int moe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows,
 namespace {
 
 constexpr int kMaxGroups = 64;
+constexpr int kMaxRouteTokens = 1 << 24;   // a wave per token: 2^30 threads
 constexpr int kMaxI8K = 131072;   // 127^2 * kMaxI8K < 2^31: int32 sums are exact
 
 bool make_rule(int32_t E, int32_t top_k, int32_t score, int32_t n_group, int32_t topk_group,
@@ -700,18 +701,19 @@ bool make_rule(int32_t E, int32_t top_k, int32_t score, int32_t n_group, int32_t
 // the int8 act with their scales.
 struct I8Layout {
   Layout base;
-  size_t xq, xs, ae, aq, as, total;
+  size_t xq, xs, am, ae, as, total;   // the codes of act take the place of its bf16
 };
 
 I8Layout i8_layout_of(int32_t M, int32_t H, int32_t E, int32_t I, int32_t top_k, int32_t block) {
   I8Layout L;
   L.base = layout_of(M, H, E, I, top_k, block);
   const size_t cap = capacity_of(M, top_k, E, block);
+  const size_t blocks = ((size_t)I + 127) / 128;
   size_t off = round_up(L.base.total, kAlign);
   L.xq = off;  off += round_up((size_t)M * H, kAlign);
   L.xs = off;  off += round_up((size_t)M * sizeof(float), kAlign);
-  L.ae = off;  off += round_up(cap * (size_t)((I + 31) / 32), kAlign);
-  L.aq = off;  off += round_up(cap * (size_t)I, kAlign);
+  L.am = off;  off += round_up(cap * blocks * 128 * sizeof(int16_t), kAlign);
+  L.ae = off;  off += round_up(cap * blocks * 4, kAlign);
   L.as = off;  off += round_up(cap * sizeof(float), kAlign);
   L.total = off;
   return L;
@@ -743,7 +745,8 @@ int moe_route_groups(const uint16_t* x, const uint16_t* router_w, const float* s
   moe::GroupRule rule;
   if (!make_rule(E, top_k, score, n_group, topk_group, group_top, renormalize, scale, &rule))
     return MOE_ERR_INVALID_ARG;
-  if (M < 0 || H < 8 || H > kMaxH || H % 8 != 0 || (int64_t)M * top_k >= ((int64_t)1 << 31))
+  if (M < 0 || M > kMaxRouteTokens || H < 8 || H > kMaxH || H % 8 != 0 ||
+      (int64_t)M * top_k >= ((int64_t)1 << 31))
     return MOE_ERR_INVALID_ARG;
   if (M == 0) return MOE_OK;
   if (!x || !router_w || !topk_ids || !topk_w || !aligned(x, 16) || !aligned(router_w, 16) ||
@@ -763,7 +766,7 @@ int moe_route_logits(const float* logits, int64_t ld, const float* select_bias, 
   moe::GroupRule rule;
   if (!make_rule(E, top_k, score, n_group, topk_group, group_top, renormalize, scale, &rule))
     return MOE_ERR_INVALID_ARG;
-  if (M < 0 || ld < E || ld > ((int64_t)1 << 32) || (int64_t)M * top_k >= ((int64_t)1 << 31))
+  if (M < 0 || M > kMaxRouteTokens || ld < E || ld > ((int64_t)1 << 32) || (int64_t)M * top_k >= ((int64_t)1 << 31))
     return MOE_ERR_INVALID_ARG;
   if (M == 0) return MOE_OK;
   if (!logits || !topk_ids || !topk_w || !aligned(logits, 4) || !aligned(topk_ids, 4) ||
@@ -823,10 +826,10 @@ int moe_forward_i8(const uint16_t* x, const uint16_t* router_w, const float* sel
                    void* workspace, size_t workspace_bytes, const moe_event_t* stage_events,
                    moe_stream_t stream) {
   moe::GroupRule rule;
-  if (!i8_sizes_ok(M, H, E, I, top_k) || !(eps > 0.0f) || !isfinite(eps) ||
+  if (!i8_sizes_ok(M, H, E, I, top_k) || M > kMaxRouteTokens || !(eps > 0.0f) || !isfinite(eps) ||
       !make_rule(E, top_k, score, n_group, topk_group, group_top, renormalize, scale, &rule))
     return MOE_ERR_INVALID_ARG;
-  if (!gemm_block_ok(block)) return MOE_ERR_UNSUPPORTED;
+  if (!gemm_block_ok(block) || (int64_t)M * H >= ((int64_t)1 << 32)) return MOE_ERR_UNSUPPORTED;
   if (M == 0) return MOE_OK;
   if (!x || !router_w || !w13_codes || !w13_scales || !w2_codes || !w2_scales || !residual ||
       !norm_w || !out)
@@ -854,13 +857,13 @@ int moe_forward_i8(const uint16_t* x, const uint16_t* router_w, const float* sel
   int32_t* npad = num_padded_out ? num_padded_out : reinterpret_cast<int32_t*>(ws + B.npad);
   int2* tiles = reinterpret_cast<int2*>(ws + B.tiles);
   int32_t* ntiles = reinterpret_cast<int32_t*>(ws + B.ntiles);
-  int16_t* act = reinterpret_cast<int16_t*>(ws + B.act);
+  int16_t* act = reinterpret_cast<int16_t*>(ws + L.am);
   uint8_t* ae = reinterpret_cast<uint8_t*>(ws + L.ae);
   uint16_t* y = reinterpret_cast<uint16_t*>(ws + B.y);
   float* y0 = reinterpret_cast<float*>(ws + B.y0);
   int8_t* xq = reinterpret_cast<int8_t*>(ws + L.xq);
   float* xs = reinterpret_cast<float*>(ws + L.xs);
-  int8_t* aq = reinterpret_cast<int8_t*>(ws + L.aq);
+  int8_t* aq = reinterpret_cast<int8_t*>(ws + B.act);
   float* as = reinterpret_cast<float*>(ws + L.as);
   hipStream_t s = (hipStream_t)stream;
 
@@ -881,7 +884,7 @@ int moe_forward_i8(const uint16_t* x, const uint16_t* router_w, const float* sel
     return MOE_ERR_HIP;
   if (!mark(2)) return MOE_ERR_HIP;
   if (moe::launch_i8_up(xq, xs, w13_codes, w13_scales, sorted, bexp, tiles, ntiles, max_tiles,
-                        trows, H, I, top_k, block, act, ae, s) != hipSuccess)
+                        trows, H, I, top_k, block, act, ae, (int)cap, s) != hipSuccess)
     return MOE_ERR_HIP;
   if (!mark(3)) return MOE_ERR_HIP;
   if (moe::launch_i8_act(act, ae, (int64_t)cap, I, sorted, npad, n, aq, as, s) != hipSuccess ||
