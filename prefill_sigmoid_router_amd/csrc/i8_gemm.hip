@@ -139,6 +139,23 @@ __device__ __forceinline__ void store_act(const I8Args& p, int row, int c, const
   if ((c & 31) == 0 && c < p.ncols) p.act_exps[block_row * 4 + ((c >> 5) & 3)] = (uint8_t)E;
 }
 
+// 16 results of a dense row that starts at `row` (in values), columns n0 on
+template <bool F32>
+__device__ __forceinline__ void store_dense(const I8Args& p, size_t row, int n0,
+                                            const float (&v)[16]) {
+  if (n0 + 15 < p.ncols && p.ncols % 8 == 0) {
+    if (F32) store16(static_cast<float*>(p.out) + row + n0, v);
+    else store16(static_cast<uint16_t*>(p.out) + row + n0, v);
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < 16; ++q)
+    if (n0 + q < p.ncols) {
+      if (F32) static_cast<float*>(p.out)[row + n0 + q] = v[q];
+      else static_cast<uint16_t*>(p.out)[row + n0 + q] = (uint16_t)f32_to_bf16_rne(v[q]);
+    }
+}
+
 template <int BM, int WN, int WM>
 struct I8Cfg {
   static constexpr int THREADS = 64 * WN * WM;
@@ -303,30 +320,21 @@ __global__ __launch_bounds__(64 * WN * WM) void i8_gemm_kernel(I8Args p) {
       } else if (n0 < p.ncols) {
         const float xs = p.tok_scale[row];
         const i32x4 v4[4] = {acc[0][s], acc[1][s], acc[2][s], acc[3][s]};
-        float v[16];
-        if (MODE == kDown || (n0 + 15 < p.ncols && p.ncols % 8 == 0)) {
-          float w[16];
+        float v[16], w[16];
+        if (MODE == kDown || n0 + 15 < p.ncols) {
           load16(ws + n0, w);
-#pragma unroll
-          for (int q = 0; q < 16; ++q) v[q] = (float)v4[q >> 2][q & 3] * (xs * w[q]);
-          if (MODE == kDown) {
-            const YRow yr = y_row(p.sorted_ids[row], p.top_k, p.ncols);
-            if (yr.first) store16(p.y0 + yr.off + n0, v);
-            else store16(p.y + yr.off + n0, v);
-          } else if (F32) {
-            store16(static_cast<float*>(p.out) + (size_t)row * p.ncols + n0, v);
-          } else {
-            store16(static_cast<uint16_t*>(p.out) + (size_t)row * p.ncols + n0, v);
-          }
         } else {
-          const size_t o = (size_t)row * p.ncols + n0;
 #pragma unroll
-          for (int q = 0; q < 16; ++q)
-            if (n0 + q < p.ncols) {
-              const float f = (float)v4[q >> 2][q & 3] * (xs * ws[n0 + q]);
-              if (F32) static_cast<float*>(p.out)[o + q] = f;
-              else static_cast<uint16_t*>(p.out)[o + q] = (uint16_t)f32_to_bf16_rne(f);
-            }
+          for (int q = 0; q < 16; ++q) w[q] = ws[min(n0 + q, p.ncols - 1)];
+        }
+#pragma unroll
+        for (int q = 0; q < 16; ++q) v[q] = (float)v4[q >> 2][q & 3] * (xs * w[q]);
+        if (MODE == kDense) {
+          store_dense<F32>(p, (size_t)row * p.ncols, n0, v);
+        } else {
+          const YRow yr = y_row(p.sorted_ids[row], p.top_k, p.ncols);
+          if (yr.first) store16(p.y0 + yr.off + n0, v);
+          else store16(p.y + yr.off + n0, v);
         }
       }
     }
@@ -345,7 +353,7 @@ hipError_t launch(I8Args& a, long token_tiles, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Grouped products over whole 128-wide chunks (K % 128 == 0).
+// Grouped products, and dense ones of many rows, over whole 128-wide chunks (K % 128 == 0).
 //
 // 256 weight rows (UP: 128 act columns) per workgroup of 8 waves, 4 along the weight rows and
 // 2 along the tokens, against up to ROWS token rows of an expert at once, so that its weights
@@ -387,7 +395,7 @@ struct GroupedItem {
   int start, nlive, e, col0;
 };
 
-template <Mode MODE, typename R, int WPOL>
+template <Mode MODE, typename R, int WPOL, bool F32>
 __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char* lds) {
   constexpr bool UP = MODE == kUp;
   constexpr int D = R::D, PW = R::PW, TPW = R::TPW, MTW = R::MTW;
@@ -397,16 +405,22 @@ __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char*
   const int K = p.K;
   unsigned char* const tlds = lds + 2 * R::WSTAGE;
 
-  TiledWalk walk(*p.num_tiles, p.n_ntiles);
+  TiledWalk walk(MODE == kDense ? (p.M + R::ROWS - 1) / R::ROWS : *p.num_tiles, p.n_ntiles);
   auto next_item = [&](GroupedItem& it) -> bool {
     int ntile, ti;
     if (!walk.next(ntile, ti)) return false;
     const int l = ntile * walk.ntiles_live + ti;   // expert by expert: its N tiles share its
     ti = l / p.n_ntiles;                           // token rows through the XCD's L2
-    const int2 tile = p.tiles[ti];
-    it.start = tile.x;
-    it.nlive = tile.y;
-    it.e = p.block_expert[tile.x / p.block];
+    if (MODE == kDense) {
+      it.start = ti * R::ROWS;
+      it.nlive = min(R::ROWS, p.M - it.start);
+      it.e = 0;
+    } else {
+      const int2 tile = p.tiles[ti];
+      it.start = tile.x;
+      it.nlive = tile.y;
+      it.e = p.block_expert[tile.x / p.block];
+    }
     it.col0 = (l % p.n_ntiles) * (UP ? 128 : 256);
     return true;
   };
@@ -530,7 +544,7 @@ __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char*
 #pragma unroll
     for (int s = 0; s < MTW; ++s) {
       const int row = it.start + min(16 * (2 * s + wm) + li, it.nlive - 1);
-      id[s] = p.sorted_ids[row];
+      id[s] = MODE == kDense ? 0 : p.sorted_ids[row];
       if (!UP) xs[s] = p.tok_scale[row];
     }
     if (UP) {
@@ -546,13 +560,23 @@ __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char*
       }
     } else if (n0 < p.ncols) {
       float w[16];
-      load16(ws + n0, w);
+      if (MODE == kDown || n0 + 15 < p.ncols) {
+        load16(ws + n0, w);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 16; ++q) w[q] = ws[min(n0 + q, p.ncols - 1)];
+      }
 #pragma unroll
       for (int s = 0; s < MTW; ++s) {
-        if (16 * (2 * s + wm) + li >= it.nlive) continue;
+        const int r = 16 * (2 * s + wm) + li;
+        if (r >= it.nlive) continue;
         float v[16];
 #pragma unroll
         for (int q = 0; q < 16; ++q) v[q] = (float)acc[q >> 2][s][q & 3] * (xs[s] * w[q]);
+        if (MODE == kDense) {
+          store_dense<F32>(p, (size_t)(it.start + r) * p.ncols, n0, v);
+          continue;
+        }
         const YRow yr = y_row(id[s], p.top_k, p.ncols);
         if (yr.first) store16(p.y0 + yr.off + n0, v);
         else store16(p.y + yr.off + n0, v);
@@ -625,12 +649,12 @@ __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char*
 
 constexpr int kGroupedLds = 160 * 1024;
 
-template <Mode MODE, typename R, int WPOL>
+template <Mode MODE, typename R, int WPOL, bool F32>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void i8_grouped_kernel(
     I8Args p) {
   __shared__ __align__(16) unsigned char lds[R::LDS];
 #ifdef __HIP_DEVICE_COMPILE__
-  grouped_products<MODE, R, WPOL>(p, lds);
+  grouped_products<MODE, R, WPOL, F32>(p, lds);
 #endif
 }
 
@@ -638,14 +662,100 @@ using RingFew = Ring<64, 4>;
 using RingMid = Ring<128, 4>;
 using RingMany = Ring<256, 2>;
 
-template <Mode MODE, typename R, int WPOL>
+template <Mode MODE, typename R, int WPOL, bool F32 = false>
 hipError_t launch_grouped(I8Args& a, long token_tiles, hipStream_t s) {
   const int per = MODE == kUp ? 128 : 256;
   a.n_ntiles = (a.ncols + per - 1) / per;
   // one workgroup per CU, whatever its LDS would allow: 512 threads of up to 256 registers
   const long grid = walk_grid(token_tiles * a.n_ntiles, kGroupedLds);
-  hipLaunchKernelGGL((i8_grouped_kernel<MODE, R, WPOL>), dim3((unsigned)grid), dim3(512), 0, s, a);
+  hipLaunchKernelGGL((i8_grouped_kernel<MODE, R, WPOL, F32>), dim3((unsigned)grid), dim3(512), 0, s, a);
   return hipGetLastError();
+}
+
+// Dense products of few rows: 16 weight rows x 16 MT token rows per workgroup, the 128-wide
+// units of K dealt over its 8 waves, whose int32 sums meet in LDS.  Fragments come straight
+// from memory (a weight row's line is read by one wave), BATCH units at a time in flight.
+// Bound by the latency of one pass over the weights: 16 rows per workgroup, so that N = 4096
+// fills the 256 CUs.
+template <int MT, bool F32>
+__global__ __launch_bounds__(512) void i8_skinny_kernel(I8Args p, int mblocks, int per_xcd) {
+  constexpr int WAVES = 8, BATCH = MT == 1 ? 4 : 2;
+  __shared__ int part[WAVES][MT][4][kWave];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int li = lane & 15, lg = lane >> 4;
+  // the token blocks of a weight tile run on one XCD
+  const int slot = blockIdx.x / kXcds, item = (blockIdx.x % kXcds) * per_xcd + slot;
+  if (slot >= per_xcd || item >= p.n_ntiles * mblocks) return;
+  const int n0 = item / mblocks * 16, m0 = item % mblocks * (16 * MT);
+  const int K = p.K, units = (K + kKC - 1) / kKC, whole = K / kKC;
+  const int8_t* wrow = p.w + (size_t)min(n0 + li, p.ncols - 1) * K + 16 * lg;
+  const int8_t* trow[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) trow[t] = p.tok + (size_t)min(m0 + 16 * t + li, p.M - 1) * K + 16 * lg;
+  i32x4 acc[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) acc[t] = i32x4{0, 0, 0, 0};
+  for (int u0 = wave; u0 < units; u0 += WAVES * BATCH) {
+    u32x4 w[BATCH][2], x[BATCH][MT][2];
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b) {
+      const int u = u0 + WAVES * b;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        // behind column K zeros meet zeros
+        const bool in = u < whole || (u < units && u * kKC + 64 * h + 16 * lg < K);
+        const size_t off = (size_t)u * kKC + 64 * h;
+        w[b][h] = in ? ld16(wrow + off) : u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int t = 0; t < MT; ++t) x[b][t][h] = in ? ld16(trow[t] + off) : u32x4{0, 0, 0, 0};
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[t] = mfma_i8(w[b][h], x[b][t][h], acc[t]);
+  }
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) part[wave][t][q][lane] = acc[t][q];
+  __syncthreads();
+  // thread -> token r, column c: lane 16 (c / 4) + r % 16, result c % 4 of token tile r / 16
+  for (int i = threadIdx.x; i < 256 * MT; i += 64 * WAVES) {
+    const int r = i >> 4, c = i & 15;
+    if (m0 + r >= p.M || n0 + c >= p.ncols) continue;
+    int sum = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) sum += part[w][r >> 4][c & 3][16 * (c >> 2) + (r & 15)];
+    const float v = (float)sum * (p.tok_scale[m0 + r] * p.w_scale[n0 + c]);
+    const size_t o = (size_t)(m0 + r) * p.ncols + n0 + c;
+    if (F32) static_cast<float*>(p.out)[o] = v;
+    else static_cast<uint16_t*>(p.out)[o] = (uint16_t)f32_to_bf16_rne(v);
+  }
+}
+
+template <int MT, bool F32>
+hipError_t launch_skinny(I8Args& a, hipStream_t s) {
+  a.n_ntiles = (a.ncols + 15) / 16;
+  const int mblocks = (a.M + 16 * MT - 1) / (16 * MT);
+  const int64_t per_xcd = ((int64_t)a.n_ntiles * mblocks + kXcds - 1) / kXcds;
+  hipLaunchKernelGGL((i8_skinny_kernel<MT, F32>), dim3((unsigned)(per_xcd * kXcds)), dim3(512), 0, s,
+                     a, mblocks, (int)per_xcd);
+  return hipGetLastError();
+}
+
+template <bool F32>
+hipError_t launch_dense(I8Args& a, hipStream_t s) {
+  const int64_t mid = (int64_t)((a.M + 63) / 64) * ((a.ncols + 63) / 64);
+  const int64_t big = (int64_t)((a.M + 255) / 256) * ((a.ncols + 255) / 256);
+  if (a.M <= 16) return launch_skinny<1, F32>(a, s);
+  if (a.M <= 96) return launch_skinny<2, F32>(a, s);
+  if (big >= 96 && a.K % kKC == 0 && a.K / kKC > 4)
+    return launch_grouped<kDense, RingMany, 0, F32>(a, (a.M + 255L) / 256, s);
+  if (mid >= 1024) return launch<64, 4, 1, 3, kDense, F32, 0>(a, (a.M + 63L) / 64, s);
+  return launch<64, 1, 4, 4, kDense, F32, 0>(a, (a.M + 63L) / 64, s);
 }
 
 template <Mode MODE>
@@ -676,9 +786,7 @@ hipError_t launch_i8_matmul(const int8_t* a, const float* a_scale, const int8_t*
   p.ncols = N;
   p.top_k = p.block = 1;
   p.out = out;
-  const long tt = (M + 63L) / 64;
-  return f32 ? launch<64, 4, 1, 3, kDense, true, 0>(p, tt, s)
-             : launch<64, 4, 1, 3, kDense, false, 0>(p, tt, s);
+  return f32 ? launch_dense<true>(p, s) : launch_dense<false>(p, s);
 }
 
 static I8Args grouped(const int8_t* tok, const float* tok_scale, const int8_t* w,
