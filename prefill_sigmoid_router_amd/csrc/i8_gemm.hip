@@ -11,6 +11,8 @@
 //
 // UP: tokens gathered through the plan, gate and up rows of 32 WN act columns, SwiGLU, act
 // as block floats (below).  DOWN: act rows of the plan, results to the split y rows.  DENSE: plain rows.
+#include <math.h>
+
 #include <type_traits>
 
 #include "device_common.h"
@@ -608,8 +610,8 @@ __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char*
     for (; c + 2 * D < steps; c += D) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        copy_t(qc, c + d + D);
         compute(cur, c + d, [&] {
+          copy_t(qc, c + d + D);
           put_w((d + 1) & 1, wreg[d]);
           load_w(qc, c + d + 1 + D, wreg[d]);
         });
@@ -619,8 +621,8 @@ __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char*
     // the last 2 D steps reach into the next item
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      copy_t(qc, c + d + D);
       compute(cur, c + d, [&] {
+        copy_t(qc, c + d + D);
         put_w((d + 1) & 1, wreg[d]);
         if (d + 1 < D) load_w(qc, c + d + 1 + D, wreg[d]);
         else load_w(qn, 0, wreg[d]);
@@ -630,8 +632,8 @@ __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char*
     c += D;
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      copy_t(qn, d);
       compute(cur, c + d, [&] {
+        copy_t(qn, d);
         put_w((d + 1) & 1, wreg[d]);
         load_w(qn, d + 1, wreg[d]);
       });
@@ -679,7 +681,7 @@ hipError_t launch_grouped(I8Args& a, long token_tiles, hipStream_t s) {
 // fills the 256 CUs.
 template <int MT, bool F32>
 __global__ __launch_bounds__(512) void i8_skinny_kernel(I8Args p, int mblocks, int per_xcd) {
-  constexpr int WAVES = 8, BATCH = MT == 1 ? 4 : 2;
+  constexpr int WAVES = 8, BATCH = MT == 1 ? 4 : MT == 2 ? 2 : 1;
   __shared__ int part[WAVES][MT][4][kWave];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int li = lane & 15, lg = lane >> 4;
@@ -746,16 +748,44 @@ hipError_t launch_skinny(I8Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Variants of the dense product, by the time that a 128-wide step of K takes each (us,
+// measured at K = 7168, N = 4096 with the chip full; the sums of the steps' latencies count
+// where it is not):
+//   workgroups of 16 weight rows, K over the waves, 64 tokens: 0.08 + 0.29 per 256 of them
+//     (M=64: 21 us against 26.6 for 64 x 64 tiles; M=128: 35 against 27)
+//   64 x 64 tiles, two workgroups a CU: 0.48 up to 256 of them, then 0.64 per 512
+//     (M=256: 28 us against 41; M=512: 36 against 49; M=1024: 69 against 54)
+//   step streams of 64, 128, 256 tokens x 256 weight rows: 0.88, 1.33, 2.09 per 256
+//     (M=1024: 54, 61, 88 us; M=2048: 98, 74, 92; M=3500: 178, 136, 117)
 template <bool F32>
 hipError_t launch_dense(I8Args& a, hipStream_t s) {
-  const int64_t mid = (int64_t)((a.M + 63) / 64) * ((a.ncols + 63) / 64);
-  const int64_t big = (int64_t)((a.M + 255) / 256) * ((a.ncols + 255) / 256);
   if (a.M <= 16) return launch_skinny<1, F32>(a, s);
-  if (a.M <= 96) return launch_skinny<2, F32>(a, s);
-  if (big >= 96 && a.K % kKC == 0 && a.K / kKC > 4)
-    return launch_grouped<kDense, RingMany, 0, F32>(a, (a.M + 255L) / 256, s);
-  if (mid >= 1024) return launch<64, 4, 1, 3, kDense, F32, 0>(a, (a.M + 63L) / 64, s);
-  return launch<64, 1, 4, 4, kDense, F32, 0>(a, (a.M + 63L) / 64, s);
+  if (a.M <= 32) return launch_skinny<2, F32>(a, s);
+  auto tiles = [&](int m, int n) {
+    return (double)((a.M + m - 1) / m) * (double)((a.ncols + n - 1) / n);
+  };
+  const double t64 = tiles(64, 64);
+  double best = t64 <= 256 ? 0.48 : 0.64 * ceil(t64 / 512);
+  int pick = 0;
+  auto offer = [&](int which, double cost) {
+    if (cost < best) {
+      best = cost;
+      pick = which;
+    }
+  };
+  offer(1, 0.08 + 0.29 * tiles(64, 16) / 256);
+  if (a.K % kKC == 0 && a.K / kKC > 4) {
+    offer(64, 0.88 * ceil(tiles(64, 256) / 256));
+    offer(128, 1.33 * ceil(tiles(128, 256) / 256));
+    offer(256, 2.09 * ceil(tiles(256, 256) / 256));
+  }
+  switch (pick) {
+    case 1: return launch_skinny<4, F32>(a, s);
+    case 64: return launch_grouped<kDense, RingFew, 0, F32>(a, (a.M + 63L) / 64, s);
+    case 128: return launch_grouped<kDense, RingMid, 0, F32>(a, (a.M + 127L) / 128, s);
+    case 256: return launch_grouped<kDense, RingMany, 0, F32>(a, (a.M + 255L) / 256, s);
+    default: return launch<64, 1, 4, 4, kDense, F32, 0>(a, (a.M + 63L) / 64, s);
+  }
 }
 
 template <Mode MODE>
