@@ -705,6 +705,23 @@ def moe_forward_mx(x, router_w, router_bias, w13_codes, w13_scales, w2_codes, w2
 SCORE_SIGMOID, SCORE_SOFTMAX = 0, 1   # MOE_SCORE_* of include/moe.h
 
 
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _launch_stream(stream, *tensors):
+    """The stream to launch on (the current one by default).  The library launches on the
+    current device, so every tensor has to be there."""
+    device = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"tensors must be on the current device (cuda:{device}), "
+                             f"got one on {t.device}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return _stream(stream)
+
+
 def moe_route_groups_workspace_bytes(M: int, E: int) -> int:
     return int(load_library().moe_route_groups_workspace_bytes(M, E))
 
@@ -729,9 +746,10 @@ def moe_route_groups(x, router_w, select_bias, top_k: int, topk_ids, topk_w, wor
     _need(topk_w, "topk_w", torch.float32, (M, top_k))
     _need(workspace, "workspace", torch.uint8)
     _check("moe_route_groups", load_library().moe_route_groups(
-        _ptr(x), _ptr(router_w), _ptr(select_bias), M, H, E, top_k, score, n_group, topk_group,
-        group_top, int(bool(renormalize)), float(scale), _ptr(topk_ids), _ptr(topk_w),
-        _ptr(workspace), workspace.numel(), _stream(stream)))
+        _at(x), _at(router_w), _at(select_bias), M, H, E, top_k, score, n_group, topk_group,
+        group_top, int(bool(renormalize)), float(scale), _at(topk_ids), _at(topk_w),
+        _at(workspace), workspace.numel(),
+        _launch_stream(stream, x, router_w, select_bias, topk_ids, topk_w, workspace)))
 
 
 def moe_route_logits(logits, select_bias, top_k: int, topk_ids, topk_w,
@@ -751,9 +769,9 @@ def moe_route_logits(logits, select_bias, top_k: int, topk_ids, topk_w,
     _need(topk_ids, "topk_ids", torch.int32, (M, top_k))
     _need(topk_w, "topk_w", torch.float32, (M, top_k))
     _check("moe_route_logits", load_library().moe_route_logits(
-        _ptr(logits), logits.stride(0) if M > 1 else E, _ptr(select_bias), M, E, top_k, score,
-        n_group, topk_group, group_top, int(bool(renormalize)), float(scale), _ptr(topk_ids),
-        _ptr(topk_w), _stream(stream)))
+        _at(logits), logits.stride(0) if M > 1 else E, _at(select_bias), M, E, top_k, score,
+        n_group, topk_group, group_top, int(bool(renormalize)), float(scale), _at(topk_ids),
+        _at(topk_w), _launch_stream(stream, logits, select_bias, topk_ids, topk_w)))
 
 
 def moe_i8_quantize(v, codes, scales, stream=None):
@@ -763,7 +781,8 @@ def moe_i8_quantize(v, codes, scales, stream=None):
     _need(codes, "codes", torch.int8, tuple(v.shape))
     _need(scales, "scales", torch.float32, tuple(v.shape[:-1]))
     _check("moe_i8_quantize", load_library().moe_i8_quantize(
-        _ptr(v), scales.numel(), K, _ptr(codes), _ptr(scales), _stream(stream)))
+        _at(v), scales.numel(), K, _at(codes), _at(scales),
+        _launch_stream(stream, v, codes, scales)))
 
 
 def moe_i8_matmul_workspace_bytes(M: int, N: int, K: int) -> int:
@@ -784,8 +803,9 @@ def moe_i8_matmul(a, a_scales, w, w_scales, out, workspace=None, stream=None):
     if workspace is not None:
         _need(workspace, "workspace", torch.uint8)
     _check("moe_i8_matmul", load_library().moe_i8_matmul(
-        _ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales), M, N, K, _ptr(out), int(f32),
-        _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream)))
+        _at(a), _at(a_scales), _at(w), _at(w_scales), M, N, K, _at(out), int(f32),
+        _at(workspace), 0 if workspace is None else workspace.numel(),
+        _launch_stream(stream, a, a_scales, w, w_scales, out, workspace)))
 
 
 def moe_i8_workspace_bytes(M: int, H: int, E: int, I: int, top_k: int, block: int) -> int:
@@ -841,12 +861,14 @@ def moe_forward_i8(x, router_w, select_bias, w13_codes, w13_scales, w2_codes, w2
             raise ValueError("stage_events must hold 6 events")
         ev = (ctypes.c_void_p * 6)(*[e.handle for e in stage_events])
     _check("moe_forward_i8", load_library().moe_forward_i8(
-        _ptr(x), _ptr(router_w), _ptr(select_bias), _ptr(w13_codes), _ptr(w13_scales),
-        _ptr(w2_codes), _ptr(w2_scales), _ptr(residual), _ptr(norm_w), float(eps), M, H, E, I,
+        _at(x), _at(router_w), _at(select_bias), _at(w13_codes), _at(w13_scales),
+        _at(w2_codes), _at(w2_scales), _at(residual), _at(norm_w), float(eps), M, H, E, I,
         top_k, block, score, n_group, topk_group, group_top, int(bool(renormalize)), float(scale),
-        _ptr(out), _ptr(residual_out), _ptr(topk_ids_out), _ptr(topk_w_out), _ptr(sorted_ids_out),
-        _ptr(block_expert_out), _ptr(num_padded_out), _ptr(workspace), workspace.numel(), ev,
-        _stream(stream)))
+        _at(out), _at(residual_out), _at(topk_ids_out), _at(topk_w_out), _at(sorted_ids_out),
+        _at(block_expert_out), _at(num_padded_out), _at(workspace), workspace.numel(), ev,
+        _launch_stream(stream, x, router_w, select_bias, w13_codes, w13_scales, w2_codes,
+                       w2_scales, residual, norm_w, out, workspace, residual_out, topk_ids_out,
+                       topk_w_out, sorted_ids_out, block_expert_out, num_padded_out)))
 
 
 # ---------------------------------------------------------------------------------------

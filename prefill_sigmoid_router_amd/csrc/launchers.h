@@ -18,18 +18,12 @@ hipError_t launch_route(const uint16_t* x, const uint16_t* wr, const float* bias
 hipError_t launch_router_keys(const uint16_t* x, const uint16_t* wr, int M, int H, int E,
                               double* keys, hipStream_t s);
 
-// fp32 partial logits `parts` x [M, E] and, behind them (*absdot), the sums of |x| |w|, which
-// bound a part's error by nround 2^-23 times the sum (1 + 2^-9); in the scratch of
-// launch_route.
-hipError_t launch_router_logits(const uint16_t* x, const uint16_t* wr, int M, int H, int E,
-                                float* logits, float** absdot, int* parts, int* nround,
-                                hipStream_t s);
-
 // Router with expert groups (route_groups.hip).
 struct GroupRule {
   int softmax;      // scores: softmax over the experts, else sigmoid
   int n_group;      // 1 .. 64
   int per;          // experts per group, E / n_group
+  uint32_t per_magic;   // ceil(2^20 / per): e / per = e * per_magic >> 20 for e < 1024
   int topk_group;   // groups that stay
   int group_top;    // 1 or 2: largest scores that make a group's
   int renorm;       // weights divided by their sum over the picks

@@ -692,8 +692,8 @@ bool make_rule(int32_t E, int32_t top_k, int32_t score, int32_t n_group, int32_t
   if (topk_group < 1 || topk_group > n_group || group_top < 1 || group_top > 2 || group_top > per)
     return false;
   if (top_k < 1 || top_k > topk_group * per || !isfinite(scale)) return false;
-  *rule = moe::GroupRule{score == MOE_SCORE_SOFTMAX, n_group, per, topk_group, group_top,
-                         renormalize != 0, scale};
+  *rule = moe::GroupRule{score == MOE_SCORE_SOFTMAX, n_group, per,
+                         ((1u << 20) + per - 1) / per, topk_group, group_top, renormalize != 0, scale};
   return true;
 }
 

@@ -527,33 +527,24 @@ hipError_t launch_router_keys(const uint16_t* x, const uint16_t* wr, int M, int 
                  : launch_keys<4, 4, 2>(x, wr, M, H, E, keys, s);
 }
 
-hipError_t launch_router_logits(const uint16_t* x, const uint16_t* wr, int M, int H, int E,
-                                float* logits, float** absdot, int* parts, int* nround,
-                                hipStream_t s) {
-  // K is cut into parts (whole 64-wide chunks) so that about 512 workgroups run; the
-  // workspace holds parts x [M, E] fp32 logits, then parts x [M, E] fp32 |x|.|w|
-  const int base = ((E + kLgExperts - 1) / kLgExperts) * ((M + kLgTokens - 1) / kLgTokens);
-  *parts = std::min(kLgMaxParts, std::max(1, (512 + base - 1) / base));
-  const int chunks = (H + kLgKC - 1) / kLgKC;
-  const int kpart = ((chunks + *parts - 1) / *parts) * kLgKC;
-  *nround = 32 + (kpart + 31) / 32;
-  *absdot = logits + (size_t)*parts * M * E;
-  hipLaunchKernelGGL(router_logits_mfma_kernel,
-                     dim3((E + kLgExperts - 1) / kLgExperts, (M + kLgTokens - 1) / kLgTokens, *parts),
-                     dim3(256), 0, s, x, wr, M, H, E, kpart, logits, *absdot);
-  return hipGetLastError();
-}
-
 hipError_t launch_route(const uint16_t* x, const uint16_t* wr, const float* bias, int M, int H,
                         int E, int top_k, int32_t* ids, float* w, double* keys, hipStream_t s) {
   hipError_t err;
   const int per_thread = (E + kTopkThreads - 1) / kTopkThreads;
   if (M >= kRouteCertifiedMinTokens) {
-    int parts = 0, nround = 0;
+    // K is cut into parts (whole 64-wide chunks) so that about 512 workgroups run; the
+    // workspace holds parts x [M, E] fp32 logits, then parts x [M, E] fp32 |x|.|w|
+    const int base = ((E + kLgExperts - 1) / kLgExperts) * ((M + kLgTokens - 1) / kLgTokens);
+    const int parts = std::min(kLgMaxParts, std::max(1, (512 + base - 1) / base));
+    const int chunks = (H + kLgKC - 1) / kLgKC;
+    const int kpart = ((chunks + parts - 1) / parts) * kLgKC;
+    const int nround = 32 + (kpart + 31) / 32;
     float* logits = reinterpret_cast<float*>(keys);
-    float* absdot = nullptr;
-    err = launch_router_logits(x, wr, M, H, E, logits, &absdot, &parts, &nround, s);
-    if (err != hipSuccess) return err;
+    float* absdot = logits + (size_t)parts * M * E;
+    hipLaunchKernelGGL(router_logits_mfma_kernel,
+                       dim3((E + kLgExperts - 1) / kLgExperts, (M + kLgTokens - 1) / kLgTokens, parts),
+                       dim3(256), 0, s, x, wr, M, H, E, kpart, logits, absdot);
+    if ((err = hipGetLastError()) != hipSuccess) return err;
     const size_t lds = (size_t)H * 2 + (size_t)E * (3 * sizeof(double) + sizeof(int));
 #define MOE_SELECT(SLV)                                                                     \
   hipLaunchKernelGGL((router_select_kernel<SLV>), dim3(M), dim3(kTopkThreads), lds, s, x, wr, \

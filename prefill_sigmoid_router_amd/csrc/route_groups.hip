@@ -15,10 +15,12 @@
 // adds nothing to its group, it is picked only after every scored expert of the groups that
 // stay, in id order; a group without a scored expert comes after all others.  top_k never
 // exceeds the experts of the groups that stay, so the picks are always distinct experts.
+#include <algorithm>
 #include <type_traits>
 
 #include "device_common.h"
 #include "launchers.h"
+#include "tiled_common.h"
 
 namespace moe {
 
@@ -40,6 +42,38 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
 #undef MOE_DPP_MAX
   return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
+
+// The same for floats: largest, sum, and each lane's largest of the lanes below it.
+#define MOE_DPP_F32(v, old, ctrl, rows)                                                       \
+  __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp((int)__float_as_uint(old),            \
+                                                        (int)__float_as_uint(v), ctrl, rows, \
+                                                        0xf, false))
+__device__ __forceinline__ float scan_max_f32(float v) {
+  v = fmaxf(v, MOE_DPP_F32(v, -INFINITY, 0x111, 0xf));
+  v = fmaxf(v, MOE_DPP_F32(v, -INFINITY, 0x112, 0xf));
+  v = fmaxf(v, MOE_DPP_F32(v, -INFINITY, 0x114, 0xf));
+  v = fmaxf(v, MOE_DPP_F32(v, -INFINITY, 0x118, 0xf));
+  v = fmaxf(v, MOE_DPP_F32(v, -INFINITY, 0x142, 0xa));
+  v = fmaxf(v, MOE_DPP_F32(v, -INFINITY, 0x143, 0xc));
+  return v;   // largest of the lanes up to this one
+}
+__device__ __forceinline__ float lane63(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
+__device__ __forceinline__ float wave_max_f32(float v) { return lane63(scan_max_f32(v)); }
+__device__ __forceinline__ float below_max_f32(float v) {
+  return scan_max_f32(MOE_DPP_F32(v, -INFINITY, 0x138, 0xf));   // wave_shr 1
+}
+__device__ __forceinline__ float wave_sum_f32(float v) {
+  v += MOE_DPP_F32(v, 0.0f, 0x111, 0xf);
+  v += MOE_DPP_F32(v, 0.0f, 0x112, 0xf);
+  v += MOE_DPP_F32(v, 0.0f, 0x114, 0xf);
+  v += MOE_DPP_F32(v, 0.0f, 0x118, 0xf);
+  v += MOE_DPP_F32(v, 0.0f, 0x142, 0xa);
+  v += MOE_DPP_F32(v, 0.0f, 0x143, 0xc);
+  return lane63(v);
+}
+#undef MOE_DPP_F32
 
 __device__ __forceinline__ double wave_max_f64(double v) {
 #pragma unroll
@@ -79,8 +113,140 @@ __device__ __forceinline__ int wave_best(uint64_t key, int slot, int lane) {
   return __ffsll((unsigned long long)who) - 1;
 }
 
+// fp32 logits with a bound, for many tokens.
+//
+// bf16 products are exact in fp32, so only the sums round: a product passes at most 31
+// roundings inside its 32-wide MFMA, one for each of the 8 MFMAs of a 256-wide piece of K,
+// whose sum then goes to fp64, and one more when a part's logit is stored in fp32: 40
+// roundings of at most 2^-23 of A = sum |x| |w| over the part (2^-24, doubled in case the
+// hardware truncates).  A comes from the same fragments with the sign bits cleared; its own
+// roundings are within 2^-10 of it.  (One running fp32 sum over the part: 88 to 144 roundings
+// and three times as many choices that the bound leaves open.)
+//
+// 64 tokens x 64 experts x one part of K per workgroup, 2 x 2 waves of 32 x 32; 64-wide chunks
+// (one 128-byte line per row) by direct copies into a 4-stage LDS ring, two workgroups per
+// CU.  The expert tiles of a token tile run on one XCD and share its rows through the L2.
+constexpr int kBlTile = 64, kBlStages = 4, kBlMaxParts = 4, kBlRounds = 40;
+static_assert(2 * kBlMaxParts * sizeof(float) <= kRouteScratchPerPair &&
+                  sizeof(double) <= kRouteScratchPerPair,
+              "router scratch per (token, expert)");
+
+__global__ __launch_bounds__(256) void bounded_logits_kernel(
+    const uint16_t* __restrict__ x, const uint16_t* __restrict__ wr, int M, int H, int E, int parts,
+    int kpart, int per_xcd, float* __restrict__ logits, float* __restrict__ absdot) {
+  constexpr int STAGE = 2 * kBlTile * 128, PPW = 4;
+  __shared__ __align__(16) unsigned char lds[kBlStages * STAGE];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int li = lane & 15, lg = lane >> 4, rr = lane >> 3;
+  const int etiles = (E + kBlTile - 1) / kBlTile, ttiles = (M + kBlTile - 1) / kBlTile;
+  const int slot = blockIdx.x / kXcds, item = (blockIdx.x % kXcds) * per_xcd + slot;
+  if (slot >= per_xcd || item >= etiles * ttiles * parts) return;
+  const int e0 = item % etiles * kBlTile;
+  const int part = item / etiles % parts, t0 = item / (etiles * parts) * kBlTile;
+  const int kbeg = min(H, part * kpart), klen = min(H, kbeg + kpart) - kbeg;
+
+  // LDS rows 0 .. 63 tokens, 64 .. 127 experts; slot q of row r holds part q ^ (r / 2) % 8.
+  // Rows past the last repeat it and are never stored.
+  const uint16_t* src[PPW];
+  int koff[PPW];
+#pragma unroll
+  for (int i = 0; i < PPW; ++i) {
+    const int r = (wave * PPW + i) * 8 + rr;
+    koff[i] = 8 * ((lane & 7) ^ ((r >> 1) & 7));
+    src[i] = (r < kBlTile ? x + (size_t)min(t0 + r, M - 1) * H
+                          : wr + (size_t)min(e0 + r - kBlTile, E - 1) * H) + kbeg + koff[i];
+  }
+  const int nch = (klen + 63) / 64, ndma = klen / 64;
+  auto issue = [&](int c) {
+    unsigned char* base = lds + (c % kBlStages) * STAGE + wave * PPW * 1024;
+    if (c < ndma) {
+#pragma unroll
+      for (int i = 0; i < PPW; ++i)
+        __builtin_amdgcn_global_load_lds((global_void*)(src[i] + c * 64),
+                                         (lds_void*)(base + i * 1024), 16, 0, 0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < PPW; ++i)
+        *reinterpret_cast<u32x4*>(base + i * 1024 + lane * 16) =
+            c * 64 + koff[i] < klen ? ld16(src[i] + c * 64) : u32x4{0, 0, 0, 0};
+    }
+  };
+  const int trow = 32 * (wave & 1), erow = kBlTile + 32 * (wave >> 1);
+  auto frag = [&](int c, int row, int ks) {
+    return *reinterpret_cast<const u32x4*>(lds + (c % kBlStages) * STAGE + (row + li) * 128 +
+                                           (((lg + 4 * ks) ^ (li >> 1)) * 16));
+  };
+  const u32x4 mag = u32x4{0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu};
+  f32x4 acc[2][2], aab[2][2];   // [expert tile][token tile]
+  double sum[2][2][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      acc[i][j] = aab[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sum[i][j][q] = 0.0;
+    }
+  auto flush = [&] {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sum[i][j][q] += (double)acc[i][j][q];
+        acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+  };
+#pragma unroll
+  for (int c = 0; c < kBlStages - 1; ++c)
+    if (c < nch) issue(c);
+  for (int c = 0; c < nch; ++c) {
+    const int after = c < ndma ? min(kBlStages - 2, ndma - 1 - c) : 0;
+    if (after >= 2) wait_vmcnt<2 * PPW>();
+    else if (after == 1) wait_vmcnt<PPW>();
+    else wait_vmcnt<0>();
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (c + kBlStages - 1 < nch) issue(c + kBlStages - 1);
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      u32x4 xf[2], wf[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        xf[j] = frag(c, trow + 16 * j, ks);
+        wf[j] = frag(c, erow + 16 * j, ks);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          acc[i][j] = mfma16x16x32(wf[i], xf[j], acc[i][j]);
+          aab[i][j] = mfma16x16x32(wf[i] & mag, xf[j] & mag, aab[i][j]);
+        }
+    }
+    if ((c & 3) == 3) flush();
+  }
+  flush();
+  // lane (li, lg): token li of a tile, experts 4 lg .. 4 lg + 3
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int t = t0 + trow + 16 * j + li;
+    if (t >= M) continue;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int e = e0 + (erow - kBlTile) + 16 * i + 4 * lg;
+      const size_t o = ((size_t)part * M + t) * E + e;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (e + q < E) {
+          logits[o + q] = (float)sum[i][j][q];
+          absdot[o + q] = aab[i][j][q];
+        }
+    }
+  }
+}
+
 // Logits of a token: fp64 keys, the caller's fp32 logits, or fp32 MFMA partial logits with
-// their |x| . |w| sums (router_logits_mfma_kernel), which bound their error.
+// their |x| . |w| sums (bounded_logits_kernel), which bound their error.
 struct KeySource {
   const double* keys;
   int64_t ld;
@@ -110,7 +276,8 @@ struct BoundedSource {
       l += (double)logits[((int64_t)p * M + t) * ld + e];
       a += (double)absdot[((int64_t)p * M + t) * ld + e];
     }
-    d = a * rel + fabs(l) * 0x1p-50 + (double)H * 0x1p-126 + 1e-300;
+    // (subnormal products may be flushed: H times the smallest normal number)
+    d = a * rel + (double)H * 0x1p-126;
   }
 };
 
@@ -122,24 +289,314 @@ __device__ __forceinline__ void exact_logits(const BoundedSource& q, int64_t t, 
   const uint16_t* w0 = q.wr + (size_t)e0 * q.H;
   const uint16_t* w1 = q.wr + (size_t)e1 * q.H;
   double a0 = 0.0, a1 = 0.0;
-  for (int c = lane; c < (q.H >> 3); c += kWave) {
-    const u32x4 xv = ld16(xr + (size_t)c * 8), v0 = ld16(w0 + (size_t)c * 8), v1 = ld16(w1 + (size_t)c * 8);
+  constexpr int B = 7;   // chunks of 8 values a lane in flight per row (H = 7168: two rounds)
+  const int n = q.H >> 3;
+  for (int c0 = lane; c0 < n; c0 += kWave * B) {
+    u32x4 xv[B], v0[B], v1[B];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const double lo = bf16lo(xv[j]), hi = bf16hi(xv[j]);
-      a0 = fma(lo, (double)bf16lo(v0[j]), a0);
-      a0 = fma(hi, (double)bf16hi(v0[j]), a0);
-      a1 = fma(lo, (double)bf16lo(v1[j]), a1);
-      a1 = fma(hi, (double)bf16hi(v1[j]), a1);
+    for (int i = 0; i < B; ++i) {
+      const int c = c0 + kWave * i;
+      const size_t o = (size_t)(c < n ? c : 0) * 8;
+      xv[i] = c < n ? ld16(xr + o) : u32x4{0, 0, 0, 0};
+      v0[i] = c < n ? ld16(w0 + o) : u32x4{0, 0, 0, 0};
+      v1[i] = c < n ? ld16(w1 + o) : u32x4{0, 0, 0, 0};
     }
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const double lo = bf16lo(xv[i][j]), hi = bf16hi(xv[i][j]);
+        a0 = fma(lo, (double)bf16lo(v0[i][j]), a0);
+        a0 = fma(hi, (double)bf16hi(v0[i][j]), a0);
+        a1 = fma(lo, (double)bf16lo(v1[i][j]), a1);
+        a1 = fma(hi, (double)bf16hi(v1[i][j]), a1);
+      }
   }
   l0 = wave_sum(a0);
   l1 = wave_sum(a1);
 }
 
-// LDS of a wave: c of E experts (and its bound), the picks' scores (values, bounds) and ids.
+// The picks of a token by fp32 values with bounds, if no bound can turn a choice: kDone.
+// Otherwise nothing is written: kRedo with the experts (bit s of `redo`: this lane's in slot
+// s) whose exact logits can settle it, or kOpen, and the fp64 code below decides.  Each
+// value's bound covers its logit's (|l - exact| <= d, and l's rounding to fp32) and the fp32
+// arithmetic: __expf of z is within (|z| + 4) 2^-22 of itself, reciprocals and products
+// within a few 2^-24.
+//
+// Top-k without rounds: the k-th largest of the 64 lanes' largest keys is a lower limit of the
+// k-th largest of all; the keys that reach it (k and a few) are collected, one per lane, and
+// ranked by counting.  (A round of a k-step selection costs 500 cycles: M=8192, E=384, k=8
+// 22 us.)
+enum Fast { kDone, kRedo, kOpen };
+template <int SL>
+__device__ __forceinline__ Fast select_fast(const double (&l)[SL], const double (&d)[SL],
+                                            bool bounded, const float* bias, int64_t t, int E,
+                                            int top_k, const GroupRule& rule, float* s_v, float* s_d,
+                                            uint32_t* s_key, int* s_id, int lane, uint32_t& redo,
+                                            int32_t* ids, float* weights) {
+  constexpr float u = 0x1p-22f;
+  float v[SL], dv[SL], b[SL];
+  uint32_t live = 0;
+  bool odd = false;   // a logit or bound that fp32 does not hold
+#pragma unroll
+  for (int s = 0; s < SL; ++s) {
+    const int e = lane + kWave * s;
+    b[s] = bias && e < E ? bias[e] : 0.0f;
+  }
+#pragma unroll
+  for (int s = 0; s < SL; ++s) {
+    v[s] = (float)l[s];
+    dv[s] = (float)d[s] * 1.001f + fabsf(v[s]) * u;
+    const bool has = l[s] > -INFINITY;
+    live |= (uint32_t)has << s;
+    // (given logits may mask experts; bounded ones that are not finite may be due to fp32)
+    odd |= (has || (bounded && lane + kWave * s < E)) && !(fabsf(v[s]) < 1e30f && dv[s] <= 0.25f);
+    if (!has) v[s] = dv[s] = 0.0f;
+  }
+  if (__any(odd)) return kOpen;
+  float c[SL], dc[SL];
+  // scores only where something but the picks' weights needs them
+  const bool by_group = rule.n_group > 1 && rule.topk_group < rule.n_group;
+  float top = -INFINITY;
+  if (rule.softmax) {
+#pragma unroll
+    for (int s = 0; s < SL; ++s)
+      if (live >> s & 1) top = fmaxf(top, v[s]);
+    top = wave_max_f32(top);
+  }
+  if (bias || by_group) {
+    if (rule.softmax) {
+      float total = 0.0f;
+#pragma unroll
+      for (int s = 0; s < SL; ++s) {
+        const float z = v[s] - top;
+        c[s] = live >> s & 1 ? __expf(z) : 0.0f;
+        dc[s] = c[s] * (1.2f * dv[s] + (4.0f - z) * u);
+        total += c[s];
+      }
+      if (bias) {
+        total = wave_sum_f32(total);
+        const float inv = total > 0.0f ? __builtin_amdgcn_rcpf(total) : 0.0f;
+#pragma unroll
+        for (int s = 0; s < SL; ++s) {   // (given logits only: the divisor has no bound else)
+          c[s] *= inv;
+          dc[s] = dc[s] * inv + c[s] * (80.0f * u);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < SL; ++s) {
+        const float ex = __expf(-fmaxf(v[s], -80.0f));
+        const float sc = __builtin_amdgcn_rcpf(1.0f + ex);
+        c[s] = live >> s & 1 ? sc : 0.0f;
+        dc[s] = c[s] * (fminf(1.0f, ex * sc) * (1.2f * dv[s] + (fabsf(v[s]) + 4.0f) * u) + 2.0f * u);
+        if (v[s] < -79.0f) dc[s] += 1e-34f;
+      }
+    }
+    if (bias) {
+#pragma unroll
+      for (int s = 0; s < SL; ++s) {
+        c[s] += b[s];
+        dc[s] += fabsf(c[s]) * u + 1e-37f;
+        if ((live >> s & 1) && !(fabsf(c[s]) < 1e30f)) odd = true;
+      }
+      if (__any(odd)) return kOpen;
+    }
+  }
+  uint64_t stay = ~0ull;
+  auto group_of = [&](int e) { return (int)((uint32_t)e * rule.per_magic >> 20); };
+  if (by_group) {
+#pragma unroll
+    for (int s = 0; s < SL; ++s) {
+      const int e = lane + kWave * s;
+      if (e < E) {
+        s_v[e] = live >> s & 1 ? c[s] : -INFINITY;
+        s_d[e] = live >> s & 1 ? dc[s] : 0.0f;
+      }
+    }
+    wave_lds_fence();
+    // span lanes (a power of two) join a group's two best values, upper and lower ends
+    int span = 1, log = 0;
+    while (span * 2 * rule.n_group <= kWave) {
+      span *= 2;
+      ++log;
+    }
+    const int g = lane >> log, sub = lane & (span - 1);
+    float h1 = -INFINITY, h2 = -INFINITY, w1 = -INFINITY, w2 = -INFINITY;
+    auto join = [](float& p1, float& p2, float o1, float o2) {
+      p2 = fmaxf(fminf(p1, o1), fmaxf(p2, o2));
+      p1 = fmaxf(p1, o1);
+    };
+    if (g < rule.n_group)
+      for (int j = sub; j < rule.per; j += span) {
+        const float x = s_v[g * rule.per + j], dx = s_d[g * rule.per + j];
+        join(h1, h2, x + dx, -INFINITY);
+        join(w1, w2, x - dx, -INFINITY);
+      }
+    for (int off = 1; off < span; off <<= 1) {
+      join(h1, h2, __shfl_xor(h1, off, kWave), __shfl_xor(h2, off, kWave));
+      join(w1, w2, __shfl_xor(w1, off, kWave), __shfl_xor(w2, off, kWave));
+    }
+    const bool two = rule.group_top == 2;
+    // (outwards by the sums' rounding)
+    float most = two && h2 > -INFINITY ? h1 + h2 : h1, least = two && w2 > -INFINITY ? w1 + w2 : w1;
+    if (most > -INFINITY) most += fabsf(most) * u;
+    if (least > -INFINITY) least -= fabsf(least) * u;
+    wave_lds_fence();
+    if (sub == 0 && g < rule.n_group) {
+      s_v[g] = most;
+      s_d[g] = least;
+    }
+    wave_lds_fence();
+    // a group stays if fewer than topk_group others can reach it; the rest must be out of reach
+    const bool mine = lane < rule.n_group;
+    const float my_least = mine ? s_d[lane] : INFINITY, my_most = mine ? s_v[lane] : -INFINITY;
+    int ahead = 0, open = 0;   // groups certainly above this one, and those that may be
+    for (int j = 0; j < rule.n_group; ++j) {
+      ahead += s_d[j] > my_most ? 1 : 0;
+      open += s_v[j] >= my_least && j != lane ? 1 : 0;
+    }
+    const bool in = mine && open < rule.topk_group, out = mine && ahead >= rule.topk_group;
+    if (__any(mine && !in && !out)) {
+      // what can make an open group's score: values that reach its group_top-th lower end
+      wave_lds_fence();
+      if (sub == 0 && g < rule.n_group) s_v[g] = two ? w2 : w1;
+      if (mine) s_d[lane] = !in && !out ? 1.0f : 0.0f;
+      wave_lds_fence();
+#pragma unroll
+      for (int s = 0; s < SL; ++s) {
+        const int e = lane + kWave * s;
+        if (e < E && (live >> s & 1) && d[s] > 0.0) {
+          const int ge = group_of(e);
+          if (s_d[ge] != 0.0f && c[s] + dc[s] >= s_v[ge]) redo |= 1u << s;
+        }
+      }
+      return __any(redo != 0) ? kRedo : kOpen;
+    }
+    stay = __ballot(in);
+    wave_lds_fence();
+  }
+  if (bias) {
+#pragma unroll
+    for (int s = 0; s < SL; ++s) {
+      v[s] = c[s];
+      dv[s] = dc[s];
+    }
+  }
+  uint32_t key[SL];
+#pragma unroll
+  for (int s = 0; s < SL; ++s) {
+    const int e = lane + kWave * s;
+    const bool is = (live >> s & 1) && (!by_group || (stay >> group_of(e) & 1));
+    const uint32_t bits = __float_as_uint(v[s] + 0.0f);
+    key[s] = is ? ((int)bits < 0 ? ~bits : bits | 0x80000000u) : 0u;
+    if (e < E) {
+      s_v[e] = v[s];
+      s_d[e] = dv[s];
+    }
+  }
+  // limit: the largest key that at least top_k lanes' largest keys reach
+  uint32_t largest = key[0];
+#pragma unroll
+  for (int s = 1; s < SL; ++s) largest = max(largest, key[s]);
+  uint32_t limit = 1u;
+  if (SL > 1) {
+    s_key[lane] = largest;
+    wave_lds_fence();
+    int reached = 0;
+#pragma unroll
+    for (int j = 0; j < kWave; j += 4) {
+      const uint4 o = *reinterpret_cast<const uint4*>(s_key + j);
+      reached += (o.x >= largest) + (o.y >= largest) + (o.z >= largest) + (o.w >= largest);
+    }
+    limit = max(wave_max_u32(reached >= top_k ? largest : 0u), 1u);
+    wave_lds_fence();
+  }
+  // candidates, one per lane, in slot and lane order
+  int found = 0;
+#pragma unroll
+  for (int s = 0; s < SL; ++s) {
+    const bool is = key[s] >= limit;
+    const uint64_t who = __ballot(is);
+    const int at = found + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32),
+                                                     __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+    found += __popcll(who);
+    if (is && at < kWave) {
+      s_key[at] = key[s];
+      s_id[at] = lane + kWave * s;
+    }
+  }
+  if (found < top_k || found > kWave) return kOpen;   // too few scored experts, or many alike
+  if (lane >= found) s_key[lane] = 0u;
+  wave_lds_fence();
+  const uint32_t my_key = s_key[lane];
+  const int my_id = lane < found ? s_id[lane] : 0;
+  int rank = 0;
+  for (int j = 0; j < found; j += 4) {   // (equal keys share a rank: the check below fails)
+    const uint4 o = *reinterpret_cast<const uint4*>(s_key + j);
+    rank += (o.x > my_key) + (o.y > my_key) + (o.z > my_key) + (o.w > my_key);
+  }
+  const float my_v = s_v[my_id], my_d = s_d[my_id];
+  wave_lds_fence();
+  const bool ahead = lane < found && rank < top_k;
+  s_id[lane] = -1;
+  wave_lds_fence();
+  if (ahead) s_id[rank] = my_id;
+  wave_lds_fence();
+  // What is not picked reaches no further than `reach` (of equal keys one is picked); pick r,
+  // held by lane 63 - r, has to be above that and above every pick behind it.
+  float reach = -INFINITY;
+#pragma unroll
+  for (int s = 0; s < SL; ++s)
+    if (key[s] && key[s] < limit) reach = fmaxf(reach, v[s] + dv[s]);
+  if (lane < found && !(ahead && s_id[rank] == my_id)) reach = fmaxf(reach, my_v + my_d);
+  reach = wave_max_f32(reach);
+  const int r = kWave - 1 - lane;
+  const int id = r < top_k ? max(s_id[r], 0) : 0;
+  const bool mine = r < top_k && s_id[r] >= 0;
+  const float pv = s_v[id], pd = s_d[id];
+  const float behind = fmaxf(reach, below_max_f32(mine ? pv + pd : -INFINITY));
+  const bool weak = mine && !(pv - pd > behind);
+  if (__any(weak)) {   // the logits whose values meet the hull of the picks that do not stand
+    const float high = wave_max_f32(weak ? pv + pd : -INFINITY);
+    const float low = -wave_max_f32(weak ? pd - pv : -INFINITY);
+#pragma unroll
+    for (int s = 0; s < SL; ++s)
+      if (key[s] && d[s] > 0.0 && v[s] + dv[s] >= low && v[s] - dv[s] <= high) redo |= 1u << s;
+    return __any(redo != 0) ? kRedo : kOpen;
+  }
+  // weights from the picks' logits in fp64
+  double lp = 0.0;
+#pragma unroll
+  for (int s = 0; s < SL; ++s) {
+    const double o = __shfl(l[s], id & 63, kWave);
+    if ((id >> 6) == s) lp = o;
+  }
+  const double w = mine ? (rule.softmax ? exp(lp - (double)top) : 1.0 / (1.0 + exp(-lp))) : 0.0;
+  double divisor = 1.0;
+  if (rule.renorm) {
+    divisor = wave_sum(w);
+  } else if (rule.softmax) {
+    double total = 0.0;
+#pragma unroll
+    for (int s = 0; s < SL; ++s)
+      if (live >> s & 1) total += exp(l[s] - (double)top);
+    divisor = wave_sum(total);
+  }
+  const double factor = divisor > 0.0 ? (double)rule.scale / divisor : 0.0;
+  if (mine) {
+    ids[t * top_k + r] = id;
+    weights[t * top_k + r] = (float)(w * factor);
+  }
+  return kDone;
+}
+
+// LDS of a wave, in doubles: c of E experts (and its bound), the picks' scores (values, bounds)
+// and ids (room for 64), 64 keys; a multiple of 16 bytes, as are the parts before the ids.
 __host__ __device__ constexpr int select_lds_doubles(bool bounds, int E, int top_k) {
-  return bounds ? 2 * E + 3 * top_k + (top_k + 1) / 2 : E + top_k + (top_k + 1) / 2;
+  const int even_E = (E + 1) / 2 * 2, even_k = (top_k + 1) / 2 * 2;
+  const int ids = ((top_k > 64 ? top_k : 64) + 3) / 4 * 2;
+  return (bounds ? 2 * even_E + 3 * even_k : even_E + even_k) + ids + 32;
 }
 
 // One wave per token; lane l owns experts l, l + 64, ... (SL of them).
@@ -155,16 +612,18 @@ __global__ __launch_bounds__(kSelWaves* kWave) void select_groups_kernel(
     SRC src, const float* __restrict__ bias, int M, int E, int top_k, GroupRule rule,
     int32_t* __restrict__ ids, float* __restrict__ weights) {
   constexpr bool BOUNDS = std::is_same<SRC, BoundedSource>::value;
-  extern __shared__ double sel_lds[];
+  extern __shared__ __align__(16) double sel_lds[];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t t = (int64_t)blockIdx.x * kSelWaves + wave;
   if (t >= M) return;
   double* s_c = sel_lds + (size_t)wave * select_lds_doubles(BOUNDS, E, top_k);
-  double* s_d = s_c + E;                                   // BOUNDS
-  double* s_pick = s_c + (BOUNDS ? 2 : 1) * E;
-  double* s_pv = s_pick + top_k;                           // BOUNDS: the picks' values
-  double* s_pd = s_pv + top_k;                             // BOUNDS: and their bounds
-  int* s_id = reinterpret_cast<int*>(s_pick + (BOUNDS ? 3 : 1) * top_k);   // and the picks
+  const int even_E = (E + 1) / 2 * 2, even_k = (top_k + 1) / 2 * 2;
+  double* s_d = s_c + even_E;                              // BOUNDS
+  double* s_pick = s_c + (BOUNDS ? 2 : 1) * even_E;
+  double* s_pv = s_pick + even_k;                          // BOUNDS: the picks' values
+  double* s_pd = s_pv + even_k;                            // BOUNDS: and their bounds
+  int* s_id = reinterpret_cast<int*>(s_pick + (BOUNDS ? 3 : 1) * even_k);   // and the picks
+  uint32_t* s_key = reinterpret_cast<uint32_t*>(s_id + (max(top_k, kWave) + 3) / 4 * 4);
 
   double l[SL], d[SL];
   uint32_t redo = 0;   // bit s: this lane's expert in slot s gets its exact logit
@@ -176,12 +635,11 @@ __global__ __launch_bounds__(kSelWaves* kWave) void select_groups_kernel(
     if (e < E) src.get(t, e, l[s], d[s]);
     if (BOUNDS && !(d[s] <= 0.25)) redo |= 1u << s;        // too wide, or not a number
   }
-
-  for (;;) {
+  auto make_exact = [&](uint32_t mask) {
     if constexpr (BOUNDS) {
 #pragma unroll
       for (int s = 0; s < SL; ++s) {
-        uint64_t todo = __ballot((redo >> s) & 1);
+        uint64_t todo = __ballot((mask >> s) & 1);
         while (todo) {
           const int a = __ffsll((unsigned long long)todo) - 1;
           todo &= todo - 1;
@@ -195,8 +653,26 @@ __global__ __launch_bounds__(kSelWaves* kWave) void select_groups_kernel(
           }
         }
       }
+    }
+  };
+  make_exact(redo);
+  redo = 0;
+  if (top_k <= kWave) {
+    Fast got;
+    while ((got = select_fast<SL>(l, d, BOUNDS, bias, t, E, top_k, rule,
+                                  reinterpret_cast<float*>(s_c), reinterpret_cast<float*>(s_c) + E,
+                                  s_key, s_id, lane, redo, ids, weights)) == kRedo) {
+      wave_lds_fence();
+      make_exact(redo);   // at least one logit: this ends
       redo = 0;
     }
+    if (got == kDone) return;
+  }
+  wave_lds_fence();
+
+  for (;;) {
+    make_exact(redo);
+    redo = 0;
     // scores (softmax with bounds: without the divisor, which is applied at the end)
     double score[SL], c[SL], dc[SL], divisor = 1.0;
     bool live[SL];
@@ -447,18 +923,30 @@ hipError_t launch_route_groups(const uint16_t* x, const uint16_t* wr, const floa
                                int H, int E, int top_k, const GroupRule& rule, int32_t* ids,
                                float* w, void* scratch, hipStream_t s) {
   if (M >= kBoundedMinTokens && E <= kBoundedMaxExperts && top_k <= 64 && !(rule.softmax && bias)) {
-    int parts = 0, nround = 0;
+    // K in parts (of whole 256-wide pieces) so that about 512 workgroups run
+    const int64_t tiles = (int64_t)((E + kBlTile - 1) / kBlTile) * ((M + kBlTile - 1) / kBlTile);
+    const int pieces = (H + 255) / 256;
+    int parts = (int)std::min<int64_t>({kBlMaxParts, pieces, std::max<int64_t>(1, (512 + tiles - 1) / tiles)});
+    const int kpart = (pieces + parts - 1) / parts * 256;
+    parts = (H + kpart - 1) / kpart;
+    const int per_xcd = (int)((tiles * parts + kXcds - 1) / kXcds);
     float* logits = static_cast<float*>(scratch);
-    float* absdot = nullptr;
-    const hipError_t err = launch_router_logits(x, wr, M, H, E, logits, &absdot, &parts, &nround, s);
+    float* absdot = logits + (size_t)parts * M * E;
+    hipLaunchKernelGGL(bounded_logits_kernel, dim3((unsigned)per_xcd * kXcds), dim3(256), 0, s, x,
+                       wr, M, H, E, parts, kpart, per_xcd, logits, absdot);
+    const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    const double rel = (double)nround * 0x1p-23 * (1.0 + 0x1p-9);
+    const double rel = kBlRounds * 0x1p-23 * (1.0 + 0x1p-9);
     return launch_select(BoundedSource{logits, absdot, x, wr, parts, M, H, rel, E}, bias, M, E,
                          top_k, rule, ids, w, s);
   }
   double* keys = static_cast<double*>(scratch);
-  const hipError_t err = launch_router_keys(x, wr, M, H, E, keys, s);
-  if (err != hipSuccess) return err;
+  constexpr int kMost = 1 << 17;   // tokens of one launch (its grid has them in y)
+  for (int t0 = 0; t0 < M; t0 += kMost) {
+    const hipError_t err = launch_router_keys(x + (size_t)t0 * H, wr, std::min(kMost, M - t0), H, E,
+                                              keys + (size_t)t0 * E, s);
+    if (err != hipSuccess) return err;
+  }
   return launch_select(KeySource{keys, E}, bias, M, E, top_k, rule, ids, w, s);
 }
 
