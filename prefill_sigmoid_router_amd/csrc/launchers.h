@@ -29,8 +29,9 @@ struct GroupRule {
   int renorm;       // weights divided by their sum over the picks
   float scale;
 };
-// From hidden states (scratch of kRouteScratchPerPair bytes per (token, expert)), or from
-// fp32 logits with a row stride of ld values.
+// From hidden states (16-byte aligned scratch of route_groups_scratch_bytes), or from fp32
+// logits with a row stride of ld values.
+size_t route_groups_scratch_bytes(int M, int E);
 hipError_t launch_route_groups(const uint16_t* x, const uint16_t* wr, const float* bias, int M,
                                int H, int E, int top_k, const GroupRule& rule, int32_t* ids,
                                float* w, void* scratch, hipStream_t s);

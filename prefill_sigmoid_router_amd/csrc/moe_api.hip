@@ -701,7 +701,7 @@ bool make_rule(int32_t E, int32_t top_k, int32_t score, int32_t n_group, int32_t
 // the int8 act with their scales.
 struct I8Layout {
   Layout base;
-  size_t xq, xs, am, ae, as, total;   // the codes of act take the place of its bf16
+  size_t keys, xq, xs, am, ae, as, total;   // the codes of act take the place of its bf16
 };
 
 I8Layout i8_layout_of(int32_t M, int32_t H, int32_t E, int32_t I, int32_t top_k, int32_t block) {
@@ -710,6 +710,7 @@ I8Layout i8_layout_of(int32_t M, int32_t H, int32_t E, int32_t I, int32_t top_k,
   const size_t cap = capacity_of(M, top_k, E, block);
   const size_t blocks = ((size_t)I + 127) / 128;
   size_t off = round_up(L.base.total, kAlign);
+  L.keys = off;  off += round_up(moe::route_groups_scratch_bytes(M, E), kAlign);
   L.xq = off;  off += round_up((size_t)M * H, kAlign);
   L.xs = off;  off += round_up((size_t)M * sizeof(float), kAlign);
   L.am = off;  off += round_up(cap * blocks * 128 * sizeof(int16_t), kAlign);
@@ -734,7 +735,8 @@ int i8_tile_rows(int32_t M, int32_t E, int32_t top_k) {
 extern "C" {
 
 size_t moe_route_groups_workspace_bytes(int32_t M, int32_t E) {
-  return moe_route_workspace_bytes(M, E);
+  if (M < 0 || M > kMaxRouteTokens || E < 1 || E > kMaxE) return 0;
+  return round_up(moe::route_groups_scratch_bytes(M, E), kAlign) + kAlign;
 }
 
 int moe_route_groups(const uint16_t* x, const uint16_t* router_w, const float* select_bias,
@@ -874,7 +876,7 @@ int moe_forward_i8(const uint16_t* x, const uint16_t* router_w, const float* sel
     return !stage_events || hipEventRecord((hipEvent_t)stage_events[i], s) == hipSuccess;
   };
   if (!mark(0)) return MOE_ERR_HIP;
-  if (moe::launch_route_groups(x, router_w, select_bias, M, H, E, top_k, rule, ids, w, ws + B.keys,
+  if (moe::launch_route_groups(x, router_w, select_bias, M, H, E, top_k, rule, ids, w, ws + L.keys,
                                s) != hipSuccess ||
       moe::launch_i8_rows(x, M, H, xq, xs, s) != hipSuccess)
     return MOE_ERR_HIP;

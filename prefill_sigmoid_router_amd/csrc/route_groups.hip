@@ -126,12 +126,9 @@ __device__ __forceinline__ int wave_best(uint64_t key, int slot, int lane) {
 // 64 tokens x 64 experts x one part of K per workgroup, 2 x 2 waves of 32 x 32; 64-wide chunks
 // (one 128-byte line per row) by direct copies into a 4-stage LDS ring, two workgroups per
 // CU.  The expert tiles of a token tile run on one XCD and share its rows through the L2.
-constexpr int kBlTile = 64, kBlStages = 4, kBlMaxParts = 4, kBlRounds = 40;
-static_assert(2 * kBlMaxParts * sizeof(float) <= kRouteScratchPerPair &&
-                  sizeof(double) <= kRouteScratchPerPair,
-              "router scratch per (token, expert)");
+constexpr int kBlTile = 64, kBlStages = 4, kBlRounds = 40;
 
-__global__ __launch_bounds__(256) void bounded_logits_kernel(
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void bounded_logits_kernel(
     const uint16_t* __restrict__ x, const uint16_t* __restrict__ wr, int M, int H, int E, int parts,
     int kpart, int per_xcd, float* __restrict__ logits, float* __restrict__ absdot) {
   constexpr int STAGE = 2 * kBlTile * 128, PPW = 4;
@@ -197,10 +194,7 @@ __global__ __launch_bounds__(256) void bounded_logits_kernel(
         acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
   };
-#pragma unroll
-  for (int c = 0; c < kBlStages - 1; ++c)
-    if (c < nch) issue(c);
-  for (int c = 0; c < nch; ++c) {
+  auto step = [&](int c) {
     const int after = c < ndma ? min(kBlStages - 2, ndma - 1 - c) : 0;
     if (after >= 2) wait_vmcnt<2 * PPW>();
     else if (after == 1) wait_vmcnt<PPW>();
@@ -223,8 +217,17 @@ __global__ __launch_bounds__(256) void bounded_logits_kernel(
           aab[i][j] = mfma16x16x32(wf[i] & mag, xf[j] & mag, aab[i][j]);
         }
     }
-    if ((c & 3) == 3) flush();
+  };
+#pragma unroll
+  for (int c = 0; c < kBlStages - 1; ++c)
+    if (c < nch) issue(c);
+  int c = 0;
+  for (; c + 4 <= nch; c += 4) {   // 256 values of K
+#pragma unroll
+    for (int k = 0; k < 4; ++k) step(c + k);
+    flush();
   }
+  for (; c < nch; ++c) step(c);
   flush();
   // lane (li, lg): token li of a tile, experts 4 lg .. 4 lg + 3
 #pragma unroll
@@ -235,6 +238,14 @@ __global__ __launch_bounds__(256) void bounded_logits_kernel(
     for (int i = 0; i < 2; ++i) {
       const int e = e0 + (erow - kBlTile) + 16 * i + 4 * lg;
       const size_t o = ((size_t)part * M + t) * E + e;
+      if (E % 4 == 0) {
+        if (e < E) {
+          *reinterpret_cast<float4*>(logits + o) =
+              make_float4((float)sum[i][j][0], (float)sum[i][j][1], (float)sum[i][j][2], (float)sum[i][j][3]);
+          *reinterpret_cast<f32x4*>(absdot + o) = aab[i][j];
+        }
+        continue;
+      }
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         if (e + q < E) {
@@ -272,6 +283,7 @@ struct BoundedSource {
   __device__ void get(int64_t t, int e, double& l, double& d) const {
     double a = 0.0;
     l = 0.0;
+#pragma unroll 4
     for (int p = 0; p < parts; ++p) {
       l += (double)logits[((int64_t)p * M + t) * ld + e];
       a += (double)absdot[((int64_t)p * M + t) * ld + e];
@@ -281,40 +293,95 @@ struct BoundedSource {
   }
 };
 
-// fp64 dot products of row t of x with rows e0 and e1 of the router weight, by one wave; the
-// same order for every expert, so that equal rows give equal sums.
-__device__ __forceinline__ void exact_logits(const BoundedSource& q, int64_t t, int e0, int e1,
-                                             int lane, double& l0, double& l1) {
+// Exact logits that the workgroup's waves ask for: fp64 dot products, every wave a quarter of
+// the row, the quarters added in wave order, so that equal rows of the router weight give
+// equal sums.  Each wave leaves up to kAsk pairs a round.
+constexpr int kAsk = 8;
+struct ExactQueue {
+  int expert[kSelWaves][kAsk];   // -1: none
+  double part[kSelWaves][kAsk][kSelWaves];
+};
+
+// One wave's quarter of N dot products of row t of x.
+template <int N>
+__device__ __forceinline__ void quarter_dots(const BoundedSource& q, int64_t t, const int* experts,
+                                             int wave, int lane, double (&sum)[N]) {
   const uint16_t* xr = q.x + t * q.H;
-  const uint16_t* w0 = q.wr + (size_t)e0 * q.H;
-  const uint16_t* w1 = q.wr + (size_t)e1 * q.H;
-  double a0 = 0.0, a1 = 0.0;
-  constexpr int B = 7;   // chunks of 8 values a lane in flight per row (H = 7168: two rounds)
-  const int n = q.H >> 3;
-  for (int c0 = lane; c0 < n; c0 += kWave * B) {
-    u32x4 xv[B], v0[B], v1[B];
+  const uint16_t* w[N];
 #pragma unroll
-    for (int i = 0; i < B; ++i) {
-      const int c = c0 + kWave * i;
-      const size_t o = (size_t)(c < n ? c : 0) * 8;
-      xv[i] = c < n ? ld16(xr + o) : u32x4{0, 0, 0, 0};
-      v0[i] = c < n ? ld16(w0 + o) : u32x4{0, 0, 0, 0};
-      v1[i] = c < n ? ld16(w1 + o) : u32x4{0, 0, 0, 0};
+  for (int i = 0; i < N; ++i) {
+    w[i] = q.wr + (size_t)max(experts[i], 0) * q.H;
+    sum[i] = 0.0;
+  }
+  constexpr int B = 4;   // chunks of 8 values a lane in flight per row: H = 7168 in one batch
+  const int n = q.H >> 3, beg = n * wave / kSelWaves, end = n * (wave + 1) / kSelWaves;
+  for (int c0 = beg + lane; c0 < end; c0 += kWave * B) {
+    u32x4 xv[B], v[N][B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int c = c0 + kWave * b;
+      const bool in = c < end;
+      xv[b] = in ? ld16(xr + (size_t)c * 8) : u32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i][b] = in ? ld16(w[i] + (size_t)c * 8) : u32x4{0, 0, 0, 0};
     }
 #pragma unroll
-    for (int i = 0; i < B; ++i)
+    for (int b = 0; b < B; ++b)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const double lo = bf16lo(xv[i][j]), hi = bf16hi(xv[i][j]);
-        a0 = fma(lo, (double)bf16lo(v0[i][j]), a0);
-        a0 = fma(hi, (double)bf16hi(v0[i][j]), a0);
-        a1 = fma(lo, (double)bf16lo(v1[i][j]), a1);
-        a1 = fma(hi, (double)bf16hi(v1[i][j]), a1);
+        const double lo = bf16lo(xv[b][j]), hi = bf16hi(xv[b][j]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          sum[i] = fma(lo, (double)bf16lo(v[i][b][j]), sum[i]);
+          sum[i] = fma(hi, (double)bf16hi(v[i][b][j]), sum[i]);
+        }
       }
   }
-  l0 = wave_sum(a0);
-  l1 = wave_sum(a1);
+#pragma unroll
+  for (int i = 0; i < N; ++i) sum[i] = wave_sum(sum[i]);
 }
+
+// All waves of the workgroup, together: computes what `redo` asks for (bit s: this lane's
+// expert in slot s) as far as the queue goes and clears those bits.  False if no wave asked.
+template <int SL>
+__device__ __forceinline__ bool exact_round(const BoundedSource& q, ExactQueue& queue, int64_t t0,
+                                            int64_t M, int wave, int lane, uint32_t& redo,
+                                            double (&l)[SL], double (&d)[SL]) {
+  if (lane < kAsk) queue.expert[wave][lane] = -1;
+  wave_lds_fence();
+  int asked = 0;
+  int at[SL];   // this lane's place in the queue for slot s
+#pragma unroll
+  for (int s = 0; s < SL; ++s) {
+    const bool ask = (redo >> s) & 1;
+    const uint64_t who = __ballot(ask);
+    const int place = asked + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32),
+                                                        __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+    at[s] = ask && place < kAsk ? place : -1;
+    if (at[s] >= 0) queue.expert[wave][place] = lane + kWave * s;
+    asked += __popcll(who);
+  }
+  if (!__syncthreads_or(asked)) return false;
+  for (int w = 0; w < kSelWaves; ++w) {
+    const int64_t t = min(t0 + w, M - 1);
+    for (int i = 0; i < kAsk && queue.expert[w][i] >= 0; i += 2) {
+      double sum[2];
+      quarter_dots<2>(q, t, &queue.expert[w][i], wave, lane, sum);
+      if (lane < 2) queue.part[w][i + lane][wave] = lane ? sum[1] : sum[0];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int s = 0; s < SL; ++s)
+    if (at[s] >= 0) {
+      const double* part = queue.part[wave][at[s]];
+      l[s] = ((part[0] + part[1]) + part[2]) + part[3];
+      d[s] = 0.0;
+      redo &= ~(1u << s);
+    }
+  return true;
+}
+static_assert(kSelWaves == 4 && kAsk % 2 == 0, "the sums and pairs above");
 
 // The picks of a token by fp32 values with bounds, if no bound can turn a choice: kDone.
 // Otherwise nothing is written: kRedo with the experts (bit s of `redo`: this lane's in slot
@@ -599,23 +666,238 @@ __host__ __device__ constexpr int select_lds_doubles(bool bounds, int E, int top
   return (bounds ? 2 * even_E + 3 * even_k : even_E + even_k) + ids + 32;
 }
 
-// One wave per token; lane l owns experts l, l + 64, ... (SL of them).
+// The same in fp64: kDone, or (with bounds) kRedo.
 //
 // With bounded logits |l - exact| <= d, every value that a choice compares carries a bound of
 // its own (sigmoid: s (1 - s) (e^d - 1) <= 1.2 d s (1 - s) for d <= 1/4; softmax without its
 // common divisor: 1.2 d e^l), and a choice stands if no bound can turn it.  Where one can,
-// the experts that it hangs on get their exact logits and the token is done again; choices
-// between exact values are exact, so this ends.  At M=2048, E=256 about one token in five
-// comes to two or three exact logits (recomputing every candidate's: seventeen for each).
+// the experts that it hangs on are asked for; choices between exact values are exact, so this
+// ends.
+template <int SL, bool BOUNDS>
+__device__ __forceinline__ Fast select_fp64(const double (&l)[SL], const double (&d)[SL],
+                                            const float* bias, int64_t t, int E, int top_k,
+                                            const GroupRule& rule, double* s_c, double* s_d,
+                                            double* s_pick, double* s_pv, double* s_pd, int* s_id,
+                                            int lane, uint32_t& redo, int32_t* ids,
+                                            float* weights) {
+  // scores (softmax with bounds: without the divisor, which is applied at the end)
+  double score[SL], c[SL], dc[SL], divisor = 1.0;
+  bool live[SL];
+#pragma unroll
+  for (int s = 0; s < SL; ++s) live[s] = l[s] > -INFINITY;
+  if (rule.softmax) {
+    double top = -INFINITY;
+#pragma unroll
+    for (int s = 0; s < SL; ++s)
+      if (live[s]) top = fmax(top, l[s]);
+    top = fmin(wave_max_f64(top), 1.7976931348623157e308);   // +inf counts as the largest number
+    double total = 0.0;
+#pragma unroll
+    for (int s = 0; s < SL; ++s) {
+      score[s] = live[s] ? exp(fmin(l[s], 1.7976931348623157e308) - top) : 0.0;
+      total += score[s];
+      dc[s] = 1.2 * d[s] * score[s];
+    }
+    divisor = wave_sum(total);
+    if (!BOUNDS) {
+#pragma unroll
+      for (int s = 0; s < SL; ++s) score[s] = live[s] ? score[s] / divisor : 0.0;
+      divisor = 1.0;
+    }
+  } else {
+#pragma unroll
+    for (int s = 0; s < SL; ++s) {
+      const double ex = exp(-l[s]);
+      score[s] = live[s] ? 1.0 / (1.0 + ex) : 0.0;
+      dc[s] = d[s] > 0.0 ? 1.2 * d[s] * score[s] * fmin(1.0, ex * score[s]) + 1e-14 : 0.0;
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < SL; ++s) {
+    const int e = lane + kWave * s;
+    c[s] = score[s];
+    if (bias && e < E) c[s] += (double)bias[e];
+    live[s] = live[s] && c[s] > -INFINITY;
+    if (!live[s]) {
+      c[s] = -INFINITY;
+      score[s] = 0.0;
+      dc[s] = 0.0;
+    }
+  }
+
+  uint64_t stay = ~0ull;   // bit g: group g stays
+  if (rule.n_group > 1) {
+#pragma unroll
+    for (int s = 0; s < SL; ++s)
+      if (lane + kWave * s < E) {
+        s_c[lane + kWave * s] = c[s];
+        if (BOUNDS) s_d[lane + kWave * s] = dc[s];
+      }
+    wave_lds_fence();
+    // span lanes (a power of two) read a group's experts and join their two best; lane
+    // g span ends up with group g
+    int span = 1;
+    while (span * 2 * rule.n_group <= kWave) span *= 2;
+    const int g = lane / span, sub = lane % span;
+    const bool mine = g < rule.n_group;
+    double b1 = -INFINITY, b2 = -INFINITY;   // best two c
+    double h1 = -INFINITY, h2 = -INFINITY;   // best two c + dc
+    double w1 = -INFINITY, w2 = -INFINITY;   // best two c - dc
+    auto join = [](double& p1, double& p2, double o1, double o2) {
+      p2 = fmax(fmin(p1, o1), fmax(p2, o2));
+      p1 = fmax(p1, o1);
+    };
+    if (mine)
+      for (int j = sub; j < rule.per; j += span) {
+        const double v = s_c[g * rule.per + j];
+        join(b1, b2, v, -INFINITY);
+        if (BOUNDS) {
+          const double dv = s_d[g * rule.per + j];
+          join(h1, h2, v + dv, -INFINITY);
+          join(w1, w2, v - dv, -INFINITY);
+        }
+      }
+    for (int off = 1; off < span; off <<= 1) {
+      join(b1, b2, __shfl_xor(b1, off, kWave), __shfl_xor(b2, off, kWave));
+      if (BOUNDS) {
+        join(h1, h2, __shfl_xor(h1, off, kWave), __shfl_xor(h2, off, kWave));
+        join(w1, w2, __shfl_xor(w1, off, kWave), __shfl_xor(w2, off, kWave));
+      }
+    }
+    const bool two = rule.group_top == 2;
+    const double total = two && b2 > -INFINITY ? b1 + b2 : b1;
+    int rank = 0;
+    for (int j = 0; j < rule.n_group; ++j) {
+      const double o = __shfl(total, j * span, kWave);
+      rank += (o > total || (o == total && j < g)) ? 1 : 0;
+    }
+    const bool keep = mine && rank < rule.topk_group;
+    const uint64_t kept = __ballot(keep && sub == 0);
+    stay = 0;
+    for (int j = 0; j < rule.n_group; ++j) stay |= ((kept >> (j * span)) & 1) << j;
+    if (BOUNDS && rule.topk_group < rule.n_group) {
+      const double top = two && h2 > -INFINITY ? h1 + h2 : h1;
+      const double low = two && w2 > -INFINITY ? w1 + w2 : w1;
+      const double least = -wave_max_f64(keep ? -low : -INFINITY);
+      const double most = wave_max_f64(mine && !keep ? top : -INFINITY);
+      if (!(least > most)) {   // a group's place is open: exact logits of what makes it
+        const bool open = mine && (keep ? low <= most : top >= least);
+        wave_lds_fence();      // s_c, s_d were read
+        if (sub == 0 && mine) s_c[g] = open ? (two ? w2 : w1) : INFINITY;
+        wave_lds_fence();
+#pragma unroll
+        for (int s = 0; s < SL; ++s) {
+          const int e = lane + kWave * s;
+          if (e < E && d[s] > 0.0 && live[s] && c[s] + dc[s] >= s_c[e / rule.per]) redo |= 1u << s;
+        }
+        wave_lds_fence();
+        if (__any(redo != 0)) return kRedo;
+      }
+    }
+  }
+
+  uint64_t key[SL];
+  double v[SL], dv[SL];   // what orders the picks, and its bound
+#pragma unroll
+  for (int s = 0; s < SL; ++s) {
+    const int e = lane + kWave * s;
+    v[s] = bias ? c[s] : l[s];
+    dv[s] = bias ? dc[s] : d[s];
+    key[s] = kKeyOutside;
+    if (e < E && ((stay >> (e / rule.per)) & 1)) key[s] = live[s] ? order_key(v[s]) : kKeyUnscored;
+  }
+  uint32_t inside = 0, taken = 0;
+#pragma unroll
+  for (int s = 0; s < SL; ++s) inside |= (uint32_t)(key[s] > kKeyUnscored) << s;
+  for (int r = 0; r < top_k; ++r) {
+    uint64_t best = key[0];
+    int slot = 0;
+#pragma unroll
+    for (int s = 1; s < SL; ++s)
+      if (key[s] > best) {
+        best = key[s];
+        slot = s;
+      }
+    if (lane == wave_best(best, slot, lane)) {
+      double sc = score[0], pv = v[0], pd = dv[0];
+#pragma unroll
+      for (int s = 0; s < SL; ++s)
+        if (s == slot) {
+          sc = score[s];
+          pv = v[s];
+          pd = dv[s];
+          key[s] = kKeyTaken;
+          taken |= 1u << s;
+        }
+      s_id[r] = lane + kWave * slot;
+      s_pick[r] = sc;
+      if (BOUNDS) {
+        s_pv[r] = best > kKeyUnscored ? pv : -INFINITY;
+        s_pd[r] = best > kKeyUnscored ? pd : 0.0;
+      }
+    }
+  }
+  wave_lds_fence();
+  if constexpr (BOUNDS) {
+    // what is left: the largest value that bounded logits can reach, the largest exact one
+    double reach = -INFINITY, exact = -INFINITY;
+#pragma unroll
+    for (int s = 0; s < SL; ++s)
+      if ((inside & ~taken) >> s & 1) {
+        if (d[s] > 0.0) reach = fmax(reach, v[s] + dv[s]);
+        else exact = fmax(exact, v[s]);
+      }
+    reach = wave_max_f64(reach);
+    exact = wave_max_f64(exact);
+    // pick r stands if it is above all behind it (or exact, and so are those it is not above)
+    double low = INFINITY, high = -INFINITY;   // hull of the picks that do not stand
+    for (int r = lane; r < top_k; r += kWave) {
+      const double pv = s_pv[r], pd = s_pd[r];
+      double hb = reach, eb = exact;
+      for (int j = r + 1; j < top_k; ++j) {
+        if (s_pd[j] > 0.0) hb = fmax(hb, s_pv[j] + s_pd[j]);
+        else eb = fmax(eb, s_pv[j]);
+      }
+      if (pv > -INFINITY && (pv - pd <= hb || (pd > 0.0 && pv - pd <= eb))) {
+        low = fmin(low, pv - pd);
+        high = fmax(high, pv + pd);
+      }
+    }
+    low = -wave_max_f64(-low);
+    high = wave_max_f64(high);
+    if (low <= high) {
+#pragma unroll
+      for (int s = 0; s < SL; ++s)
+        if ((inside >> s & 1) && d[s] > 0.0 && v[s] + dv[s] >= low && v[s] - dv[s] <= high)
+          redo |= 1u << s;
+      wave_lds_fence();
+      if (__any(redo != 0)) return kRedo;
+    }
+  }
+  double factor = (double)rule.scale / divisor;
+  if (rule.renorm) {
+    double total = 0.0;
+    for (int r = lane; r < top_k; r += kWave) total += s_pick[r];
+    total = wave_sum(total);
+    factor = total > 0.0 ? (double)rule.scale / total : 0.0;
+  }
+  for (int r = lane; r < top_k; r += kWave) {
+    ids[t * top_k + r] = s_id[r];
+    weights[t * top_k + r] = s_pick[r] > 0.0 ? (float)(s_pick[r] * factor) : 0.0f;
+  }
+  return kDone;
+}
+
+// One wave per token; lane l owns experts l, l + 64, ... (SL of them).  At M=2048, E=256, k=16
+// one token in nine asks for exact logits, two or three of them.
 template <int SL, typename SRC>
 __global__ __launch_bounds__(kSelWaves* kWave) void select_groups_kernel(
     SRC src, const float* __restrict__ bias, int M, int E, int top_k, GroupRule rule,
     int32_t* __restrict__ ids, float* __restrict__ weights) {
   constexpr bool BOUNDS = std::is_same<SRC, BoundedSource>::value;
   extern __shared__ __align__(16) double sel_lds[];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * kSelWaves + wave;
-  if (t >= M) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int64_t t0 = (int64_t)blockIdx.x * kSelWaves, t = t0 + wave;
   double* s_c = sel_lds + (size_t)wave * select_lds_doubles(BOUNDS, E, top_k);
   const int even_E = (E + 1) / 2 * 2, even_k = (top_k + 1) / 2 * 2;
   double* s_d = s_c + even_E;                              // BOUNDS
@@ -627,258 +909,38 @@ __global__ __launch_bounds__(kSelWaves* kWave) void select_groups_kernel(
 
   double l[SL], d[SL];
   uint32_t redo = 0;   // bit s: this lane's expert in slot s gets its exact logit
+  const bool on = t < M;
 #pragma unroll
   for (int s = 0; s < SL; ++s) {
     const int e = lane + kWave * s;
     l[s] = -INFINITY;
     d[s] = 0.0;
-    if (e < E) src.get(t, e, l[s], d[s]);
+    if (on && e < E) src.get(t, e, l[s], d[s]);
     if (BOUNDS && !(d[s] <= 0.25)) redo |= 1u << s;        // too wide, or not a number
   }
-  auto make_exact = [&](uint32_t mask) {
-    if constexpr (BOUNDS) {
-#pragma unroll
-      for (int s = 0; s < SL; ++s) {
-        uint64_t todo = __ballot((mask >> s) & 1);
-        while (todo) {
-          const int a = __ffsll((unsigned long long)todo) - 1;
-          todo &= todo - 1;
-          const int b = todo ? __ffsll((unsigned long long)todo) - 1 : a;
-          todo &= todo ? todo - 1 : 0;
-          double la, lb;
-          exact_logits(src, t, a + kWave * s, b + kWave * s, lane, la, lb);
-          if (lane == a || lane == b) {
-            l[s] = lane == a ? la : lb;
-            d[s] = 0.0;
-          }
-        }
-      }
+  bool fast = top_k <= kWave;
+  auto select = [&]() -> Fast {
+    if (fast) {
+      const Fast got = select_fast<SL>(l, d, BOUNDS, bias, t, E, top_k, rule,
+                                       reinterpret_cast<float*>(s_c),
+                                       reinterpret_cast<float*>(s_c) + E, s_key, s_id, lane, redo,
+                                       ids, weights);
+      if (got != kOpen) return got;
+      fast = false;
+      wave_lds_fence();
     }
+    return select_fp64<SL, BOUNDS>(l, d, bias, t, E, top_k, rule, s_c, s_d, s_pick, s_pv, s_pd, s_id,
+                                   lane, redo, ids, weights);
   };
-  make_exact(redo);
-  redo = 0;
-  if (top_k <= kWave) {
-    Fast got;
-    while ((got = select_fast<SL>(l, d, BOUNDS, bias, t, E, top_k, rule,
-                                  reinterpret_cast<float*>(s_c), reinterpret_cast<float*>(s_c) + E,
-                                  s_key, s_id, lane, redo, ids, weights)) == kRedo) {
-      wave_lds_fence();
-      make_exact(redo);   // at least one logit: this ends
-      redo = 0;
+  if constexpr (BOUNDS) {
+    __shared__ ExactQueue queue;
+    bool done = !on;
+    for (;;) {
+      if (!done && !__any(redo != 0)) done = select() == kDone;
+      if (!exact_round<SL>(src, queue, t0, M, wave, lane, redo, l, d)) break;
     }
-    if (got == kDone) return;
-  }
-  wave_lds_fence();
-
-  for (;;) {
-    make_exact(redo);
-    redo = 0;
-    // scores (softmax with bounds: without the divisor, which is applied at the end)
-    double score[SL], c[SL], dc[SL], divisor = 1.0;
-    bool live[SL];
-#pragma unroll
-    for (int s = 0; s < SL; ++s) live[s] = l[s] > -INFINITY;
-    if (rule.softmax) {
-      double top = -INFINITY;
-#pragma unroll
-      for (int s = 0; s < SL; ++s)
-        if (live[s]) top = fmax(top, l[s]);
-      top = fmin(wave_max_f64(top), 1.7976931348623157e308);   // +inf counts as the largest number
-      double total = 0.0;
-#pragma unroll
-      for (int s = 0; s < SL; ++s) {
-        score[s] = live[s] ? exp(fmin(l[s], 1.7976931348623157e308) - top) : 0.0;
-        total += score[s];
-        dc[s] = 1.2 * d[s] * score[s];
-      }
-      divisor = wave_sum(total);
-      if (!BOUNDS) {
-#pragma unroll
-        for (int s = 0; s < SL; ++s) score[s] = live[s] ? score[s] / divisor : 0.0;
-        divisor = 1.0;
-      }
-    } else {
-#pragma unroll
-      for (int s = 0; s < SL; ++s) {
-        const double ex = exp(-l[s]);
-        score[s] = live[s] ? 1.0 / (1.0 + ex) : 0.0;
-        dc[s] = d[s] > 0.0 ? 1.2 * d[s] * score[s] * fmin(1.0, ex * score[s]) + 1e-14 : 0.0;
-      }
-    }
-#pragma unroll
-    for (int s = 0; s < SL; ++s) {
-      const int e = lane + kWave * s;
-      c[s] = score[s];
-      if (bias && e < E) c[s] += (double)bias[e];
-      live[s] = live[s] && c[s] > -INFINITY;
-      if (!live[s]) {
-        c[s] = -INFINITY;
-        score[s] = 0.0;
-        dc[s] = 0.0;
-      }
-    }
-
-    uint64_t stay = ~0ull;   // bit g: group g stays
-    if (rule.n_group > 1) {
-#pragma unroll
-      for (int s = 0; s < SL; ++s)
-        if (lane + kWave * s < E) {
-          s_c[lane + kWave * s] = c[s];
-          if (BOUNDS) s_d[lane + kWave * s] = dc[s];
-        }
-      wave_lds_fence();
-      // span lanes (a power of two) read a group's experts and join their two best; lane
-      // g span ends up with group g
-      int span = 1;
-      while (span * 2 * rule.n_group <= kWave) span *= 2;
-      const int g = lane / span, sub = lane % span;
-      const bool mine = g < rule.n_group;
-      double b1 = -INFINITY, b2 = -INFINITY;   // best two c
-      double h1 = -INFINITY, h2 = -INFINITY;   // best two c + dc
-      double w1 = -INFINITY, w2 = -INFINITY;   // best two c - dc
-      auto join = [](double& p1, double& p2, double o1, double o2) {
-        p2 = fmax(fmin(p1, o1), fmax(p2, o2));
-        p1 = fmax(p1, o1);
-      };
-      if (mine)
-        for (int j = sub; j < rule.per; j += span) {
-          const double v = s_c[g * rule.per + j];
-          join(b1, b2, v, -INFINITY);
-          if (BOUNDS) {
-            const double dv = s_d[g * rule.per + j];
-            join(h1, h2, v + dv, -INFINITY);
-            join(w1, w2, v - dv, -INFINITY);
-          }
-        }
-      for (int off = 1; off < span; off <<= 1) {
-        join(b1, b2, __shfl_xor(b1, off, kWave), __shfl_xor(b2, off, kWave));
-        if (BOUNDS) {
-          join(h1, h2, __shfl_xor(h1, off, kWave), __shfl_xor(h2, off, kWave));
-          join(w1, w2, __shfl_xor(w1, off, kWave), __shfl_xor(w2, off, kWave));
-        }
-      }
-      const bool two = rule.group_top == 2;
-      const double total = two && b2 > -INFINITY ? b1 + b2 : b1;
-      int rank = 0;
-      for (int j = 0; j < rule.n_group; ++j) {
-        const double o = __shfl(total, j * span, kWave);
-        rank += (o > total || (o == total && j < g)) ? 1 : 0;
-      }
-      const bool keep = mine && rank < rule.topk_group;
-      const uint64_t kept = __ballot(keep && sub == 0);
-      stay = 0;
-      for (int j = 0; j < rule.n_group; ++j) stay |= ((kept >> (j * span)) & 1) << j;
-      if (BOUNDS && rule.topk_group < rule.n_group) {
-        const double top = two && h2 > -INFINITY ? h1 + h2 : h1;
-        const double low = two && w2 > -INFINITY ? w1 + w2 : w1;
-        const double least = -wave_max_f64(keep ? -low : -INFINITY);
-        const double most = wave_max_f64(mine && !keep ? top : -INFINITY);
-        if (!(least > most)) {   // a group's place is open: exact logits of what makes it
-          const bool open = mine && (keep ? low <= most : top >= least);
-          wave_lds_fence();      // s_c, s_d were read
-          if (sub == 0 && mine) s_c[g] = open ? (two ? w2 : w1) : INFINITY;
-          wave_lds_fence();
-#pragma unroll
-          for (int s = 0; s < SL; ++s) {
-            const int e = lane + kWave * s;
-            if (e < E && d[s] > 0.0 && live[s] && c[s] + dc[s] >= s_c[e / rule.per]) redo |= 1u << s;
-          }
-          wave_lds_fence();
-          if (__any(redo != 0)) continue;
-        }
-      }
-    }
-
-    uint64_t key[SL];
-    double v[SL], dv[SL];   // what orders the picks, and its bound
-#pragma unroll
-    for (int s = 0; s < SL; ++s) {
-      const int e = lane + kWave * s;
-      v[s] = bias ? c[s] : l[s];
-      dv[s] = bias ? dc[s] : d[s];
-      key[s] = kKeyOutside;
-      if (e < E && ((stay >> (e / rule.per)) & 1)) key[s] = live[s] ? order_key(v[s]) : kKeyUnscored;
-    }
-    uint32_t inside = 0, taken = 0;
-#pragma unroll
-    for (int s = 0; s < SL; ++s) inside |= (uint32_t)(key[s] > kKeyUnscored) << s;
-    for (int r = 0; r < top_k; ++r) {
-      uint64_t best = key[0];
-      int slot = 0;
-#pragma unroll
-      for (int s = 1; s < SL; ++s)
-        if (key[s] > best) {
-          best = key[s];
-          slot = s;
-        }
-      if (lane == wave_best(best, slot, lane)) {
-        double sc = score[0], pv = v[0], pd = dv[0];
-#pragma unroll
-        for (int s = 0; s < SL; ++s)
-          if (s == slot) {
-            sc = score[s];
-            pv = v[s];
-            pd = dv[s];
-            key[s] = kKeyTaken;
-            taken |= 1u << s;
-          }
-        s_id[r] = lane + kWave * slot;
-        s_pick[r] = sc;
-        if (BOUNDS) {
-          s_pv[r] = best > kKeyUnscored ? pv : -INFINITY;
-          s_pd[r] = best > kKeyUnscored ? pd : 0.0;
-        }
-      }
-    }
-    wave_lds_fence();
-    if constexpr (BOUNDS) {
-      // what is left: the largest value that bounded logits can reach, the largest exact one
-      double reach = -INFINITY, exact = -INFINITY;
-#pragma unroll
-      for (int s = 0; s < SL; ++s)
-        if ((inside & ~taken) >> s & 1) {
-          if (d[s] > 0.0) reach = fmax(reach, v[s] + dv[s]);
-          else exact = fmax(exact, v[s]);
-        }
-      reach = wave_max_f64(reach);
-      exact = wave_max_f64(exact);
-      // pick r stands if it is above all behind it (or exact, and so are those it is not above)
-      double low = INFINITY, high = -INFINITY;   // hull of the picks that do not stand
-      for (int r = lane; r < top_k; r += kWave) {
-        const double pv = s_pv[r], pd = s_pd[r];
-        double hb = reach, eb = exact;
-        for (int j = r + 1; j < top_k; ++j) {
-          if (s_pd[j] > 0.0) hb = fmax(hb, s_pv[j] + s_pd[j]);
-          else eb = fmax(eb, s_pv[j]);
-        }
-        if (pv > -INFINITY && (pv - pd <= hb || (pd > 0.0 && pv - pd <= eb))) {
-          low = fmin(low, pv - pd);
-          high = fmax(high, pv + pd);
-        }
-      }
-      low = -wave_max_f64(-low);
-      high = wave_max_f64(high);
-      if (low <= high) {
-#pragma unroll
-        for (int s = 0; s < SL; ++s)
-          if ((inside >> s & 1) && d[s] > 0.0 && v[s] + dv[s] >= low && v[s] - dv[s] <= high)
-            redo |= 1u << s;
-        wave_lds_fence();
-        if (__any(redo != 0)) continue;
-      }
-    }
-    double factor = (double)rule.scale / divisor;
-    if (rule.renorm) {
-      double total = 0.0;
-      for (int r = lane; r < top_k; r += kWave) total += s_pick[r];
-      total = wave_sum(total);
-      factor = total > 0.0 ? (double)rule.scale / total : 0.0;
-    }
-    for (int r = lane; r < top_k; r += kWave) {
-      ids[t * top_k + r] = s_id[r];
-      weights[t * top_k + r] = s_pick[r] > 0.0 ? (float)(s_pick[r] * factor) : 0.0f;
-    }
-    return;
+  } else if (on) {
+    select();
   }
 }
 
@@ -913,6 +975,27 @@ hipError_t launch_route_logits(const float* logits, int64_t ld, const float* bia
   return launch_select(LogitSource{logits, ld}, bias, M, E, top_k, rule, ids, w, s);
 }
 
+namespace {
+
+// K in parts (of whole 256-wide pieces) so that about 512 workgroups run; more than 8 cost the
+// selection more than they save (M=333, E=160, H=4096: 4, 8, 16 parts 28, 26, 29 us in all).
+constexpr int kBlMaxParts = 8, kBlWorkgroups = 512;
+int bounded_parts(int64_t M, int E) {
+  const int64_t tiles = (int64_t)((E + kBlTile - 1) / kBlTile) * ((M + kBlTile - 1) / kBlTile);
+  return (int)std::min<int64_t>(kBlMaxParts, (kBlWorkgroups + tiles - 1) / tiles);
+}
+
+}  // namespace
+
+// fp64 keys, or the parts' fp32 logits and |x| |w| sums: M times bounded_parts is at most
+// M + 512 * 64 / (tiles of 64 experts), which grows with M, so that a workspace for some
+// number of tokens does for fewer.
+size_t route_groups_scratch_bytes(int M, int E) {
+  const size_t etiles = (E + kBlTile - 1) / kBlTile;
+  const size_t rows = std::min((size_t)M * kBlMaxParts, (size_t)M + kBlWorkgroups * kBlTile / etiles);
+  return rows * E * 2 * sizeof(float);
+}
+
 // From this many tokens on bounded fp32 MFMA logits replace fp64 ones for every (token,
 // expert).  Not for softmax scores with a bias, whose choices hang on the divisor and so on
 // every expert's exact logit, for more experts than 512 (registers), or where a pick of
@@ -923,10 +1006,9 @@ hipError_t launch_route_groups(const uint16_t* x, const uint16_t* wr, const floa
                                int H, int E, int top_k, const GroupRule& rule, int32_t* ids,
                                float* w, void* scratch, hipStream_t s) {
   if (M >= kBoundedMinTokens && E <= kBoundedMaxExperts && top_k <= 64 && !(rule.softmax && bias)) {
-    // K in parts (of whole 256-wide pieces) so that about 512 workgroups run
     const int64_t tiles = (int64_t)((E + kBlTile - 1) / kBlTile) * ((M + kBlTile - 1) / kBlTile);
     const int pieces = (H + 255) / 256;
-    int parts = (int)std::min<int64_t>({kBlMaxParts, pieces, std::max<int64_t>(1, (512 + tiles - 1) / tiles)});
+    int parts = std::min(bounded_parts(M, E), pieces);
     const int kpart = (pieces + parts - 1) / parts * 256;
     parts = (H + kpart - 1) / kpart;
     const int per_xcd = (int)((tiles * parts + kXcds - 1) / kXcds);
