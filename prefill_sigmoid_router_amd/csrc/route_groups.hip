@@ -43,7 +43,7 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// The same for floats: largest, sum, and each lane's largest of the lanes below it.
+// The same for floats: largest and sum.
 #define MOE_DPP_F32(v, old, ctrl, rows)                                                       \
   __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp((int)__float_as_uint(old),            \
                                                         (int)__float_as_uint(v), ctrl, rows, \
@@ -61,9 +61,6 @@ __device__ __forceinline__ float lane63(float v) {
   return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
 __device__ __forceinline__ float wave_max_f32(float v) { return lane63(scan_max_f32(v)); }
-__device__ __forceinline__ float below_max_f32(float v) {
-  return scan_max_f32(MOE_DPP_F32(v, -INFINITY, 0x138, 0xf));   // wave_shr 1
-}
 __device__ __forceinline__ float wave_sum_f32(float v) {
   v += MOE_DPP_F32(v, 0.0f, 0x111, 0xf);
   v += MOE_DPP_F32(v, 0.0f, 0x112, 0xf);
@@ -74,6 +71,28 @@ __device__ __forceinline__ float wave_sum_f32(float v) {
   return lane63(v);
 }
 #undef MOE_DPP_F32
+
+// Sum of a wave's doubles, in every lane, in a fixed order: DPP moves of both halves.
+__device__ __forceinline__ double wave_sum_f64(double v) {
+#define MOE_DPP_ADD(ctrl, rows)                                                              \
+  {                                                                                          \
+    const uint64_t b = (uint64_t)__double_as_longlong(v);                                    \
+    const int lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, ctrl, rows, 0xf, false); \
+    const int hi = __builtin_amdgcn_update_dpp(0, (int)(b >> 32), ctrl, rows, 0xf, false);   \
+    v += __longlong_as_double((long long)((uint64_t)(uint32_t)hi << 32 | (uint32_t)lo));     \
+  }
+  MOE_DPP_ADD(0x111, 0xf)
+  MOE_DPP_ADD(0x112, 0xf)
+  MOE_DPP_ADD(0x114, 0xf)
+  MOE_DPP_ADD(0x118, 0xf)
+  MOE_DPP_ADD(0x142, 0xa)
+  MOE_DPP_ADD(0x143, 0xc)
+#undef MOE_DPP_ADD
+  const uint64_t b = (uint64_t)__double_as_longlong(v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, 63);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
+  return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
 
 __device__ __forceinline__ double wave_max_f64(double v) {
 #pragma unroll
@@ -241,7 +260,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       if (E % 4 == 0) {
         if (e < E) {
           *reinterpret_cast<float4*>(logits + o) =
-              make_float4((float)sum[i][j][0], (float)sum[i][j][1], (float)sum[i][j][2], (float)sum[i][j][3]);
+              make_float4((float)sum[i][j][0], (float)sum[i][j][1], (float)sum[i][j][2],
+                          (float)sum[i][j][3]);
           *reinterpret_cast<f32x4*>(absdot + o) = aab[i][j];
         }
         continue;
@@ -296,7 +316,7 @@ struct BoundedSource {
 // Exact logits that the workgroup's waves ask for: fp64 dot products, every wave a quarter of
 // the row, the quarters added in wave order, so that equal rows of the router weight give
 // equal sums.  Each wave leaves up to kAsk pairs a round.
-constexpr int kAsk = 8;
+constexpr int kAsk = 8;   // experts, worked off four at a time
 struct ExactQueue {
   int expert[kSelWaves][kAsk];   // -1: none
   double part[kSelWaves][kAsk][kSelWaves];
@@ -338,7 +358,7 @@ __device__ __forceinline__ void quarter_dots(const BoundedSource& q, int64_t t, 
       }
   }
 #pragma unroll
-  for (int i = 0; i < N; ++i) sum[i] = wave_sum(sum[i]);
+  for (int i = 0; i < N; ++i) sum[i] = wave_sum_f64(sum[i]);
 }
 
 // All waves of the workgroup, together: computes what `redo` asks for (bit s: this lane's
@@ -364,10 +384,13 @@ __device__ __forceinline__ bool exact_round(const BoundedSource& q, ExactQueue& 
   if (!__syncthreads_or(asked)) return false;
   for (int w = 0; w < kSelWaves; ++w) {
     const int64_t t = min(t0 + w, M - 1);
-    for (int i = 0; i < kAsk && queue.expert[w][i] >= 0; i += 2) {
-      double sum[2];
-      quarter_dots<2>(q, t, &queue.expert[w][i], wave, lane, sum);
-      if (lane < 2) queue.part[w][i + lane][wave] = lane ? sum[1] : sum[0];
+    for (int i = 0; i < kAsk && queue.expert[w][i] >= 0; i += 4) {
+      double sum[4];
+      quarter_dots<4>(q, t, &queue.expert[w][i], wave, lane, sum);
+      if (lane == 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) queue.part[w][i + j][wave] = sum[j];
+      }
     }
   }
   __syncthreads();
@@ -381,7 +404,7 @@ __device__ __forceinline__ bool exact_round(const BoundedSource& q, ExactQueue& 
     }
   return true;
 }
-static_assert(kSelWaves == 4 && kAsk % 2 == 0, "the sums and pairs above");
+static_assert(kSelWaves == 4 && kAsk % 4 == 0, "the sums and fours above");
 
 // The picks of a token by fp32 values with bounds, if no bound can turn a choice: kDone.
 // Otherwise nothing is written: kRedo with the experts (bit s of `redo`: this lane's in slot
@@ -390,10 +413,10 @@ static_assert(kSelWaves == 4 && kAsk % 2 == 0, "the sums and pairs above");
 // arithmetic: __expf of z is within (|z| + 4) 2^-22 of itself, reciprocals and products
 // within a few 2^-24.
 //
-// Top-k without rounds: the k-th largest of the 64 lanes' largest keys is a lower limit of the
-// k-th largest of all; the keys that reach it (k and a few) are collected, one per lane, and
-// ranked by counting.  (A round of a k-step selection costs 500 cycles: M=8192, E=384, k=8
-// 22 us.)
+// Top-k without rounds: the k-th largest of the 64 lanes' largest values is a lower limit of
+// the k-th largest of all; what can reach it (k and a few) is collected, one per lane, and
+// ranked by counting, in fp64.  (A round of a k-step selection costs 500 cycles: M=8192,
+// E=384, k=8 22 us.)
 enum Fast { kDone, kRedo, kOpen };
 template <int SL>
 __device__ __forceinline__ Fast select_fast(const double (&l)[SL], const double (&d)[SL],
@@ -495,10 +518,19 @@ __device__ __forceinline__ Fast select_fast(const double (&l)[SL], const double 
       p1 = fmaxf(p1, o1);
     };
     if (g < rule.n_group)
-      for (int j = sub; j < rule.per; j += span) {
-        const float x = s_v[g * rule.per + j], dx = s_d[g * rule.per + j];
-        join(h1, h2, x + dx, -INFINITY);
-        join(w1, w2, x - dx, -INFINITY);
+      for (int j0 = sub; j0 < rule.per; j0 += 4 * span) {
+        float x[4], dx[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = g * rule.per + min(j0 + i * span, rule.per - 1);
+          x[i] = j0 + i * span < rule.per ? s_v[j] : -INFINITY;
+          dx[i] = s_d[j];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          join(h1, h2, x[i] + dx[i], -INFINITY);
+          join(w1, w2, x[i] - dx[i], -INFINITY);
+        }
       }
     for (int off = 1; off < span; off <<= 1) {
       join(h1, h2, __shfl_xor(h1, off, kWave), __shfl_xor(h2, off, kWave));
@@ -509,19 +541,24 @@ __device__ __forceinline__ Fast select_fast(const double (&l)[SL], const double 
     float most = two && h2 > -INFINITY ? h1 + h2 : h1, least = two && w2 > -INFINITY ? w1 + w2 : w1;
     if (most > -INFINITY) most += fabsf(most) * u;
     if (least > -INFINITY) least -= fabsf(least) * u;
+    float* const s_most = reinterpret_cast<float*>(s_key);   // 64 each
+    float* const s_least = reinterpret_cast<float*>(s_id);
+    s_most[lane] = s_least[lane] = -INFINITY;
     wave_lds_fence();
     if (sub == 0 && g < rule.n_group) {
-      s_v[g] = most;
-      s_d[g] = least;
+      s_most[g] = most;
+      s_least[g] = least;
     }
     wave_lds_fence();
     // a group stays if fewer than topk_group others can reach it; the rest must be out of reach
     const bool mine = lane < rule.n_group;
-    const float my_least = mine ? s_d[lane] : INFINITY, my_most = mine ? s_v[lane] : -INFINITY;
-    int ahead = 0, open = 0;   // groups certainly above this one, and those that may be
-    for (int j = 0; j < rule.n_group; ++j) {
-      ahead += s_d[j] > my_most ? 1 : 0;
-      open += s_v[j] >= my_least && j != lane ? 1 : 0;
+    const float my_least = s_least[lane], my_most = s_most[lane];
+    int ahead = 0, open = -1;   // groups certainly above this one, those (without it) that may be
+    for (int j = 0; j < rule.n_group; j += 4) {
+      const float4 m = *reinterpret_cast<const float4*>(s_most + j);
+      const float4 n = *reinterpret_cast<const float4*>(s_least + j);
+      ahead += (n.x > my_most) + (n.y > my_most) + (n.z > my_most) + (n.w > my_most);
+      open += (m.x >= my_least) + (m.y >= my_least) + (m.z >= my_least) + (m.w >= my_least);
     }
     const bool in = mine && open < rule.topk_group, out = mine && ahead >= rule.topk_group;
     if (__any(mine && !in && !out)) {
@@ -550,23 +587,19 @@ __device__ __forceinline__ Fast select_fast(const double (&l)[SL], const double 
       dv[s] = dc[s];
     }
   }
-  uint32_t key[SL];
+  auto order32 = [](float f) {
+    const uint32_t bits = __float_as_uint(f + 0.0f);
+    return (int)bits < 0 ? ~bits : bits | 0x80000000u;
+  };
+  // limit: the largest lower end that at least top_k lanes reach with one of their values
+  uint32_t inside = 0, largest = 0;
 #pragma unroll
   for (int s = 0; s < SL; ++s) {
-    const int e = lane + kWave * s;
-    const bool is = (live >> s & 1) && (!by_group || (stay >> group_of(e) & 1));
-    const uint32_t bits = __float_as_uint(v[s] + 0.0f);
-    key[s] = is ? ((int)bits < 0 ? ~bits : bits | 0x80000000u) : 0u;
-    if (e < E) {
-      s_v[e] = v[s];
-      s_d[e] = dv[s];
-    }
+    const bool is = (live >> s & 1) && (!by_group || (stay >> group_of(lane + kWave * s) & 1));
+    inside |= (uint32_t)is << s;
+    if (is) largest = max(largest, order32(v[s] - dv[s]));
   }
-  // limit: the largest key that at least top_k lanes' largest keys reach
-  uint32_t largest = key[0];
-#pragma unroll
-  for (int s = 1; s < SL; ++s) largest = max(largest, key[s]);
-  uint32_t limit = 1u;
+  uint32_t limit = 0;
   if (SL > 1) {
     s_key[lane] = largest;
     wave_lds_fence();
@@ -576,92 +609,118 @@ __device__ __forceinline__ Fast select_fast(const double (&l)[SL], const double 
       const uint4 o = *reinterpret_cast<const uint4*>(s_key + j);
       reached += (o.x >= largest) + (o.y >= largest) + (o.z >= largest) + (o.w >= largest);
     }
-    limit = max(wave_max_u32(reached >= top_k ? largest : 0u), 1u);
+    limit = wave_max_u32(reached >= top_k ? largest : 0u);
     wave_lds_fence();
   }
-  // candidates, one per lane, in slot and lane order
+  // candidates: what can reach the limit, one per lane, in id order.  Each gets its value in
+  // fp64, with the bound that its logit's leaves (softmax with a bias: the fp32 value and
+  // bound, since the divisor is an fp32 sum); what is left cannot be among the picks.
+  double* s_l = reinterpret_cast<double*>(s_v);   // s_v and s_d are free: 64 logits, values, bounds
+  double* s_val = s_l + kWave;
+  double* s_bound = s_val + kWave;
   int found = 0;
 #pragma unroll
   for (int s = 0; s < SL; ++s) {
-    const bool is = key[s] >= limit;
+    const bool is = (inside >> s & 1) && order32(v[s] + dv[s]) >= limit;
     const uint64_t who = __ballot(is);
     const int at = found + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32),
                                                      __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
     found += __popcll(who);
     if (is && at < kWave) {
-      s_key[at] = key[s];
       s_id[at] = lane + kWave * s;
+      s_l[at] = l[s];
+      s_bound[at] = rule.softmax && bias ? (double)dv[s] : d[s];
+      s_val[at] = rule.softmax && bias ? (double)v[s] : (double)b[s];
     }
   }
   if (found < top_k || found > kWave) return kOpen;   // too few scored experts, or many alike
-  if (lane >= found) s_key[lane] = 0u;
   wave_lds_fence();
-  const uint32_t my_key = s_key[lane];
-  const int my_id = lane < found ? s_id[lane] : 0;
+  const bool cand = lane < found;
+  const int my_id = cand ? s_id[lane] : 0;
+  const double my_l = cand ? s_l[lane] : 0.0;
+  double my_v = cand ? s_val[lane] : -INFINITY, my_d = cand ? s_bound[lane] : 0.0;
+  const double ex = exp(rule.softmax ? my_l - (double)top : -my_l);
+  const double score = rule.softmax ? ex : 1.0 / (1.0 + ex);
+  if (!bias) {
+    my_v = cand ? my_l : -INFINITY;
+  } else if (!rule.softmax) {
+    my_v += score;
+    if (my_d > 0.0) my_d = 1.2 * my_d * score * fmin(1.0, ex * score) + 1e-14;
+  }
+  wave_lds_fence();
+  s_val[lane] = my_v;
+  s_bound[lane] = my_d;
+  wave_lds_fence();
   int rank = 0;
-  for (int j = 0; j < found; j += 4) {   // (equal keys share a rank: the check below fails)
-    const uint4 o = *reinterpret_cast<const uint4*>(s_key + j);
-    rank += (o.x > my_key) + (o.y > my_key) + (o.z > my_key) + (o.w > my_key);
-  }
-  const float my_v = s_v[my_id], my_d = s_d[my_id];
-  wave_lds_fence();
-  const bool ahead = lane < found && rank < top_k;
-  s_id[lane] = -1;
-  wave_lds_fence();
-  if (ahead) s_id[rank] = my_id;
-  wave_lds_fence();
-  // What is not picked reaches no further than `reach` (of equal keys one is picked); pick r,
-  // held by lane 63 - r, has to be above that and above every pick behind it.
-  float reach = -INFINITY;
+  bool close = false;   // another candidate that the bounds cannot tell from this one
+  for (int j0 = 0; j0 < found; j0 += 4) {   // (places past the last hold -inf and 0)
+    double o[4], od[4];
 #pragma unroll
-  for (int s = 0; s < SL; ++s)
-    if (key[s] && key[s] < limit) reach = fmaxf(reach, v[s] + dv[s]);
-  if (lane < found && !(ahead && s_id[rank] == my_id)) reach = fmaxf(reach, my_v + my_d);
-  reach = wave_max_f32(reach);
-  const int r = kWave - 1 - lane;
-  const int id = r < top_k ? max(s_id[r], 0) : 0;
-  const bool mine = r < top_k && s_id[r] >= 0;
-  const float pv = s_v[id], pd = s_d[id];
-  const float behind = fmaxf(reach, below_max_f32(mine ? pv + pd : -INFINITY));
-  const bool weak = mine && !(pv - pd > behind);
-  if (__any(weak)) {   // the logits whose values meet the hull of the picks that do not stand
-    const float high = wave_max_f32(weak ? pv + pd : -INFINITY);
-    const float low = -wave_max_f32(weak ? pd - pv : -INFINITY);
+    for (int i = 0; i < 4; ++i) {
+      o[i] = s_val[j0 + i];
+      od[i] = s_bound[j0 + i];
+    }
 #pragma unroll
-    for (int s = 0; s < SL; ++s)
-      if (key[s] && d[s] > 0.0 && v[s] + dv[s] >= low && v[s] - dv[s] <= high) redo |= 1u << s;
-    return __any(redo != 0) ? kRedo : kOpen;
+    for (int i = 0; i < 4; ++i) {
+      rank += (o[i] > my_v || (o[i] == my_v && j0 + i < lane)) ? 1 : 0;
+      close |= j0 + i != lane && fabs(o[i] - my_v) <= my_d + od[i] && my_d + od[i] > 0.0;
+    }
   }
-  // weights from the picks' logits in fp64
-  double lp = 0.0;
+  if (__any(cand && close)) {   // it matters if one of the two is picked
+    s_key[lane] = (uint32_t)rank;
+    wave_lds_fence();
+    bool ask = false, matters = false;
+    for (int j = 0; j < found; ++j) {
+      const double o = s_val[j], od = s_bound[j];
+      const bool pair = j != lane && fabs(o - my_v) <= my_d + od && my_d + od > 0.0 &&
+                        (rank < top_k || (int)s_key[j] < top_k);
+      matters |= pair;
+      ask |= pair && my_d > 0.0;
+    }
+    if (__any(cand && matters)) {
+      if (rule.softmax && bias) return kOpen;
+      wave_lds_fence();
+      s_key[lane] = cand && ask ? 1u : 0u;
+      wave_lds_fence();
+      for (int j = 0; j < found; ++j)
+        if (s_key[j]) {
+          const int e = s_id[j];
 #pragma unroll
-  for (int s = 0; s < SL; ++s) {
-    const double o = __shfl(l[s], id & 63, kWave);
-    if ((id >> 6) == s) lp = o;
+          for (int s = 0; s < SL; ++s)
+            if (e == lane + kWave * s) redo |= 1u << s;
+        }
+      return kRedo;
+    }
   }
-  const double w = mine ? (rule.softmax ? exp(lp - (double)top) : 1.0 / (1.0 + exp(-lp))) : 0.0;
+  const bool mine = cand && rank < top_k;
   double divisor = 1.0;
   if (rule.renorm) {
-    divisor = wave_sum(w);
+    divisor = wave_sum_f64(mine ? score : 0.0);
   } else if (rule.softmax) {
     double total = 0.0;
 #pragma unroll
     for (int s = 0; s < SL; ++s)
       if (live >> s & 1) total += exp(l[s] - (double)top);
-    divisor = wave_sum(total);
+    divisor = wave_sum_f64(total);
   }
   const double factor = divisor > 0.0 ? (double)rule.scale / divisor : 0.0;
   if (mine) {
-    ids[t * top_k + r] = id;
-    weights[t * top_k + r] = (float)(w * factor);
+    ids[t * top_k + rank] = my_id;
+    weights[t * top_k + rank] = (float)(score * factor);
   }
   return kDone;
+}
+
+// Doubles of an array with a place for each expert: 192 at least in all (64 candidates' three).
+__host__ __device__ constexpr int select_lds_experts(bool bounds, int E) {
+  const int even = (E + 1) / 2 * 2, least = bounds ? 96 : 192;
+  return even > least ? even : least;
 }
 
 // LDS of a wave, in doubles: c of E experts (and its bound), the picks' scores (values, bounds)
 // and ids (room for 64), 64 keys; a multiple of 16 bytes, as are the parts before the ids.
 __host__ __device__ constexpr int select_lds_doubles(bool bounds, int E, int top_k) {
-  const int even_E = (E + 1) / 2 * 2, even_k = (top_k + 1) / 2 * 2;
+  const int even_E = select_lds_experts(bounds, E), even_k = (top_k + 1) / 2 * 2;
   const int ids = ((top_k > 64 ? top_k : 64) + 3) / 4 * 2;
   return (bounds ? 2 * even_E + 3 * even_k : even_E + even_k) + ids + 32;
 }
@@ -698,7 +757,7 @@ __device__ __forceinline__ Fast select_fp64(const double (&l)[SL], const double 
       total += score[s];
       dc[s] = 1.2 * d[s] * score[s];
     }
-    divisor = wave_sum(total);
+    divisor = wave_sum_f64(total);
     if (!BOUNDS) {
 #pragma unroll
       for (int s = 0; s < SL; ++s) score[s] = live[s] ? score[s] / divisor : 0.0;
@@ -899,7 +958,7 @@ __global__ __launch_bounds__(kSelWaves* kWave) void select_groups_kernel(
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int64_t t0 = (int64_t)blockIdx.x * kSelWaves, t = t0 + wave;
   double* s_c = sel_lds + (size_t)wave * select_lds_doubles(BOUNDS, E, top_k);
-  const int even_E = (E + 1) / 2 * 2, even_k = (top_k + 1) / 2 * 2;
+  const int even_E = select_lds_experts(BOUNDS, E), even_k = (top_k + 1) / 2 * 2;
   double* s_d = s_c + even_E;                              // BOUNDS
   double* s_pick = s_c + (BOUNDS ? 2 : 1) * even_E;
   double* s_pv = s_pick + even_k;                          // BOUNDS: the picks' values
