@@ -114,9 +114,9 @@ __device__ __forceinline__ void scaled_act(i32x4 g0, i32x4 g1, i32x4 u0, i32x4 u
 }
 
 // act leaves the up product as block floats: 32 columns of a row share a power of two (byte
-// E: value = int16 * 2^(E - 140), the largest below 2^14), because rounding act to bf16 first
-// moves one int8 code in ten by one (the layer's output 0.6 % off in relative L2 instead of
-// 0.2 %) and fp32 is twice the bytes.  Four lanes (lane / 16) hold the 32 columns, 8 each;
+// E: value = int16 * 2^(E - 141), the largest up to 2^15 - 1), because rounding act to bf16
+// first moves one int8 code in ten by one (the layer's output 0.6 % off in relative L2 instead
+// of 0.2 %) and fp32 is twice the bytes; these 16 bits move one code in 2,000.  Four lanes (lane / 16) hold the 32 columns, 8 each;
 // they call it together.  a: act of this lane's columns, 0 past the last; c: its first column.
 // Layout [ceil(I / 128)][rows][128]: what a workgroup writes is one piece of memory.
 __device__ __forceinline__ void store_act(const I8Args& p, int row, int c, const float (&a)[8]) {
@@ -125,13 +125,14 @@ __device__ __forceinline__ void store_act(const I8Args& p, int row, int c, const
   for (int q = 0; q < 8; ++q) m = max(m, __float_as_uint(a[q]) & 0x7fffffffu);
   m = max(m, (uint32_t)__shfl_xor((int)m, 16, kWave));
   m = max(m, (uint32_t)__shfl_xor((int)m, 32, kWave));
-  const uint32_t E = max(m >> 23, 14u);
-  const float mult = E == 255u ? 0.0f : __uint_as_float((267u - E) << 23);   // 2^(140 - E)
+  const uint32_t E = max(m >> 23, 15u);
+  const float mult = E == 255u ? 0.0f : __uint_as_float((268u - E) << 23);   // 2^(141 - E)
   uint32_t v[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const int lo = E == 255u ? 0 : (int)rintf(a[2 * q] * mult);
-    const int hi = E == 255u ? 0 : (int)rintf(a[2 * q + 1] * mult);
+    // (32768 from the last few values below 2^15: 32767; -32768 the same by symmetry)
+    const int lo = E == 255u ? 0 : (int)fminf(fmaxf(rintf(a[2 * q] * mult), -32767.0f), 32767.0f);
+    const int hi = E == 255u ? 0 : (int)fminf(fmaxf(rintf(a[2 * q + 1] * mult), -32767.0f), 32767.0f);
     v[q] = (uint32_t)(lo & 0xffff) | (uint32_t)hi << 16;
   }
   const size_t block_row = (size_t)(c >> 7) * p.act_rows + row;

@@ -103,7 +103,7 @@ __global__ __launch_bounds__(kQThreads) void i8_act_kernel(
   auto value8 = [&](int ch) { return act + ((ch >> 4) * rows + row) * 128 + (ch & 15) * 8; };
   auto exp8 = [&](int ch) { return exps[((ch >> 4) * rows + row) * 4 + ((ch >> 2) & 3)]; };
   const int nchunk = I >> 3;
-  auto unit = [](uint32_t e) { return __uint_as_float((e - 13u) << 23); };   // 2^(e - 140)
+  auto unit = [](uint32_t e) { return __uint_as_float((e - 14u) << 23); };   // 2^(e - 141)
   auto largest = [](u32x4 v) {
     int m = 0;
 #pragma unroll
@@ -119,7 +119,7 @@ __global__ __launch_bounds__(kQThreads) void i8_act_kernel(
     const int ch = lane + kWave * i;
     const bool in = ch < nchunk;
     keep[i] = in ? ld16(value8(ch)) : u32x4{0, 0, 0, 0};
-    e[i] = in ? exp8(ch) : 14u;
+    e[i] = in ? exp8(ch) : 15u;
   }
 #pragma unroll
   for (int i = 0; i < KEEP; ++i) {
