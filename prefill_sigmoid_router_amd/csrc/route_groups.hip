@@ -277,21 +277,29 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 }
 
 // Logits of a token: fp64 keys, the caller's fp32 logits, or fp32 MFMA partial logits with
-// their |x| . |w| sums (bounded_logits_kernel), which bound their error.
+// their |x| . |w| sums (bounded_logits_kernel), which bound their error.  -inf past the last.
 struct KeySource {
   const double* keys;
   int64_t ld;
-  __device__ void get(int64_t t, int e, double& l, double& d) const {
-    l = keys[t * ld + e];
-    d = 0.0;
+  template <int SL>
+  __device__ void get(int64_t t, int E, int lane, double (&l)[SL], double (&d)[SL]) const {
+#pragma unroll
+    for (int s = 0; s < SL; ++s) {
+      l[s] = lane + kWave * s < E ? keys[t * ld + lane + kWave * s] : -INFINITY;
+      d[s] = 0.0;
+    }
   }
 };
 struct LogitSource {
   const float* logits;
   int64_t ld;
-  __device__ void get(int64_t t, int e, double& l, double& d) const {
-    l = (double)logits[t * ld + e];
-    d = 0.0;
+  template <int SL>
+  __device__ void get(int64_t t, int E, int lane, double (&l)[SL], double (&d)[SL]) const {
+#pragma unroll
+    for (int s = 0; s < SL; ++s) {
+      l[s] = lane + kWave * s < E ? (double)logits[t * ld + lane + kWave * s] : -INFINITY;
+      d[s] = 0.0;
+    }
   }
 };
 struct BoundedSource {
@@ -300,30 +308,63 @@ struct BoundedSource {
   int parts, M, H;
   double rel;   // error of a partial logit over its |x| . |w| sum
   int64_t ld;
-  __device__ void get(int64_t t, int e, double& l, double& d) const {
-    double a = 0.0;
-    l = 0.0;
-#pragma unroll 4
-    for (int p = 0; p < parts; ++p) {
-      l += (double)logits[((int64_t)p * M + t) * ld + e];
-      a += (double)absdot[((int64_t)p * M + t) * ld + e];
+  template <int SL>
+  __device__ void get(int64_t t, int E, int lane, double (&l)[SL], double (&d)[SL]) const {
+    constexpr int B = SL > 4 ? 2 : 4;   // parts in flight
+#pragma unroll
+    for (int s = 0; s < SL; ++s) l[s] = d[s] = 0.0;
+    for (int p0 = 0; p0 < parts; p0 += B) {
+      float v[B][SL], a[B][SL];
+#pragma unroll
+      for (int p = 0; p < B; ++p) {
+        const int64_t row = ((int64_t)min(p0 + p, parts - 1) * M + t) * ld;
+#pragma unroll
+        for (int s = 0; s < SL; ++s) {
+          const int e = min(lane + kWave * s, E - 1);
+          v[p][s] = logits[row + e];
+          a[p][s] = absdot[row + e];
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < B; ++p) {
+        if (p0 + p >= parts) break;
+#pragma unroll
+        for (int s = 0; s < SL; ++s) {
+          l[s] += (double)v[p][s];
+          d[s] += (double)a[p][s];
+        }
+      }
     }
-    // (subnormal products may be flushed: H times the smallest normal number)
-    d = a * rel + (double)H * 0x1p-126;
+#pragma unroll
+    for (int s = 0; s < SL; ++s) {
+      // (subnormal products may be flushed: H times the smallest normal number)
+      const bool in = lane + kWave * s < E;
+      l[s] = in ? l[s] : -INFINITY;
+      d[s] = in ? d[s] * rel + (double)H * 0x1p-126 : 0.0;
+    }
   }
+};
+
+// An expert that may be among the picks: one per lane.
+struct Candidate {
+  int id;
+  double l, d;       // logit and its bound
+  double b;          // bias
+  uint32_t lo, hi;   // ends of the fp32 interval of what orders the picks, as order32 keys
 };
 
 // Exact logits that the workgroup's waves ask for: fp64 dot products, every wave a quarter of
 // the row, the quarters added in wave order, so that equal rows of the router weight give
-// equal sums.  Each wave leaves up to kAsk pairs a round.
-constexpr int kAsk = 8;   // experts, worked off four at a time
+// equal sums.  Each wave leaves up to kAsk experts a round.
+constexpr int kAsk = 8;   // experts, worked off two at a time (most tokens that ask have two)
 struct ExactQueue {
   int expert[kSelWaves][kAsk];   // -1: none
   double part[kSelWaves][kAsk][kSelWaves];
 };
 
-// One wave's quarter of N dot products of row t of x.
-template <int N>
+// One wave's quarter of N dot products of row t of x, B chunks of 8 values a lane in flight per
+// row (4: H = 7168 in one batch).
+template <int N, int B>
 __device__ __forceinline__ void quarter_dots(const BoundedSource& q, int64_t t, const int* experts,
                                              int wave, int lane, double (&sum)[N]) {
   const uint16_t* xr = q.x + t * q.H;
@@ -333,7 +374,6 @@ __device__ __forceinline__ void quarter_dots(const BoundedSource& q, int64_t t, 
     w[i] = q.wr + (size_t)max(experts[i], 0) * q.H;
     sum[i] = 0.0;
   }
-  constexpr int B = 4;   // chunks of 8 values a lane in flight per row: H = 7168 in one batch
   const int n = q.H >> 3, beg = n * wave / kSelWaves, end = n * (wave + 1) / kSelWaves;
   for (int c0 = beg + lane; c0 < end; c0 += kWave * B) {
     u32x4 xv[B], v[N][B];
@@ -361,78 +401,89 @@ __device__ __forceinline__ void quarter_dots(const BoundedSource& q, int64_t t, 
   for (int i = 0; i < N; ++i) sum[i] = wave_sum_f64(sum[i]);
 }
 
-// All waves of the workgroup, together: computes what `redo` asks for (bit s: this lane's
-// expert in slot s) as far as the queue goes and clears those bits.  False if no wave asked.
+// All waves of the workgroup, together: computes what `redo` (bit s: this lane's expert in
+// slot s) and `ask` (this lane's candidate) ask for as far as the queue goes and clears those.
+// False if no wave asked.
 template <int SL>
 __device__ __forceinline__ bool exact_round(const BoundedSource& q, ExactQueue& queue, int64_t t0,
                                             int64_t M, int wave, int lane, uint32_t& redo,
-                                            double (&l)[SL], double (&d)[SL]) {
+                                            double (&l)[SL], double (&d)[SL], bool& ask,
+                                            Candidate& mine) {
   if (lane < kAsk) queue.expert[wave][lane] = -1;
   wave_lds_fence();
   int asked = 0;
-  int at[SL];   // this lane's place in the queue for slot s
+  int at[SL + 1];   // this lane's place in the queue for slot s, and for its candidate
 #pragma unroll
-  for (int s = 0; s < SL; ++s) {
-    const bool ask = (redo >> s) & 1;
-    const uint64_t who = __ballot(ask);
+  for (int s = 0; s <= SL; ++s) {
+    const bool wants = s < SL ? (redo >> s) & 1 : ask;
+    const uint64_t who = __ballot(wants);
     const int place = asked + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32),
                                                         __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
-    at[s] = ask && place < kAsk ? place : -1;
-    if (at[s] >= 0) queue.expert[wave][place] = lane + kWave * s;
+    at[s] = wants && place < kAsk ? place : -1;
+    if (at[s] >= 0) queue.expert[wave][place] = s < SL ? lane + kWave * s : mine.id;
     asked += __popcll(who);
   }
   if (!__syncthreads_or(asked)) return false;
   for (int w = 0; w < kSelWaves; ++w) {
     const int64_t t = min(t0 + w, M - 1);
-    for (int i = 0; i < kAsk && queue.expert[w][i] >= 0; i += 4) {
-      double sum[4];
-      quarter_dots<4>(q, t, &queue.expert[w][i], wave, lane, sum);
+    for (int i = 0; i < kAsk && queue.expert[w][i] >= 0; i += 2) {
+      double sum[2];
+      quarter_dots<2, (SL > 4 ? 2 : 4)>(q, t, &queue.expert[w][i], wave, lane, sum);
       if (lane == 0) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) queue.part[w][i + j][wave] = sum[j];
+        for (int j = 0; j < 2; ++j) queue.part[w][i + j][wave] = sum[j];
       }
     }
   }
   __syncthreads();
 #pragma unroll
-  for (int s = 0; s < SL; ++s)
+  for (int s = 0; s <= SL; ++s)
     if (at[s] >= 0) {
       const double* part = queue.part[wave][at[s]];
-      l[s] = ((part[0] + part[1]) + part[2]) + part[3];
-      d[s] = 0.0;
-      redo &= ~(1u << s);
+      const double got = ((part[0] + part[1]) + part[2]) + part[3];
+      if (s < SL) {
+        l[s] = got;
+        d[s] = 0.0;
+        redo &= ~(1u << s);
+      } else {
+        mine.l = got;
+        mine.d = 0.0;
+        ask = false;
+      }
     }
   return true;
 }
-static_assert(kSelWaves == 4 && kAsk % 4 == 0, "the sums and fours above");
+static_assert(kSelWaves == 4 && kAsk % 2 == 0, "the sums and pairs above");
 
-// The picks of a token by fp32 values with bounds, if no bound can turn a choice: kDone.
-// Otherwise nothing is written: kRedo with the experts (bit s of `redo`: this lane's in slot
-// s) whose exact logits can settle it, or kOpen, and the fp64 code below decides.  Each
-// value's bound covers its logit's (|l - exact| <= d, and l's rounding to fp32) and the fp32
-// arithmetic: __expf of z is within (|z| + 4) 2^-22 of itself, reciprocals and products
-// within a few 2^-24.
+// Selection of a token by fp32 values with bounds, in two steps: groups and candidates
+// (collect_fast), order and weights (rank_fast).  kDone: no bound can turn a choice.  kRedo:
+// `redo` or `ask` mark the experts whose exact logits can settle it.  kOpen: the fp64 code
+// below decides.  Each value's bound covers its logit's (|l - exact| <= d, and l's rounding
+// to fp32) and the fp32 arithmetic: __expf of z is within (|z| + 4) 2^-22 of itself,
+// reciprocals and products within a few 2^-24.
 //
 // Top-k without rounds: the k-th largest of the 64 lanes' largest values is a lower limit of
 // the k-th largest of all; what can reach it (k and a few) is collected, one per lane, and
-// ranked by counting, in fp64.  (A round of a k-step selection costs 500 cycles: M=8192,
-// E=384, k=8 22 us.)
+// ranked by counting the intervals above each, or, where intervals meet, the fp64 values.  (A
+// round of a k-step selection costs 500 cycles: M=8192, E=384, k=8 22 us.)
 enum Fast { kDone, kRedo, kOpen };
+
+__device__ __forceinline__ uint32_t order32(float f) {   // orders as the numbers do
+  const uint32_t bits = __float_as_uint(f + 0.0f);
+  return (int)bits < 0 ? ~bits : bits | 0x80000000u;
+}
+
 template <int SL>
-__device__ __forceinline__ Fast select_fast(const double (&l)[SL], const double (&d)[SL],
-                                            bool bounded, const float* bias, int64_t t, int E,
-                                            int top_k, const GroupRule& rule, float* s_v, float* s_d,
-                                            uint32_t* s_key, int* s_id, int lane, uint32_t& redo,
-                                            int32_t* ids, float* weights) {
+__device__ __forceinline__ Fast collect_fast(const double (&l)[SL], const double (&d)[SL],
+                                             const float (&b)[SL], bool bounded, bool bias, int E,
+                                             int top_k, const GroupRule& rule, float* s_v,
+                                             float* s_d, uint32_t* s_key, int* s_id, int lane,
+                                             uint32_t& redo, float& top, int& found,
+                                             Candidate& mine) {
   constexpr float u = 0x1p-22f;
-  float v[SL], dv[SL], b[SL];
+  float v[SL], dv[SL];
   uint32_t live = 0;
   bool odd = false;   // a logit or bound that fp32 does not hold
-#pragma unroll
-  for (int s = 0; s < SL; ++s) {
-    const int e = lane + kWave * s;
-    b[s] = bias && e < E ? bias[e] : 0.0f;
-  }
 #pragma unroll
   for (int s = 0; s < SL; ++s) {
     v[s] = (float)l[s];
@@ -447,7 +498,7 @@ __device__ __forceinline__ Fast select_fast(const double (&l)[SL], const double 
   float c[SL], dc[SL];
   // scores only where something but the picks' weights needs them
   const bool by_group = rule.n_group > 1 && rule.topk_group < rule.n_group;
-  float top = -INFINITY;
+  top = -INFINITY;
   if (rule.softmax) {
 #pragma unroll
     for (int s = 0; s < SL; ++s)
@@ -551,7 +602,7 @@ __device__ __forceinline__ Fast select_fast(const double (&l)[SL], const double 
     }
     wave_lds_fence();
     // a group stays if fewer than topk_group others can reach it; the rest must be out of reach
-    const bool mine = lane < rule.n_group;
+    const bool group = lane < rule.n_group;
     const float my_least = s_least[lane], my_most = s_most[lane];
     int ahead = 0, open = -1;   // groups certainly above this one, those (without it) that may be
     for (int j = 0; j < rule.n_group; j += 4) {
@@ -560,12 +611,12 @@ __device__ __forceinline__ Fast select_fast(const double (&l)[SL], const double 
       ahead += (n.x > my_most) + (n.y > my_most) + (n.z > my_most) + (n.w > my_most);
       open += (m.x >= my_least) + (m.y >= my_least) + (m.z >= my_least) + (m.w >= my_least);
     }
-    const bool in = mine && open < rule.topk_group, out = mine && ahead >= rule.topk_group;
-    if (__any(mine && !in && !out)) {
+    const bool in = group && open < rule.topk_group, out = group && ahead >= rule.topk_group;
+    if (__any(group && !in && !out)) {
       // what can make an open group's score: values that reach its group_top-th lower end
       wave_lds_fence();
       if (sub == 0 && g < rule.n_group) s_v[g] = two ? w2 : w1;
-      if (mine) s_d[lane] = !in && !out ? 1.0f : 0.0f;
+      if (group) s_d[lane] = !in && !out ? 1.0f : 0.0f;
       wave_lds_fence();
 #pragma unroll
       for (int s = 0; s < SL; ++s) {
@@ -587,10 +638,6 @@ __device__ __forceinline__ Fast select_fast(const double (&l)[SL], const double 
       dv[s] = dc[s];
     }
   }
-  auto order32 = [](float f) {
-    const uint32_t bits = __float_as_uint(f + 0.0f);
-    return (int)bits < 0 ? ~bits : bits | 0x80000000u;
-  };
   // limit: the largest lower end that at least top_k lanes reach with one of their values
   uint32_t inside = 0, largest = 0;
 #pragma unroll
@@ -612,16 +659,16 @@ __device__ __forceinline__ Fast select_fast(const double (&l)[SL], const double 
     limit = wave_max_u32(reached >= top_k ? largest : 0u);
     wave_lds_fence();
   }
-  // candidates: what can reach the limit, one per lane, in id order.  Each gets its value in
-  // fp64, with the bound that its logit's leaves (softmax with a bias: the fp32 value and
-  // bound, since the divisor is an fp32 sum); what is left cannot be among the picks.
-  double* s_l = reinterpret_cast<double*>(s_v);   // s_v and s_d are free: 64 logits, values, bounds
-  double* s_val = s_l + kWave;
-  double* s_bound = s_val + kWave;
-  int found = 0;
+  // candidates: what can reach the limit, one per lane, in slot and lane order
+  double* s_l = reinterpret_cast<double*>(s_v);   // s_v and s_d are free: 64 of each
+  double* s_b = s_l + kWave;
+  float* s_bias = reinterpret_cast<float*>(s_b + kWave);
+  uint32_t* s_hi = reinterpret_cast<uint32_t*>(s_bias + kWave);
+  found = 0;
 #pragma unroll
   for (int s = 0; s < SL; ++s) {
-    const bool is = (inside >> s & 1) && order32(v[s] + dv[s]) >= limit;
+    const uint32_t hi = order32(v[s] + dv[s]);
+    const bool is = (inside >> s & 1) && hi >= limit;
     const uint64_t who = __ballot(is);
     const int at = found + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32),
                                                      __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
@@ -629,83 +676,96 @@ __device__ __forceinline__ Fast select_fast(const double (&l)[SL], const double 
     if (is && at < kWave) {
       s_id[at] = lane + kWave * s;
       s_l[at] = l[s];
-      s_bound[at] = rule.softmax && bias ? (double)dv[s] : d[s];
-      s_val[at] = rule.softmax && bias ? (double)v[s] : (double)b[s];
+      s_b[at] = d[s];
+      s_bias[at] = b[s];
+      s_key[at] = order32(v[s] - dv[s]);
+      s_hi[at] = hi;
     }
   }
   if (found < top_k || found > kWave) return kOpen;   // too few scored experts, or many alike
   wave_lds_fence();
   const bool cand = lane < found;
-  const int my_id = cand ? s_id[lane] : 0;
-  const double my_l = cand ? s_l[lane] : 0.0;
-  double my_v = cand ? s_val[lane] : -INFINITY, my_d = cand ? s_bound[lane] : 0.0;
-  const double ex = exp(rule.softmax ? my_l - (double)top : -my_l);
+  mine.id = cand ? s_id[lane] : 0;
+  mine.l = cand ? s_l[lane] : 0.0;
+  mine.d = cand ? s_b[lane] : 0.0;
+  mine.b = cand ? (double)s_bias[lane] : 0.0;
+  mine.lo = cand ? s_key[lane] : 0u;
+  mine.hi = cand ? s_hi[lane] : 0u;
+  wave_lds_fence();
+  return kDone;
+}
+
+// again: after exact logits came in, which the fp32 intervals do not hold
+template <int SL>
+__device__ __forceinline__ Fast rank_fast(const double (&l)[SL], const Candidate& mine, bool again,
+                                          bool bias, int64_t t, int top_k, const GroupRule& rule,
+                                          float top, int found, double* s_val, uint32_t* s_key,
+                                          int lane, bool& ask, int32_t* ids, float* weights) {
+  const bool cand = lane < found;
+  const double ex = exp(rule.softmax ? mine.l - (double)top : -mine.l);
   const double score = rule.softmax ? ex : 1.0 / (1.0 + ex);
-  if (!bias) {
-    my_v = cand ? my_l : -INFINITY;
-  } else if (!rule.softmax) {
-    my_v += score;
-    if (my_d > 0.0) my_d = 1.2 * my_d * score * fmin(1.0, ex * score) + 1e-14;
+  int rank = 0, reach = -1;   // candidates certainly above this one, those (without it) that may be
+  for (int j = 0; j < found; ++j) {
+    rank += (uint32_t)__builtin_amdgcn_readlane((int)mine.lo, j) > mine.hi ? 1 : 0;
+    reach += (uint32_t)__builtin_amdgcn_readlane((int)mine.hi, j) >= mine.lo ? 1 : 0;
   }
-  wave_lds_fence();
-  s_val[lane] = my_v;
-  s_bound[lane] = my_d;
-  wave_lds_fence();
-  int rank = 0;
-  bool close = false;   // another candidate that the bounds cannot tell from this one
-  for (int j0 = 0; j0 < found; j0 += 4) {   // (places past the last hold -inf and 0)
-    double o[4], od[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o[i] = s_val[j0 + i];
-      od[i] = s_bound[j0 + i];
+  if (__any(cand && (again || (rank != reach && rank < top_k)))) {
+    // the same in fp64, by values with the bounds that their logits' leave
+    if (rule.softmax && bias) return kOpen;   // (their divisor is an fp32 sum)
+    double* s_bound = s_val + kWave;
+    double my_v = cand ? mine.l : -INFINITY, my_d = mine.d;
+    if (bias && cand) {
+      my_v = score + mine.b;
+      if (my_d > 0.0) my_d = 1.2 * my_d * score * fmin(1.0, ex * score) + 1e-14;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      rank += (o[i] > my_v || (o[i] == my_v && j0 + i < lane)) ? 1 : 0;
-      close |= j0 + i != lane && fabs(o[i] - my_v) <= my_d + od[i] && my_d + od[i] > 0.0;
-    }
-  }
-  if (__any(cand && close)) {   // it matters if one of the two is picked
-    s_key[lane] = (uint32_t)rank;
+    s_val[lane] = my_v;
+    s_bound[lane] = my_d;
     wave_lds_fence();
-    bool ask = false, matters = false;
-    for (int j = 0; j < found; ++j) {
-      const double o = s_val[j], od = s_bound[j];
-      const bool pair = j != lane && fabs(o - my_v) <= my_d + od && my_d + od > 0.0 &&
-                        (rank < top_k || (int)s_key[j] < top_k);
-      matters |= pair;
-      ask |= pair && my_d > 0.0;
-    }
-    if (__any(cand && matters)) {
-      if (rule.softmax && bias) return kOpen;
-      wave_lds_fence();
-      s_key[lane] = cand && ask ? 1u : 0u;
-      wave_lds_fence();
-      for (int j = 0; j < found; ++j)
-        if (s_key[j]) {
-          const int e = s_id[j];
+    rank = 0;
+    bool close = false;   // another candidate that the bounds cannot tell from this one
+    for (int j0 = 0; j0 < found; j0 += 4) {   // (places past the last hold -inf and 0)
+      double o[4], od[4];
 #pragma unroll
-          for (int s = 0; s < SL; ++s)
-            if (e == lane + kWave * s) redo |= 1u << s;
-        }
-      return kRedo;
+      for (int i = 0; i < 4; ++i) {
+        o[i] = s_val[j0 + i];
+        od[i] = s_bound[j0 + i];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        rank += (o[i] > my_v || (o[i] == my_v && j0 + i < lane)) ? 1 : 0;
+        close |= j0 + i != lane && fabs(o[i] - my_v) <= my_d + od[i] && my_d + od[i] > 0.0;
+      }
+    }
+    if (__any(cand && close)) {   // it matters if one of the two is picked
+      s_key[lane] = (uint32_t)rank;
+      wave_lds_fence();
+      bool matters = false;
+      for (int j = 0; j < found; ++j) {
+        const double o = s_val[j], od = s_bound[j];
+        matters |= j != lane && fabs(o - my_v) <= my_d + od && my_d + od > 0.0 &&
+                   (rank < top_k || (int)s_key[j] < top_k);
+      }
+      wave_lds_fence();
+      if (__any(cand && matters)) {   // (one of a pair at least has a bound)
+        ask = cand && matters && my_d > 0.0;
+        return kRedo;
+      }
     }
   }
-  const bool mine = cand && rank < top_k;
+  const bool picked = cand && rank < top_k;
   double divisor = 1.0;
   if (rule.renorm) {
-    divisor = wave_sum_f64(mine ? score : 0.0);
+    divisor = wave_sum_f64(picked ? score : 0.0);
   } else if (rule.softmax) {
     double total = 0.0;
 #pragma unroll
     for (int s = 0; s < SL; ++s)
-      if (live >> s & 1) total += exp(l[s] - (double)top);
+      if (l[s] > -INFINITY) total += exp(l[s] - (double)top);
     divisor = wave_sum_f64(total);
   }
   const double factor = divisor > 0.0 ? (double)rule.scale / divisor : 0.0;
-  if (mine) {
-    ids[t * top_k + rank] = my_id;
+  if (picked) {
+    ids[t * top_k + rank] = mine.id;
     weights[t * top_k + rank] = (float)(score * factor);
   }
   return kDone;
@@ -950,7 +1010,7 @@ __device__ __forceinline__ Fast select_fp64(const double (&l)[SL], const double 
 // One wave per token; lane l owns experts l, l + 64, ... (SL of them).  At M=2048, E=256, k=16
 // one token in nine asks for exact logits, two or three of them.
 template <int SL, typename SRC>
-__global__ __launch_bounds__(kSelWaves* kWave) void select_groups_kernel(
+__global__ __launch_bounds__(kSelWaves* kWave, 2) void select_groups_kernel(
     SRC src, const float* __restrict__ bias, int M, int E, int top_k, GroupRule rule,
     int32_t* __restrict__ ids, float* __restrict__ weights) {
   constexpr bool BOUNDS = std::is_same<SRC, BoundedSource>::value;
@@ -966,28 +1026,43 @@ __global__ __launch_bounds__(kSelWaves* kWave) void select_groups_kernel(
   int* s_id = reinterpret_cast<int*>(s_pick + (BOUNDS ? 3 : 1) * even_k);   // and the picks
   uint32_t* s_key = reinterpret_cast<uint32_t*>(s_id + (max(top_k, kWave) + 3) / 4 * 4);
 
-  double l[SL], d[SL];
-  uint32_t redo = 0;   // bit s: this lane's expert in slot s gets its exact logit
   const bool on = t < M;
+  float b[SL];
+  double l[SL], d[SL];
+  src.template get<SL>(min(t, (int64_t)M - 1), E, lane, l, d);
 #pragma unroll
   for (int s = 0; s < SL; ++s) {
     const int e = lane + kWave * s;
-    l[s] = -INFINITY;
-    d[s] = 0.0;
-    if (on && e < E) src.get(t, e, l[s], d[s]);
-    if (BOUNDS && !(d[s] <= 0.25)) redo |= 1u << s;        // too wide, or not a number
+    b[s] = bias && e < E ? bias[e] : 0.0f;
   }
-  bool fast = top_k <= kWave;
+  uint32_t redo = 0;   // bit s: this lane's expert in slot s gets its exact logit
+  if (BOUNDS && on) {
+#pragma unroll
+    for (int s = 0; s < SL; ++s)
+      if (!(d[s] <= 0.25)) redo |= 1u << s;   // too wide, or not a number
+  }
+  enum { kCollect, kRank, kSlow } stage = top_k <= kWave ? kCollect : kSlow;
+  bool ask = false, again = false;   // this lane's candidate gets its exact logit; some did
+  float top = 0.0f;
+  int found = 0;
+  Candidate mine{};
   auto select = [&]() -> Fast {
-    if (fast) {
-      const Fast got = select_fast<SL>(l, d, BOUNDS, bias, t, E, top_k, rule,
-                                       reinterpret_cast<float*>(s_c),
-                                       reinterpret_cast<float*>(s_c) + E, s_key, s_id, lane, redo,
-                                       ids, weights);
-      if (got != kOpen) return got;
-      fast = false;
-      wave_lds_fence();
+    Fast got = kOpen;
+    if (stage == kCollect) {
+      got = collect_fast<SL>(l, d, b, BOUNDS, bias != nullptr, E, top_k, rule,
+                             reinterpret_cast<float*>(s_c), reinterpret_cast<float*>(s_c) + E, s_key,
+                             s_id, lane, redo, top, found, mine);
+      if (got == kRedo) return got;
+      stage = got == kDone ? kRank : kSlow;
     }
+    if (stage == kRank) {
+      got = rank_fast<SL>(l, mine, again, bias != nullptr, t, top_k, rule, top, found, s_c, s_key,
+                          lane, ask, ids, weights);
+      again = true;
+      if (got != kOpen) return got;
+      stage = kSlow;
+    }
+    wave_lds_fence();
     return select_fp64<SL, BOUNDS>(l, d, bias, t, E, top_k, rule, s_c, s_d, s_pick, s_pv, s_pd, s_id,
                                    lane, redo, ids, weights);
   };
@@ -995,8 +1070,8 @@ __global__ __launch_bounds__(kSelWaves* kWave) void select_groups_kernel(
     __shared__ ExactQueue queue;
     bool done = !on;
     for (;;) {
-      if (!done && !__any(redo != 0)) done = select() == kDone;
-      if (!exact_round<SL>(src, queue, t0, M, wave, lane, redo, l, d)) break;
+      if (!done && !__any(redo != 0 || ask)) done = select() == kDone;
+      if (!exact_round<SL>(src, queue, t0, M, wave, lane, redo, l, d, ask, mine)) break;
     }
   } else if (on) {
     select();
