@@ -705,30 +705,36 @@ def moe_forward_mx(x, router_w, router_bias, w13_codes, w13_scales, w2_codes, w2
 SCORE_SIGMOID, SCORE_SOFTMAX = 0, 1   # MOE_SCORE_* of include/moe.h
 
 
-def _at(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+def _device_of(t, name: str) -> int:
+    """The current device, where the library launches, for a call whose first tensor is t."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device (GPU) tensor")
+    return torch.cuda.current_device()
 
 
-def _launch_stream(stream, *tensors):
-    """The stream to launch on (the current one by default).  The library launches on the
-    current device, so every tensor has to be there."""
-    device = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            raise ValueError(f"tensors must be on the current device (cuda:{device}), "
-                             f"got one on {t.device}")
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device)
-    return _stream(stream)
+def _arg(device: int, t, name: str, dtype, shape=None):
+    """Address of a contiguous tensor on the current device, after the checks of _need in one
+    pass (a small call's time is the host's)."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device
+            and (shape is None or t.shape == shape) and t.is_contiguous()):
+        return t.data_ptr()
+    _need(t, name, dtype, shape)
+    raise ValueError(f"{name} must be on the current device (cuda:{device}), where the library "
+                     f"launches, got one on {t.device}")
+
+
+def _opt_arg(device: int, t, name: str, dtype, shape=None):
+    return None if t is None else _arg(device, t, name, dtype, shape)
+
+
+def _stream_on(device: int, stream):
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
 def moe_route_groups_workspace_bytes(M: int, E: int) -> int:
     return int(load_library().moe_route_groups_workspace_bytes(M, E))
-
-
-def _need_bias(select_bias, E: int):
-    if select_bias is not None:
-        _need(select_bias, "select_bias", torch.float32, (E,))
 
 
 def moe_route_groups(x, router_w, select_bias, top_k: int, topk_ids, topk_w, workspace,
@@ -739,17 +745,16 @@ def moe_route_groups(x, router_w, select_bias, top_k: int, topk_ids, topk_w, wor
     (fp32 [E] or None) and expert groups; weights from the unbiased scores."""
     M, H = x.shape
     E = router_w.shape[0]
-    _need(x, "x", torch.bfloat16)
-    _need(router_w, "router_w", torch.bfloat16, (E, H))
-    _need_bias(select_bias, E)
-    _need(topk_ids, "topk_ids", torch.int32, (M, top_k))
-    _need(topk_w, "topk_w", torch.float32, (M, top_k))
-    _need(workspace, "workspace", torch.uint8)
+    dev = _device_of(x, "x")
     _check("moe_route_groups", load_library().moe_route_groups(
-        _at(x), _at(router_w), _at(select_bias), M, H, E, top_k, score, n_group, topk_group,
-        group_top, int(bool(renormalize)), float(scale), _at(topk_ids), _at(topk_w),
-        _at(workspace), workspace.numel(),
-        _launch_stream(stream, x, router_w, select_bias, topk_ids, topk_w, workspace)))
+        _arg(dev, x, "x", torch.bfloat16),
+        _arg(dev, router_w, "router_w", torch.bfloat16, (E, H)),
+        _opt_arg(dev, select_bias, "select_bias", torch.float32, (E,)), M, H, E, top_k, score,
+        n_group, topk_group, group_top, 1 if renormalize else 0, float(scale),
+        _arg(dev, topk_ids, "topk_ids", torch.int32, (M, top_k)),
+        _arg(dev, topk_w, "topk_w", torch.float32, (M, top_k)),
+        _arg(dev, workspace, "workspace", torch.uint8), workspace.numel(),
+        _stream_on(dev, stream)))
 
 
 def moe_route_logits(logits, select_bias, top_k: int, topk_ids, topk_w,
@@ -759,30 +764,29 @@ def moe_route_logits(logits, select_bias, top_k: int, topk_ids, topk_w,
     """moe_route_groups from fp32 logits [M, E], whose rows may lie further apart than E (a
     slice of the columns of a wider tensor)."""
     M, E = logits.shape
-    if not isinstance(logits, torch.Tensor) or logits.dtype != torch.float32:
+    dev = _device_of(logits, "logits")
+    if logits.dtype != torch.float32:
         raise TypeError("logits must be a float32 tensor")
-    if not logits.is_cuda:
-        raise ValueError("logits must be a device (GPU) tensor")
-    if (E > 1 and logits.stride(1) != 1) or (M > 1 and logits.stride(0) < E):
+    if logits.get_device() != dev:
+        raise ValueError(f"logits must be a tensor on the current device (cuda:{dev})")
+    ld, step = logits.stride()
+    if (E > 1 and step != 1) or (M > 1 and ld < E):
         raise ValueError("logits must have contiguous rows that do not overlap")
-    _need_bias(select_bias, E)
-    _need(topk_ids, "topk_ids", torch.int32, (M, top_k))
-    _need(topk_w, "topk_w", torch.float32, (M, top_k))
     _check("moe_route_logits", load_library().moe_route_logits(
-        _at(logits), logits.stride(0) if M > 1 else E, _at(select_bias), M, E, top_k, score,
-        n_group, topk_group, group_top, int(bool(renormalize)), float(scale), _at(topk_ids),
-        _at(topk_w), _launch_stream(stream, logits, select_bias, topk_ids, topk_w)))
+        logits.data_ptr(), ld if M > 1 else E,
+        _opt_arg(dev, select_bias, "select_bias", torch.float32, (E,)), M, E, top_k, score,
+        n_group, topk_group, group_top, 1 if renormalize else 0, float(scale),
+        _arg(dev, topk_ids, "topk_ids", torch.int32, (M, top_k)),
+        _arg(dev, topk_w, "topk_w", torch.float32, (M, top_k)), _stream_on(dev, stream)))
 
 
 def moe_i8_quantize(v, codes, scales, stream=None):
     """v [..., K] bf16 -> codes [..., K] int8 and scales [...] fp32, a scale for each row."""
-    _need(v, "v", torch.bfloat16)
-    K = v.shape[-1]
-    _need(codes, "codes", torch.int8, tuple(v.shape))
-    _need(scales, "scales", torch.float32, tuple(v.shape[:-1]))
+    dev = _device_of(v, "v")
+    at = _arg(dev, v, "v", torch.bfloat16)
     _check("moe_i8_quantize", load_library().moe_i8_quantize(
-        _at(v), scales.numel(), K, _at(codes), _at(scales),
-        _launch_stream(stream, v, codes, scales)))
+        at, scales.numel(), v.shape[-1], _arg(dev, codes, "codes", torch.int8, v.shape),
+        _arg(dev, scales, "scales", torch.float32, v.shape[:-1]), _stream_on(dev, stream)))
 
 
 def moe_i8_matmul_workspace_bytes(M: int, N: int, K: int) -> int:
@@ -794,18 +798,15 @@ def moe_i8_matmul(a, a_scales, w, w_scales, out, workspace=None, stream=None):
     a scale for each row) transposed."""
     M, K = a.shape
     N = w.shape[0]
-    _need(a, "a", torch.int8)
-    _need(a_scales, "a_scales", torch.float32, (M,))
-    _need(w, "w", torch.int8, (N, K))
-    _need(w_scales, "w_scales", torch.float32, (N,))
-    f32 = isinstance(out, torch.Tensor) and out.dtype == torch.float32
-    _need(out, "out", torch.float32 if f32 else torch.bfloat16, (M, N))
-    if workspace is not None:
-        _need(workspace, "workspace", torch.uint8)
+    dev = _device_of(a, "a")
+    f32 = isinstance(out, torch.Tensor) and out.dtype is torch.float32
     _check("moe_i8_matmul", load_library().moe_i8_matmul(
-        _at(a), _at(a_scales), _at(w), _at(w_scales), M, N, K, _at(out), int(f32),
-        _at(workspace), 0 if workspace is None else workspace.numel(),
-        _launch_stream(stream, a, a_scales, w, w_scales, out, workspace)))
+        _arg(dev, a, "a", torch.int8), _arg(dev, a_scales, "a_scales", torch.float32, (M,)),
+        _arg(dev, w, "w", torch.int8, (N, K)),
+        _arg(dev, w_scales, "w_scales", torch.float32, (N,)), M, N, K,
+        _arg(dev, out, "out", torch.float32 if f32 else torch.bfloat16, (M, N)), 1 if f32 else 0,
+        _opt_arg(dev, workspace, "workspace", torch.uint8),
+        0 if workspace is None else workspace.numel(), _stream_on(dev, stream)))
 
 
 def moe_i8_workspace_bytes(M: int, H: int, E: int, I: int, top_k: int, block: int) -> int:
@@ -824,35 +825,19 @@ def moe_forward_i8(x, router_w, select_bias, w13_codes, w13_scales, w2_codes, w2
     M, H = x.shape
     E, two_i, _ = w13_codes.shape
     I = two_i // 2
-    _need(x, "x", torch.bfloat16)
-    _need(router_w, "router_w", torch.bfloat16, (E, H))
-    _need_bias(select_bias, E)
-    _need(w13_codes, "w13_codes", torch.int8, (E, 2 * I, H))
-    _need(w13_scales, "w13_scales", torch.float32, (E, 2 * I))
-    _need(w2_codes, "w2_codes", torch.int8, (E, H, I))
-    _need(w2_scales, "w2_scales", torch.float32, (E, H))
-    _need(residual, "residual", torch.bfloat16, (M, H))
-    _need(norm_w, "norm_w", torch.bfloat16, (H,))
-    _need(out, "out", torch.bfloat16, (M, H))
-    _need(workspace, "workspace", torch.uint8)
-    if residual_out is not None:
-        _need(residual_out, "residual_out", torch.bfloat16, (M, H))
-    if topk_ids_out is not None:
-        _need(topk_ids_out, "topk_ids_out", torch.int32, (M, top_k))
-    if topk_w_out is not None:
-        _need(topk_w_out, "topk_w_out", torch.float32, (M, top_k))
+    dev = _device_of(x, "x")
     if sorted_ids_out is not None or block_expert_out is not None:
         cap = moe_align_capacity(M, top_k, E, block)
         if sorted_ids_out is not None:
-            _need(sorted_ids_out, "sorted_ids_out", torch.int32)
+            _arg(dev, sorted_ids_out, "sorted_ids_out", torch.int32)
             if sorted_ids_out.numel() < cap:
                 raise ValueError("sorted_ids_out smaller than the plan capacity")
         if block_expert_out is not None:
-            _need(block_expert_out, "block_expert_out", torch.int32)
+            _arg(dev, block_expert_out, "block_expert_out", torch.int32)
             if block_expert_out.numel() < cap // block:
                 raise ValueError("block_expert_out smaller than capacity / block")
     if num_padded_out is not None:
-        _need(num_padded_out, "num_padded_out", torch.int32)
+        _arg(dev, num_padded_out, "num_padded_out", torch.int32)
         if num_padded_out.numel() < 1:
             raise ValueError("num_padded_out must hold one entry")
     ev = None
@@ -861,14 +846,25 @@ def moe_forward_i8(x, router_w, select_bias, w13_codes, w13_scales, w2_codes, w2
             raise ValueError("stage_events must hold 6 events")
         ev = (ctypes.c_void_p * 6)(*[e.handle for e in stage_events])
     _check("moe_forward_i8", load_library().moe_forward_i8(
-        _at(x), _at(router_w), _at(select_bias), _at(w13_codes), _at(w13_scales),
-        _at(w2_codes), _at(w2_scales), _at(residual), _at(norm_w), float(eps), M, H, E, I,
-        top_k, block, score, n_group, topk_group, group_top, int(bool(renormalize)), float(scale),
-        _at(out), _at(residual_out), _at(topk_ids_out), _at(topk_w_out), _at(sorted_ids_out),
-        _at(block_expert_out), _at(num_padded_out), _at(workspace), workspace.numel(), ev,
-        _launch_stream(stream, x, router_w, select_bias, w13_codes, w13_scales, w2_codes,
-                       w2_scales, residual, norm_w, out, workspace, residual_out, topk_ids_out,
-                       topk_w_out, sorted_ids_out, block_expert_out, num_padded_out)))
+        _arg(dev, x, "x", torch.bfloat16),
+        _arg(dev, router_w, "router_w", torch.bfloat16, (E, H)),
+        _opt_arg(dev, select_bias, "select_bias", torch.float32, (E,)),
+        _arg(dev, w13_codes, "w13_codes", torch.int8, (E, 2 * I, H)),
+        _arg(dev, w13_scales, "w13_scales", torch.float32, (E, 2 * I)),
+        _arg(dev, w2_codes, "w2_codes", torch.int8, (E, H, I)),
+        _arg(dev, w2_scales, "w2_scales", torch.float32, (E, H)),
+        _arg(dev, residual, "residual", torch.bfloat16, (M, H)),
+        _arg(dev, norm_w, "norm_w", torch.bfloat16, (H,)), float(eps), M, H, E, I, top_k, block,
+        score, n_group, topk_group, group_top, 1 if renormalize else 0, float(scale),
+        _arg(dev, out, "out", torch.bfloat16, (M, H)),
+        _opt_arg(dev, residual_out, "residual_out", torch.bfloat16, (M, H)),
+        _opt_arg(dev, topk_ids_out, "topk_ids_out", torch.int32, (M, top_k)),
+        _opt_arg(dev, topk_w_out, "topk_w_out", torch.float32, (M, top_k)),
+        _opt_arg(dev, sorted_ids_out, "sorted_ids_out", torch.int32),
+        _opt_arg(dev, block_expert_out, "block_expert_out", torch.int32),
+        _opt_arg(dev, num_padded_out, "num_padded_out", torch.int32),
+        _arg(dev, workspace, "workspace", torch.uint8), workspace.numel(), ev,
+        _stream_on(dev, stream)))
 
 
 # ---------------------------------------------------------------------------------------
