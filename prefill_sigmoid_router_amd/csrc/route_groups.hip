@@ -139,7 +139,8 @@ __device__ __forceinline__ int wave_best(uint64_t key, int slot, int lane) {
 // whose sum then goes to fp64, and one more when a part's logit is stored in fp32: 40
 // roundings of at most 2^-23 of A = sum |x| |w| over the part (2^-24, doubled in case the
 // hardware truncates).  A comes from the same fragments with the sign bits cleared; its own
-// roundings are within 2^-10 of it.  (One running fp32 sum over the part: 88 to 144 roundings
+// roundings are within 2^-10 of it; the largest A of four neighbouring experts is kept for all
+// of them (a few per cent more, a quarter of the writes).  (One running fp32 sum over the part: 88 to 144 roundings
 // and three times as many choices that the bound leaves open.)
 //
 // 64 tokens x 64 experts x one part of K per workgroup, 2 x 2 waves of 32 x 32; 64-wide chunks
@@ -256,22 +257,19 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int e = e0 + (erow - kBlTile) + 16 * i + 4 * lg;
-      const size_t o = ((size_t)part * M + t) * E + e;
+      if (e >= E) continue;
+      const size_t row = (size_t)part * M + t;
+      float* l = logits + row * E + e;
+      const f32x4 a = aab[i][j];   // (rows past the last expert repeat it)
+      absdot[row * ((E + 3) / 4) + e / 4] = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
       if (E % 4 == 0) {
-        if (e < E) {
-          *reinterpret_cast<float4*>(logits + o) =
-              make_float4((float)sum[i][j][0], (float)sum[i][j][1], (float)sum[i][j][2],
-                          (float)sum[i][j][3]);
-          *reinterpret_cast<f32x4*>(absdot + o) = aab[i][j];
-        }
-        continue;
-      }
+        *reinterpret_cast<float4*>(l) = make_float4((float)sum[i][j][0], (float)sum[i][j][1],
+                                                    (float)sum[i][j][2], (float)sum[i][j][3]);
+      } else {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (e + q < E) {
-          logits[o + q] = (float)sum[i][j][q];
-          absdot[o + q] = aab[i][j][q];
-        }
+        for (int q = 0; q < 4; ++q)
+          if (e + q < E) l[q] = (float)sum[i][j][q];
+      }
     }
   }
 }
@@ -307,7 +305,6 @@ struct BoundedSource {
   const uint16_t *x, *wr;
   int parts, M, H;
   double rel;   // error of a partial logit over its |x| . |w| sum
-  int64_t ld;
   template <int SL>
   __device__ void get(int64_t t, int E, int lane, double (&l)[SL], double (&d)[SL]) const {
     constexpr int B = SL > 4 ? 2 : 4;   // parts in flight
@@ -317,12 +314,12 @@ struct BoundedSource {
       float v[B][SL], a[B][SL];
 #pragma unroll
       for (int p = 0; p < B; ++p) {
-        const int64_t row = ((int64_t)min(p0 + p, parts - 1) * M + t) * ld;
+        const int64_t row = (int64_t)min(p0 + p, parts - 1) * M + t;
 #pragma unroll
         for (int s = 0; s < SL; ++s) {
           const int e = min(lane + kWave * s, E - 1);
-          v[p][s] = logits[row + e];
-          a[p][s] = absdot[row + e];
+          v[p][s] = logits[row * E + e];
+          a[p][s] = absdot[row * ((E + 3) / 4) + e / 4];
         }
       }
 #pragma unroll
@@ -1153,7 +1150,7 @@ hipError_t launch_route_groups(const uint16_t* x, const uint16_t* wr, const floa
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
     const double rel = kBlRounds * 0x1p-23 * (1.0 + 0x1p-9);
-    return launch_select(BoundedSource{logits, absdot, x, wr, parts, M, H, rel, E}, bias, M, E,
+    return launch_select(BoundedSource{logits, absdot, x, wr, parts, M, H, rel}, bias, M, E,
                          top_k, rule, ids, w, s);
   }
   double* keys = static_cast<double*>(scratch);
