@@ -405,7 +405,9 @@ int moe_forward_mx(const uint16_t* x, const uint16_t* router_w, const float* rou
  *            the lower id (top_k <= topk_group * E / n_group); ids are those of the exact sums.
  *            Without a bias the logits are compared, which order as the scores do.
  *   topk_w   [M, top_k] fp32 out: s of the picks (without the bias), divided by their sum if
- *            renormalize is not 0 (a sum of 0 gives weights 0), times scale (finite).
+ *            renormalize is not 0 (a sum of 0 gives weights 0), times scale (finite).  From 256
+ *            tokens on moe_route_groups takes them from fp32 sums, and from exact ones where
+ *            the bound on those could move a weight by more than 2^-9 of itself.
  * An expert whose logit is -inf (masked) or NaN has no score: weight 0, nothing added to its
  * group's score, picked only after every scored expert of the groups that stay, in id order;
  * a group without a scored expert ranks last.  A token whose experts are all masked gets
@@ -455,11 +457,12 @@ int moe_i8_matmul(const int8_t* a, const float* a_scales, const int8_t* w, const
  * [E, 2I], w2_codes [E, H, I] + w2_scales [E, H]) and the router of moe_route_groups in place
  * of step 1.  x is quantized row by row (a scale per token); the up GEMM runs on the codes,
  * SwiGLU in fp32; act is quantized row by row (a scale per token and pick; between the two
- * it is held to 2^-14 of the largest of 32 neighbours); the down GEMM runs on the codes; finalize as in moe_forward.  Other arguments,
- * stage events (quantizing x counts to step 1, quantizing act to step 4) and outputs are
- * those of moe_forward.  H % 16 == 0 and I % 16 == 0, I <= 131072, M at most 2^24 and
- * M * H below 2^32 (MOE_ERR_UNSUPPORTED otherwise); codes and their scales 16-byte aligned; workspace of moe_i8_workspace_bytes bytes (0 for invalid sizes), 256-byte
- * aligned.
+ * it is held to 2^-15 of the largest of 32 neighbours); the down GEMM runs on the codes;
+ * finalize as in moe_forward.  Other arguments, stage events (quantizing x counts to step 1,
+ * quantizing act to step 4) and outputs are those of moe_forward.  H % 16 == 0 and
+ * I % 16 == 0, I <= 131072, M at most 2^24 (MOE_ERR_INVALID_ARG otherwise) and M * H below
+ * 2^32 (MOE_ERR_UNSUPPORTED otherwise); codes and their scales 16-byte aligned; workspace of
+ * moe_i8_workspace_bytes bytes (0 for invalid sizes), 256-byte aligned.
  */
 size_t moe_i8_workspace_bytes(int32_t M, int32_t H, int32_t E, int32_t I, int32_t top_k,
                               int32_t block);

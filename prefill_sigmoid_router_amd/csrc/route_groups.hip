@@ -465,6 +465,12 @@ static_assert(kSelWaves == 4 && kAsk % 2 == 0, "the sums and pairs above");
 // round of a k-step selection costs 500 cycles: M=8192, E=384, k=8 22 us.)
 enum Fast { kDone, kRedo, kOpen };
 
+// Bounded logits also make the weights: where a bound could move one by more than this part of
+// itself, the exact logit does.  (Sums of many bf16 products are a thousand times closer than
+// their bounds, so that weights are within 2e-7 at H=7168; only large terms that cancel reach
+// this.)
+constexpr double kWeightBound = 0x1p-9;
+
 __device__ __forceinline__ uint32_t order32(float f) {   // orders as the numbers do
   const uint32_t bits = __float_as_uint(f + 0.0f);
   return (int)bits < 0 ? ~bits : bits | 0x80000000u;
@@ -693,11 +699,13 @@ __device__ __forceinline__ Fast collect_fast(const double (&l)[SL], const double
 }
 
 // again: after exact logits came in, which the fp32 intervals do not hold
-template <int SL>
-__device__ __forceinline__ Fast rank_fast(const double (&l)[SL], const Candidate& mine, bool again,
-                                          bool bias, int64_t t, int top_k, const GroupRule& rule,
-                                          float top, int found, double* s_val, uint32_t* s_key,
-                                          int lane, bool& ask, int32_t* ids, float* weights) {
+template <int SL, bool BOUNDS>
+__device__ __forceinline__ Fast rank_fast(const double (&l)[SL], const double (&d)[SL],
+                                          const Candidate& mine, bool again, bool bias, int64_t t,
+                                          int E, int top_k, const GroupRule& rule, float top,
+                                          int found, double* s_val, uint32_t* s_key, int lane,
+                                          uint32_t& redo, bool& ask, int32_t* ids,
+                                          float* weights) {
   const bool cand = lane < found;
   const double ex = exp(rule.softmax ? mine.l - (double)top : -mine.l);
   const double score = rule.softmax ? ex : 1.0 / (1.0 + ex);
@@ -750,15 +758,30 @@ __device__ __forceinline__ Fast rank_fast(const double (&l)[SL], const Candidate
     }
   }
   const bool picked = cand && rank < top_k;
+  if (BOUNDS) {
+    ask = picked && mine.d * (rule.softmax ? 1.0 : ex * score) > kWeightBound;
+    if (__any(ask)) return kRedo;
+  }
   double divisor = 1.0;
   if (rule.renorm) {
     divisor = wave_sum_f64(picked ? score : 0.0);
   } else if (rule.softmax) {
-    double total = 0.0;
+    double total = 0.0, off = 0.0;
 #pragma unroll
     for (int s = 0; s < SL; ++s)
-      if (l[s] > -INFINITY) total += exp(l[s] - (double)top);
+      if (l[s] > -INFINITY) {
+        const double e = exp(l[s] - (double)top);
+        total += e;
+        off += e * d[s];
+      }
     divisor = wave_sum_f64(total);
+    if (BOUNDS && wave_sum_f64(off) > kWeightBound * divisor) {   // the divisor's own terms
+#pragma unroll
+      for (int s = 0; s < SL; ++s)
+        if (l[s] > -INFINITY && exp(l[s] - (double)top) * d[s] * E > kWeightBound * divisor)
+          redo |= 1u << s;
+      return kRedo;
+    }
   }
   const double factor = divisor > 0.0 ? (double)rule.scale / divisor : 0.0;
   if (picked) {
@@ -990,6 +1013,17 @@ __device__ __forceinline__ Fast select_fp64(const double (&l)[SL], const double 
       if (__any(redo != 0)) return kRedo;
     }
   }
+  if (BOUNDS) {   // as in rank_fast; a softmax's divisor too
+    const bool all = rule.softmax && !rule.renorm;
+#pragma unroll
+    for (int s = 0; s < SL; ++s) {
+      const double part = d[s] * (rule.softmax ? 1.0 : 1.0 - score[s]);
+      if ((taken >> s & 1) && score[s] > 0.0 && part > kWeightBound) redo |= 1u << s;
+      if (all && live[s] && score[s] * d[s] * E > kWeightBound * divisor) redo |= 1u << s;
+    }
+    wave_lds_fence();
+    if (__any(redo != 0)) return kRedo;
+  }
   double factor = (double)rule.scale / divisor;
   if (rule.renorm) {
     double total = 0.0;
@@ -1053,8 +1087,8 @@ __global__ __launch_bounds__(kSelWaves* kWave, 2) void select_groups_kernel(
       stage = got == kDone ? kRank : kSlow;
     }
     if (stage == kRank) {
-      got = rank_fast<SL>(l, mine, again, bias != nullptr, t, top_k, rule, top, found, s_c, s_key,
-                          lane, ask, ids, weights);
+      got = rank_fast<SL, BOUNDS>(l, d, mine, again, bias != nullptr, t, E, top_k, rule, top, found,
+                                  s_c, s_key, lane, redo, ask, ids, weights);
       again = true;
       if (got != kOpen) return got;
       stage = kSlow;

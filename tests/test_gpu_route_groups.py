@@ -217,6 +217,27 @@ def test_large_values(B, dev):
         _check_x(B, x, wr, None, 4, rule, dev)
 
 
+@pytest.mark.parametrize("rule", [dict(), dict(renormalize=False), dict(softmax=True),
+                                  dict(softmax=True, renormalize=False),
+                                  dict(n_group=4, topk_group=2, group_top=2)])
+@pytest.mark.parametrize("size", [100.0, 20000.0])
+@pytest.mark.parametrize("biased", [False, True])
+def test_weights_where_large_terms_cancel(B, dev, rule, size, biased):
+    """Two halves of the row whose products cancel but for ordinary logits: the fp32 sums are
+    off by parts of the terms' size.  A weight may be off by twice 2^-9 of itself: 2^-9 from
+    its own logit, 2^-9 from those of what it is divided by."""
+    x, wr, bias = _inputs(300, 1024, 64, dev, seed=12)
+    x[:, 256:512] = size / 256
+    x[:, 768:] = -size / 256
+    wr[:, 256:512] = wr[:, 768:] = 1.0
+    b = bias if biased else None
+    ids, w = _run_x(B, x, wr, b, 6, rule, dev)
+    r, _ = _rule(rule)
+    rid, rw = orc.route(bits(x), bits(wr), None if b is None else b.cpu().numpy(), 6, **r)
+    assert np.array_equal(ids.cpu().numpy(), rid)
+    assert (np.abs(w.cpu().numpy() - rw) <= 2 * 2 ** -9 * np.abs(rw) * (1 + 2 ** -6)).all()
+
+
 @pytest.mark.parametrize("M", [8, 512])
 def test_graph_replays_equal_eager_calls(B, dev, M):
     rule = dict(n_group=4, topk_group=2, group_top=2, scale=2.5)
