@@ -441,7 +441,7 @@ int moe_route_logits(const float* logits, int64_t ld, const float* select_bias,
  *   per token.  K % 16 == 0, 16 <= K <= 131072; v and codes 16-byte, scales 4-byte aligned.
  * moe_i8_matmul: out[m, n] = a_scales[m] * w_scales[n] * sum_k a[m, k] * w[n, k] for a [M, K]
  *   and w [N, K] int8 (K as above); the sums are exact (int32), the scaling fp32.  out [M, N]
- *   is bf16, or fp32 with out_f32 = 1.  M >= 0 and N >= 1 are any.  a, w, w_scales and out
+ *   is bf16, or fp32 with out_f32 = 1.  0 <= M <= 2^30, 1 <= N <= 2^26.  a, w, w_scales and out
  *   16-byte, a_scales 4-byte aligned.  The workspace holds moe_i8_matmul_workspace_bytes
  *   bytes, 256-byte aligned (it may be NULL where that is 0); its contents are not kept.
  */
@@ -460,9 +460,9 @@ int moe_i8_matmul(const int8_t* a, const float* a_scales, const int8_t* w, const
  * it is held to 2^-15 of the largest of 32 neighbours); the down GEMM runs on the codes;
  * finalize as in moe_forward.  Other arguments, stage events (quantizing x counts to step 1,
  * quantizing act to step 4) and outputs are those of moe_forward.  H % 16 == 0 and
- * I % 16 == 0, I <= 131072, M at most 2^24 (MOE_ERR_INVALID_ARG otherwise) and M * H below
- * 2^32 (MOE_ERR_UNSUPPORTED otherwise); codes and their scales 16-byte aligned; workspace of
- * moe_i8_workspace_bytes bytes (0 for invalid sizes), 256-byte aligned.
+ * I % 16 == 0, I <= 131072; M below 2^22, M * H below 2^32 and moe_align_capacity below 2^26
+ * (MOE_ERR_UNSUPPORTED otherwise); codes and their scales 16-byte aligned; workspace of
+ * moe_i8_workspace_bytes bytes (0 for sizes that are refused), 256-byte aligned.
  */
 size_t moe_i8_workspace_bytes(int32_t M, int32_t H, int32_t E, int32_t I, int32_t top_k,
                               int32_t block);

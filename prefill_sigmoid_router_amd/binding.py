@@ -764,9 +764,9 @@ def moe_route_logits(logits, select_bias, top_k: int, topk_ids, topk_w,
     """moe_route_groups from fp32 logits [M, E], whose rows may lie further apart than E (a
     slice of the columns of a wider tensor)."""
     M, E = logits.shape
-    dev = _device_of(logits, "logits")
-    if logits.dtype != torch.float32:
+    if not isinstance(logits, torch.Tensor) or logits.dtype != torch.float32:
         raise TypeError("logits must be a float32 tensor")
+    dev = _device_of(logits, "logits")
     if logits.get_device() != dev:
         raise ValueError(f"logits must be a tensor on the current device (cuda:{dev})")
     ld, step = logits.stride()

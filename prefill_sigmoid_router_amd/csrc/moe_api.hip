@@ -683,6 +683,7 @@ namespace {
 constexpr int kMaxGroups = 64;
 constexpr int kMaxRouteTokens = 1 << 24;   // a wave per token: 2^30 threads
 constexpr int kMaxI8K = 131072;   // 127^2 * kMaxI8K < 2^31: int32 sums are exact
+constexpr int kMaxI8Rows = 1 << 30, kMaxI8Columns = 1 << 26;   // a tile's end fits in 32 bits
 
 bool make_rule(int32_t E, int32_t top_k, int32_t score, int32_t n_group, int32_t topk_group,
                int32_t group_top, int32_t renormalize, float scale, moe::GroupRule* rule) {
@@ -724,7 +725,14 @@ bool i8_sizes_ok(int32_t M, int32_t H, int32_t E, int32_t I, int32_t top_k) {
   return sizes_ok(M, H, E, I, top_k) && H % 16 == 0 && I <= kMaxI8K;
 }
 
-// Token-tile height of the grouped int8 GEMMs: 64 rows below 64 expected tokens per expert.
+// What the launches' grids (fewer than 2^32 threads: 1024 for a token in finalize, 64 for a
+// row of act) and the up GEMM's 32-bit offsets into the tokens' codes hold.
+bool i8_grids_ok(int32_t M, int32_t H, int32_t E, int32_t top_k, int32_t block) {
+  return M < (1 << 22) && (int64_t)M * H < ((int64_t)1 << 32) &&
+         capacity_of(M, top_k, E, block) < ((size_t)1 << 26);
+}
+
+// Token-tile height of the grouped int8 GEMMs, by the tokens that an expert can expect.
 int i8_tile_rows(int32_t M, int32_t E, int32_t top_k) {
   const int64_t per_expert = (int64_t)M * top_k / E;
   return per_expert < 32 ? 64 : per_expert < 96 ? 128 : 256;
@@ -768,7 +776,8 @@ int moe_route_logits(const float* logits, int64_t ld, const float* select_bias, 
   moe::GroupRule rule;
   if (!make_rule(E, top_k, score, n_group, topk_group, group_top, renormalize, scale, &rule))
     return MOE_ERR_INVALID_ARG;
-  if (M < 0 || M > kMaxRouteTokens || ld < E || ld > ((int64_t)1 << 32) || (int64_t)M * top_k >= ((int64_t)1 << 31))
+  if (M < 0 || M > kMaxRouteTokens || ld < E || ld > ((int64_t)1 << 32) ||
+      (int64_t)M * top_k >= ((int64_t)1 << 31))
     return MOE_ERR_INVALID_ARG;
   if (M == 0) return MOE_OK;
   if (!logits || !topk_ids || !topk_w || !aligned(logits, 4) || !aligned(topk_ids, 4) ||
@@ -798,7 +807,8 @@ size_t moe_i8_matmul_workspace_bytes(int32_t M, int32_t N, int32_t K) {
 int moe_i8_matmul(const int8_t* a, const float* a_scales, const int8_t* w, const float* w_scales,
                   int32_t M, int32_t N, int32_t K, void* out, int32_t out_f32, void* workspace,
                   size_t workspace_bytes, moe_stream_t stream) {
-  if (M < 0 || N < 1 || K < 16 || K % 16 != 0 || K > kMaxI8K || (out_f32 != 0 && out_f32 != 1))
+  if (M < 0 || M > kMaxI8Rows || N < 1 || N > kMaxI8Columns || K < 16 || K % 16 != 0 ||
+      K > kMaxI8K || (out_f32 != 0 && out_f32 != 1))
     return MOE_ERR_INVALID_ARG;
   if (M == 0) return MOE_OK;
   if (!a || !a_scales || !w || !w_scales || !out || !aligned(a, 16) || !aligned(a_scales, 4) ||
@@ -813,7 +823,9 @@ int moe_i8_matmul(const int8_t* a, const float* a_scales, const int8_t* w, const
 
 size_t moe_i8_workspace_bytes(int32_t M, int32_t H, int32_t E, int32_t I, int32_t top_k,
                               int32_t block) {
-  if (!i8_sizes_ok(M, H, E, I, top_k) || !gemm_block_ok(block)) return 0;
+  if (!i8_sizes_ok(M, H, E, I, top_k) || !gemm_block_ok(block) ||
+      !i8_grids_ok(M, H, E, top_k, block))
+    return 0;
   return i8_layout_of(M, H, E, I, top_k, block).total;
 }
 
@@ -828,10 +840,10 @@ int moe_forward_i8(const uint16_t* x, const uint16_t* router_w, const float* sel
                    void* workspace, size_t workspace_bytes, const moe_event_t* stage_events,
                    moe_stream_t stream) {
   moe::GroupRule rule;
-  if (!i8_sizes_ok(M, H, E, I, top_k) || M > kMaxRouteTokens || !(eps > 0.0f) || !isfinite(eps) ||
+  if (!i8_sizes_ok(M, H, E, I, top_k) || !(eps > 0.0f) || !isfinite(eps) ||
       !make_rule(E, top_k, score, n_group, topk_group, group_top, renormalize, scale, &rule))
     return MOE_ERR_INVALID_ARG;
-  if (!gemm_block_ok(block) || (int64_t)M * H >= ((int64_t)1 << 32)) return MOE_ERR_UNSUPPORTED;
+  if (!gemm_block_ok(block) || !i8_grids_ok(M, H, E, top_k, block)) return MOE_ERR_UNSUPPORTED;
   if (M == 0) return MOE_OK;
   if (!x || !router_w || !w13_codes || !w13_scales || !w2_codes || !w2_scales || !residual ||
       !norm_w || !out)
@@ -846,7 +858,6 @@ int moe_forward_i8(const uint16_t* x, const uint16_t* router_w, const float* sel
       (num_padded_out && !aligned(num_padded_out, 4)))
     return MOE_ERR_INVALID_ARG;
   const size_t cap = capacity_of(M, top_k, E, block);
-  if (cap >= ((size_t)1 << 31)) return MOE_ERR_INVALID_ARG;
   const I8Layout L = i8_layout_of(M, H, E, I, top_k, block);
   if (!workspace || !aligned(workspace, kAlign) || workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
 

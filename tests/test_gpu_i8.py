@@ -252,6 +252,10 @@ LAYERS = [  # M, H, E, I, k, block, rule: tokens per expert from 0.1 to over 128
     (203, 512, 60, 352, 4, 32, dict(softmax=True)), (130, 256, 4, 256, 1, 128, dict()),
     (300, 768, 8, 512, 4, 64, GROUPED), (600, 400, 8, 256, 3, 16, dict(softmax=True, renormalize=False)),
     (290, 16, 4, 16, 2, 16, dict()), (1, 16, 1, 16, 1, 16, dict()),
+    # both products long enough in K for the step streams, at each token tile height
+    (40, 656, 4, 768, 2, 16, dict()), (77, 1024, 8, 640, 4, 32, GROUPED),
+    (205, 768, 4, 1408, 1, 16, dict()), (333, 896, 8, 640, 4, 64, GROUPED),
+    (450, 784, 4, 768, 2, 16, dict(softmax=True)), (290, 1280, 4, 896, 3, 64, dict(scale=2.5)),
 ]
 
 
@@ -322,6 +326,51 @@ def test_layer_graph_replays_equal_eager_calls(B, dev, M):
         torch.cuda.synchronize()
         want, _ = _run_layer(B, L, k, block, GROUPED, dev)
         assert torch.equal(out, want["out"])
+
+
+def test_two_layers_at_once_on_two_streams(B, dev):
+    layers = [_layer_inputs(B, M, 768, 8, 640, dev, seed=20 + M) for M in (9, 300)]
+    want = [_run_layer(B, L, 4, 16, GROUPED, dev)[0] for L in layers]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [torch.full_like(w["out"], float("nan")) for w in want]
+    room = [torch.empty_like(w["ws"]) for w in want]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for L, s, o, ws in zip(layers, streams, outs, room):
+            B.moe_forward_i8(L["x"], L["wr"], L["bias"], L["w13"], L["s13"], L["w2"], L["s2"],
+                             L["residual"], L["g"], 1e-5, 4, 16, o, ws, n_group=4, topk_group=2,
+                             group_top=2, scale=2.5, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w["out"]) for o, w in zip(outs, want))
+
+
+def test_a_workspace_of_more_tokens_does_for_fewer(B, dev):
+    H, E, I, k, block = 768, 8, 640, 4, 16
+    ws = torch.empty(B.moe_i8_workspace_bytes(300, H, E, I, k, block), dtype=torch.uint8, device=dev)
+    for M in (300, 5, 260, 1, 130):
+        assert B.moe_i8_workspace_bytes(M, H, E, I, k, block) <= ws.numel()
+        L = _layer_inputs(B, M, H, E, I, dev, seed=M)
+        want = _run_layer(B, L, k, block, GROUPED, dev)[0]["out"]
+        out = torch.full_like(want, float("nan"))
+        B.moe_forward_i8(L["x"], L["wr"], L["bias"], L["w13"], L["s13"], L["w2"], L["s2"],
+                         L["residual"], L["g"], 1e-5, k, block, out, ws, n_group=4, topk_group=2,
+                         group_top=2, scale=2.5)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
+def test_tensors_of_another_device_are_refused(B, dev, monkeypatch):
+    v = torch.zeros(4, 32, dtype=torch.bfloat16, device=dev)
+    codes, scales = _quantize(B, v)
+    l, ids = torch.zeros(4, 8, device=dev), torch.zeros(4, 2, dtype=torch.int32, device=dev)
+    out = torch.empty(4, 4, device=dev)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError, match="current device"):
+        B.moe_i8_quantize(v, codes, scales)
+    with pytest.raises(ValueError, match="current device"):
+        B.moe_i8_matmul(codes, scales, codes, scales, out)
+    with pytest.raises(ValueError, match="current device"):
+        B.moe_route_logits(l, None, 2, ids, torch.zeros(4, 2, device=dev))
 
 
 def test_layer_beside_a_shared_expert_on_the_same_rows(B, dev):

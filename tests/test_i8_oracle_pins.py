@@ -158,6 +158,20 @@ def test_forward_i8_refuses_on_the_host(lib, bad, code):
     assert _forward(lib, **bad) == code
 
 
+@pytest.mark.parametrize("sizes", [dict(M=1 << 22, H=16, I=16), dict(M=1 << 19, H=8192, I=16),
+                                   dict(M=1 << 21, H=16, I=16, E=64, k=32)])
+def test_forward_i8_refuses_more_than_its_grids_hold(lib, sizes):
+    a = dict(E=8, k=2)
+    a.update(sizes)
+    assert _forward(lib, **sizes) == -2
+    assert lib.moe_i8_workspace_bytes(a["M"], a["H"], a["E"], a["I"], a["k"], 16) == 0
+
+
+@pytest.mark.parametrize("bad", [dict(M=(1 << 30) + 1), dict(N=(1 << 26) + 1)])
+def test_i8_matmul_refuses_more_than_its_grids_hold(lib, bad):
+    assert _matmul(lib, **bad) == -1
+
+
 def test_no_rows_is_a_success(lib):
     assert _groups(lib, M=0, x=None, ids=None, ws=None, wsb=0) == 0
     assert _logits(lib, M=0, l=None, ids=None) == 0
