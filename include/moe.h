@@ -405,8 +405,8 @@ int moe_forward_mx(const uint16_t* x, const uint16_t* router_w, const float* rou
  *            the lower id (top_k <= topk_group * E / n_group); ids are those of the exact sums.
  *            Without a bias the logits are compared, which order as the scores do.
  *   topk_w   [M, top_k] fp32 out: s of the picks (without the bias), divided by their sum if
- *            renormalize is not 0 (a sum of 0 gives weights 0), times scale (finite).  From 256
- *            tokens on moe_route_groups takes them from fp32 sums, and from exact ones where
+ *            renormalize is not 0 (a sum of 0 gives weights 0), times scale (finite).  For
+ *            many tokens moe_route_groups takes them from fp32 sums, and from exact ones where
  *            the bound on those could move a weight by more than 2^-9 of itself.
  * An expert whose logit is -inf (masked) or NaN has no score: weight 0, nothing added to its
  * group's score, picked only after every scored expert of the groups that stay, in id order;

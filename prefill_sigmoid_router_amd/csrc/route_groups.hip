@@ -150,12 +150,14 @@ constexpr int kBlTile = 64, kBlStages = 4, kBlRounds = 40;
 
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void bounded_logits_kernel(
     const uint16_t* __restrict__ x, const uint16_t* __restrict__ wr, int M, int H, int E, int parts,
-    int kpart, int per_xcd, float* __restrict__ logits, float* __restrict__ absdot) {
+    int kpart, int per_xcd, float* __restrict__ logits, float* __restrict__ absdot,
+    int* __restrict__ count) {
   constexpr int STAGE = 2 * kBlTile * 128, PPW = 4;
   __shared__ __align__(16) unsigned char lds[kBlStages * STAGE];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int li = lane & 15, lg = lane >> 4, rr = lane >> 3;
   const int etiles = (E + kBlTile - 1) / kBlTile, ttiles = (M + kBlTile - 1) / kBlTile;
+  if (count && blockIdx.x == 0 && threadIdx.x == 0) *count = 0;   // of the selection that follows
   const int slot = blockIdx.x / kXcds, item = (blockIdx.x % kXcds) * per_xcd + slot;
   if (slot >= per_xcd || item >= etiles * ttiles * parts) return;
   const int e0 = item % etiles * kBlTile;
@@ -276,7 +278,11 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 
 // Logits of a token: fp64 keys, the caller's fp32 logits, or fp32 MFMA partial logits with
 // their |x| . |w| sums (bounded_logits_kernel), which bound their error.  -inf past the last.
-struct KeySource {
+struct SameRows {   // row t of the source is token t
+  __device__ int64_t rows(int M) const { return M; }
+  __device__ int64_t token(int64_t row) const { return row; }
+};
+struct KeySource : SameRows {
   const double* keys;
   int64_t ld;
   template <int SL>
@@ -288,7 +294,24 @@ struct KeySource {
     }
   }
 };
-struct LogitSource {
+// Tokens for which every expert's exact logit is needed, in any order: *count of them were
+// asked for, the first `room` have a row.
+struct TokenList {
+  int *count, *tokens;
+  int room;
+};
+struct ListSource {   // exact logits of listed tokens
+  const double* keys;
+  int64_t ld;
+  TokenList list;
+  __device__ int64_t rows(int) const { return min(*list.count, list.room); }
+  __device__ int64_t token(int64_t row) const { return list.tokens[row]; }
+  template <int SL>
+  __device__ void get(int64_t row, int E, int lane, double (&l)[SL], double (&d)[SL]) const {
+    KeySource{{}, keys, ld}.get<SL>(row, E, lane, l, d);
+  }
+};
+struct LogitSource : SameRows {
   const float* logits;
   int64_t ld;
   template <int SL>
@@ -300,11 +323,12 @@ struct LogitSource {
     }
   }
 };
-struct BoundedSource {
+struct BoundedSource : SameRows {
   const float *logits, *absdot;
   const uint16_t *x, *wr;
   int parts, M, H;
   double rel;   // error of a partial logit over its |x| . |w| sum
+  TokenList list;   // softmax with a bias only
   template <int SL>
   __device__ void get(int64_t t, int E, int lane, double (&l)[SL], double (&d)[SL]) const {
     constexpr int B = SL > 4 ? 2 : 4;   // parts in flight
@@ -350,20 +374,22 @@ struct Candidate {
   uint32_t lo, hi;   // ends of the fp32 interval of what orders the picks, as order32 keys
 };
 
-// Exact logits that the workgroup's waves ask for: fp64 dot products, every wave a quarter of
-// the row, the quarters added in wave order, so that equal rows of the router weight give
-// equal sums.  Each wave leaves up to kAsk experts a round.
-constexpr int kAsk = 8;   // experts, worked off two at a time (most tokens that ask have two)
+// Exact logits that the workgroup's waves ask for: fp64 dot products in quarters of the row,
+// added in order, so that equal rows of the router weight give equal sums.  Each wave leaves up
+// to kAsk experts a round, worked off two at a time (most tokens that ask have two): each pair
+// by all waves, a quarter each, or, where there are many, by one.
+constexpr int kAsk = 32;
 struct ExactQueue {
   int expert[kSelWaves][kAsk];   // -1: none
+  int asked[kSelWaves];
   double part[kSelWaves][kAsk][kSelWaves];
 };
 
-// One wave's quarter of N dot products of row t of x, B chunks of 8 values a lane in flight per
-// row (4: H = 7168 in one batch).
+// A quarter of N dot products of row t of x, B chunks of 8 values a lane in flight per row
+// (4: H = 7168 in one batch).
 template <int N, int B>
 __device__ __forceinline__ void quarter_dots(const BoundedSource& q, int64_t t, const int* experts,
-                                             int wave, int lane, double (&sum)[N]) {
+                                             int quarter, int lane, double (&sum)[N]) {
   const uint16_t* xr = q.x + t * q.H;
   const uint16_t* w[N];
 #pragma unroll
@@ -371,7 +397,7 @@ __device__ __forceinline__ void quarter_dots(const BoundedSource& q, int64_t t, 
     w[i] = q.wr + (size_t)max(experts[i], 0) * q.H;
     sum[i] = 0.0;
   }
-  const int n = q.H >> 3, beg = n * wave / kSelWaves, end = n * (wave + 1) / kSelWaves;
+  const int n = q.H >> 3, beg = n * quarter / kSelWaves, end = n * (quarter + 1) / kSelWaves;
   for (int c0 = beg + lane; c0 < end; c0 += kWave * B) {
     u32x4 xv[B], v[N][B];
 #pragma unroll
@@ -420,15 +446,23 @@ __device__ __forceinline__ bool exact_round(const BoundedSource& q, ExactQueue& 
     if (at[s] >= 0) queue.expert[wave][place] = s < SL ? lane + kWave * s : mine.id;
     asked += __popcll(who);
   }
+  if (lane == 0) queue.asked[wave] = min(asked, kAsk);
   if (!__syncthreads_or(asked)) return false;
+  int pairs = 0;
+  for (int w = 0; w < kSelWaves; ++w) pairs += (queue.asked[w] + 1) / 2;
+  const bool split = pairs < 2 * kSelWaves;   // each pair over the waves, or a pair per wave
+  int pair = 0;
   for (int w = 0; w < kSelWaves; ++w) {
     const int64_t t = min(t0 + w, M - 1);
-    for (int i = 0; i < kAsk && queue.expert[w][i] >= 0; i += 2) {
-      double sum[2];
-      quarter_dots<2, (SL > 4 ? 2 : 4)>(q, t, &queue.expert[w][i], wave, lane, sum);
-      if (lane == 0) {
+    for (int i = 0; i < queue.asked[w]; i += 2, ++pair) {
+      if (!split && pair % kSelWaves != wave) continue;
+      for (int quarter = split ? wave : 0; quarter < (split ? wave + 1 : kSelWaves); ++quarter) {
+        double sum[2];
+        quarter_dots<2, (SL > 4 ? 2 : 4)>(q, t, &queue.expert[w][i], quarter, lane, sum);
+        if (lane == 0) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) queue.part[w][i + j][wave] = sum[j];
+          for (int j = 0; j < 2; ++j) queue.part[w][i + j][quarter] = sum[j];
+        }
       }
     }
   }
@@ -454,8 +488,8 @@ static_assert(kSelWaves == 4 && kAsk % 2 == 0, "the sums and pairs above");
 
 // Selection of a token by fp32 values with bounds, in two steps: groups and candidates
 // (collect_fast), order and weights (rank_fast).  kDone: no bound can turn a choice.  kRedo:
-// `redo` or `ask` mark the experts whose exact logits can settle it.  kOpen: the fp64 code
-// below decides.  Each value's bound covers its logit's (|l - exact| <= d, and l's rounding
+// `redo` or `ask` mark the experts whose exact logits can settle it.  kAll: every one is needed
+// (a softmax's divisor decides).  kOpen: the fp64 code below decides.  Each value's bound covers its logit's (|l - exact| <= d, and l's rounding
 // to fp32) and the fp32 arithmetic: __expf of z is within (|z| + 4) 2^-22 of itself,
 // reciprocals and products within a few 2^-24.
 //
@@ -463,7 +497,7 @@ static_assert(kSelWaves == 4 && kAsk % 2 == 0, "the sums and pairs above");
 // the k-th largest of all; what can reach it (k and a few) is collected, one per lane, and
 // ranked by counting the intervals above each, or, where intervals meet, the fp64 values.  (A
 // round of a k-step selection costs 500 cycles: M=8192, E=384, k=8 22 us.)
-enum Fast { kDone, kRedo, kOpen };
+enum Fast { kDone, kRedo, kAll, kOpen };
 
 // Bounded logits also make the weights: where a bound could move one by more than this part of
 // itself, the exact logit does.  (Sums of many bf16 products are a thousand times closer than
@@ -515,16 +549,21 @@ __device__ __forceinline__ Fast collect_fast(const double (&l)[SL], const double
       for (int s = 0; s < SL; ++s) {
         const float z = v[s] - top;
         c[s] = live >> s & 1 ? __expf(z) : 0.0f;
-        dc[s] = c[s] * (1.2f * dv[s] + (4.0f - z) * u);
+        dc[s] = c[s] * (dv[s] + 0.6f * dv[s] * dv[s] + (4.0f - z) * u);
         total += c[s];
       }
       if (bias) {
+        float off = 0.0f;
+#pragma unroll
+        for (int s = 0; s < SL; ++s) off += dc[s];
         total = wave_sum_f32(total);
         const float inv = total > 0.0f ? __builtin_amdgcn_rcpf(total) : 0.0f;
+        off = bounded ? wave_sum_f32(off) * inv * 1.001f : 0.0f;   // the divisor's, of itself
+        off += 2.0f * off * off;
 #pragma unroll
-        for (int s = 0; s < SL; ++s) {   // (given logits only: the divisor has no bound else)
+        for (int s = 0; s < SL; ++s) {
           c[s] *= inv;
-          dc[s] = dc[s] * inv + c[s] * (80.0f * u);
+          dc[s] = dc[s] * inv + c[s] * (off + 80.0f * u);
         }
       }
     } else {
@@ -533,7 +572,8 @@ __device__ __forceinline__ Fast collect_fast(const double (&l)[SL], const double
         const float ex = __expf(-fmaxf(v[s], -80.0f));
         const float sc = __builtin_amdgcn_rcpf(1.0f + ex);
         c[s] = live >> s & 1 ? sc : 0.0f;
-        dc[s] = c[s] * (fminf(1.0f, ex * sc) * (1.2f * dv[s] + (fabsf(v[s]) + 4.0f) * u) + 2.0f * u);
+        const float grow = dv[s] + 0.6f * dv[s] * dv[s] + (fabsf(v[s]) + 4.0f) * u;
+        dc[s] = c[s] * (fminf(1.0f, ex * sc) * grow + 2.0f * u);
         if (v[s] < -79.0f) dc[s] += 1e-34f;
       }
     }
@@ -629,7 +669,11 @@ __device__ __forceinline__ Fast collect_fast(const double (&l)[SL], const double
           if (s_d[ge] != 0.0f && c[s] + dc[s] >= s_v[ge]) redo |= 1u << s;
         }
       }
-      return __any(redo != 0) ? kRedo : kOpen;
+      if (__any(redo != 0)) return kRedo;
+      bool inexact = false;
+#pragma unroll
+      for (int s = 0; s < SL; ++s) inexact |= d[s] > 0.0;
+      return rule.softmax && bias && __any(inexact) ? kAll : kOpen;
     }
     stay = __ballot(in);
     wave_lds_fence();
@@ -649,19 +693,16 @@ __device__ __forceinline__ Fast collect_fast(const double (&l)[SL], const double
     inside |= (uint32_t)is << s;
     if (is) largest = max(largest, order32(v[s] - dv[s]));
   }
-  uint32_t limit = 0;
-  if (SL > 1) {
-    s_key[lane] = largest;
-    wave_lds_fence();
-    int reached = 0;
+  s_key[lane] = largest;
+  wave_lds_fence();
+  int reached = 0;
 #pragma unroll
-    for (int j = 0; j < kWave; j += 4) {
-      const uint4 o = *reinterpret_cast<const uint4*>(s_key + j);
-      reached += (o.x >= largest) + (o.y >= largest) + (o.z >= largest) + (o.w >= largest);
-    }
-    limit = wave_max_u32(reached >= top_k ? largest : 0u);
-    wave_lds_fence();
+  for (int j = 0; j < kWave; j += 4) {
+    const uint4 o = *reinterpret_cast<const uint4*>(s_key + j);
+    reached += (o.x >= largest) + (o.y >= largest) + (o.z >= largest) + (o.w >= largest);
   }
+  const uint32_t limit = wave_max_u32(reached >= top_k ? largest : 0u);
+  wave_lds_fence();
   // candidates: what can reach the limit, one per lane, in slot and lane order
   double* s_l = reinterpret_cast<double*>(s_v);   // s_v and s_d are free: 64 of each
   double* s_b = s_l + kWave;
@@ -715,45 +756,67 @@ __device__ __forceinline__ Fast rank_fast(const double (&l)[SL], const double (&
     reach += (uint32_t)__builtin_amdgcn_readlane((int)mine.hi, j) >= mine.lo ? 1 : 0;
   }
   if (__any(cand && (again || (rank != reach && rank < top_k)))) {
-    // the same in fp64, by values with the bounds that their logits' leave
-    if (rule.softmax && bias) return kOpen;   // (their divisor is an fp32 sum)
+    // the same in fp64, by values with the bounds that their logits' leave; a softmax's divisor
+    // moves two values by the difference of their scores
+    const bool shared = rule.softmax && bias;
+    double z = 1.0, dz = 0.0;
+    if (shared) {
+      double total = 0.0, off = 0.0;
+#pragma unroll
+      for (int s = 0; s < SL; ++s)
+        if (l[s] > -INFINITY) {
+          const double e = exp(l[s] - (double)top);
+          total += e;
+          off += e * (d[s] + 0.6 * d[s] * d[s]);
+        }
+      z = wave_sum_f64(total);
+      if (BOUNDS) dz = wave_sum_f64(off) / z;
+      dz += 2.0 * dz * dz;   // 1 / (1 - dz) - 1 for dz < 0.4
+    }
     double* s_bound = s_val + kWave;
+    double* s_part = s_bound + kWave;
+    const double part = score / z;
     double my_v = cand ? mine.l : -INFINITY, my_d = mine.d;
     if (bias && cand) {
-      my_v = score + mine.b;
-      if (my_d > 0.0) my_d = 1.2 * my_d * score * fmin(1.0, ex * score) + 1e-14;
+      my_v = part + mine.b;
+      const double grow = my_d + 0.6 * my_d * my_d;
+      if (my_d > 0.0) my_d = grow * part * (rule.softmax ? 1.0 : fmin(1.0, ex * score)) + 1e-14;
     }
     s_val[lane] = my_v;
     s_bound[lane] = my_d;
+    s_part[lane] = part;
     wave_lds_fence();
     rank = 0;
     bool close = false;   // another candidate that the bounds cannot tell from this one
     for (int j0 = 0; j0 < found; j0 += 4) {   // (places past the last hold -inf and 0)
-      double o[4], od[4];
+      double o[4], tol[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         o[i] = s_val[j0 + i];
-        od[i] = s_bound[j0 + i];
+        tol[i] = my_d + s_bound[j0 + i];
+        if (shared) tol[i] += dz * fabs(s_part[j0 + i] - part);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         rank += (o[i] > my_v || (o[i] == my_v && j0 + i < lane)) ? 1 : 0;
-        close |= j0 + i != lane && fabs(o[i] - my_v) <= my_d + od[i] && my_d + od[i] > 0.0;
+        close |= j0 + i != lane && fabs(o[i] - my_v) <= tol[i] && tol[i] > 0.0;
       }
     }
     if (__any(cand && close)) {   // it matters if one of the two is picked
       s_key[lane] = (uint32_t)rank;
       wave_lds_fence();
       bool matters = false;
+#pragma unroll 4
       for (int j = 0; j < found; ++j) {
-        const double o = s_val[j], od = s_bound[j];
-        matters |= j != lane && fabs(o - my_v) <= my_d + od && my_d + od > 0.0 &&
+        double tol = my_d + s_bound[j];
+        if (shared) tol += dz * fabs(s_part[j] - part);
+        matters |= j != lane && fabs(s_val[j] - my_v) <= tol && tol > 0.0 &&
                    (rank < top_k || (int)s_key[j] < top_k);
       }
       wave_lds_fence();
-      if (__any(cand && matters)) {   // (one of a pair at least has a bound)
+      if (__any(cand && matters)) {
         ask = cand && matters && my_d > 0.0;
-        return kRedo;
+        return __any(ask) ? kRedo : kAll;   // (only the divisor leaves it open)
       }
     }
   }
@@ -811,7 +874,7 @@ __host__ __device__ constexpr int select_lds_doubles(bool bounds, int E, int top
 // its own (sigmoid: s (1 - s) (e^d - 1) <= 1.2 d s (1 - s) for d <= 1/4; softmax without its
 // common divisor: 1.2 d e^l), and a choice stands if no bound can turn it.  Where one can,
 // the experts that it hangs on are asked for; choices between exact values are exact, so this
-// ends.
+// ends.  (Softmax with a bias: the kernel asks for every logit first.)
 template <int SL, bool BOUNDS>
 __device__ __forceinline__ Fast select_fp64(const double (&l)[SL], const double (&d)[SL],
                                             const float* bias, int64_t t, int E, int top_k,
@@ -819,7 +882,7 @@ __device__ __forceinline__ Fast select_fp64(const double (&l)[SL], const double 
                                             double* s_pick, double* s_pv, double* s_pd, int* s_id,
                                             int lane, uint32_t& redo, int32_t* ids,
                                             float* weights) {
-  // scores (softmax with bounds: without the divisor, which is applied at the end)
+  // scores (softmax with bounds and no bias: without the divisor, which is applied at the end)
   double score[SL], c[SL], dc[SL], divisor = 1.0;
   bool live[SL];
 #pragma unroll
@@ -838,7 +901,7 @@ __device__ __forceinline__ Fast select_fp64(const double (&l)[SL], const double 
       dc[s] = 1.2 * d[s] * score[s];
     }
     divisor = wave_sum_f64(total);
-    if (!BOUNDS) {
+    if (!BOUNDS || bias) {
 #pragma unroll
       for (int s = 0; s < SL; ++s) score[s] = live[s] ? score[s] / divisor : 0.0;
       divisor = 1.0;
@@ -1039,7 +1102,9 @@ __device__ __forceinline__ Fast select_fp64(const double (&l)[SL], const double 
 }
 
 // One wave per token; lane l owns experts l, l + 64, ... (SL of them).  At M=2048, E=256, k=16
-// one token in nine asks for exact logits, two or three of them.
+// one token in nine asks for exact logits, mostly two.  Bound by latencies, not by work: one
+// wave takes 6 us from start to end (M=8: 5.9 us), and what asks a second time as long again and
+// the dot products (M=2048: 25 us).
 template <int SL, typename SRC>
 __global__ __launch_bounds__(kSelWaves* kWave, 2) void select_groups_kernel(
     SRC src, const float* __restrict__ bias, int M, int E, int top_k, GroupRule rule,
@@ -1047,7 +1112,10 @@ __global__ __launch_bounds__(kSelWaves* kWave, 2) void select_groups_kernel(
   constexpr bool BOUNDS = std::is_same<SRC, BoundedSource>::value;
   extern __shared__ __align__(16) double sel_lds[];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int64_t t0 = (int64_t)blockIdx.x * kSelWaves, t = t0 + wave;
+  const int64_t t0 = (int64_t)blockIdx.x * kSelWaves, row = t0 + wave;
+  const bool on = row < src.rows(M);
+  if (!BOUNDS && !on) return;
+  const int64_t t = on ? src.token(row) : row;
   double* s_c = sel_lds + (size_t)wave * select_lds_doubles(BOUNDS, E, top_k);
   const int even_E = select_lds_experts(BOUNDS, E), even_k = (top_k + 1) / 2 * 2;
   double* s_d = s_c + even_E;                              // BOUNDS
@@ -1057,10 +1125,9 @@ __global__ __launch_bounds__(kSelWaves* kWave, 2) void select_groups_kernel(
   int* s_id = reinterpret_cast<int*>(s_pick + (BOUNDS ? 3 : 1) * even_k);   // and the picks
   uint32_t* s_key = reinterpret_cast<uint32_t*>(s_id + (max(top_k, kWave) + 3) / 4 * 4);
 
-  const bool on = t < M;
   float b[SL];
   double l[SL], d[SL];
-  src.template get<SL>(min(t, (int64_t)M - 1), E, lane, l, d);
+  src.template get<SL>(min(row, (int64_t)M - 1), E, lane, l, d);
 #pragma unroll
   for (int s = 0; s < SL; ++s) {
     const int e = lane + kWave * s;
@@ -1084,14 +1151,35 @@ __global__ __launch_bounds__(kSelWaves* kWave, 2) void select_groups_kernel(
                              reinterpret_cast<float*>(s_c), reinterpret_cast<float*>(s_c) + E, s_key,
                              s_id, lane, redo, top, found, mine);
       if (got == kRedo) return got;
-      stage = got == kDone ? kRank : kSlow;
+      if (got != kAll) stage = got == kDone ? kRank : kSlow;
     }
     if (stage == kRank) {
       got = rank_fast<SL, BOUNDS>(l, d, mine, again, bias != nullptr, t, E, top_k, rule, top, found,
                                   s_c, s_key, lane, redo, ask, ids, weights);
       again = true;
-      if (got != kOpen) return got;
-      stage = kSlow;
+      if (__any(redo != 0) || got == kAll) {
+        stage = kCollect;
+        again = false;
+      }
+      if (got != kAll) return got;
+    }
+    if constexpr (BOUNDS) {
+      bool inexact = false;
+#pragma unroll
+      for (int s = 0; s < SL; ++s) inexact |= d[s] > 0.0;
+      if (got == kAll || (rule.softmax && bias && __any(inexact))) {
+        // a kernel of its own does it for listed tokens; the workgroup where the list is full
+        int row = 0;
+        if (lane == 0) row = atomicAdd(src.list.count, 1);
+        row = __builtin_amdgcn_readfirstlane(row);
+        if (row < src.list.room) {
+          if (lane == 0) src.list.tokens[row] = (int)t;
+          return kDone;
+        }
+#pragma unroll
+        for (int s = 0; s < SL; ++s) redo |= (uint32_t)(d[s] > 0.0) << s;
+        return kRedo;
+      }
     }
     wave_lds_fence();
     return select_fp64<SL, BOUNDS>(l, d, bias, t, E, top_k, rule, s_c, s_d, s_pick, s_pv, s_pd, s_id,
@@ -1104,8 +1192,40 @@ __global__ __launch_bounds__(kSelWaves* kWave, 2) void select_groups_kernel(
       if (!done && !__any(redo != 0 || ask)) done = select() == kDone;
       if (!exact_round<SL>(src, queue, t0, M, wave, lane, redo, l, d, ask, mine)) break;
     }
-  } else if (on) {
+  } else {
     select();
+  }
+}
+
+// Exact logits of listed tokens, with the sums of exact_round: 8 experts of a token per
+// workgroup at a time, two per wave.  Softmax scores with a bias: 3 to 5 tokens in 100 have two
+// experts whose order hangs on the divisor, and so on every logit (one workgroup takes 460 us
+// for one token's at E=512, H=7168).
+__global__ __launch_bounds__(kSelWaves* kWave, 2) void exact_rows_kernel(BoundedSource src, int E,
+                                                                          double* __restrict__ keys) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int groups = (E + 2 * kSelWaves - 1) / (2 * kSelWaves);
+  const int64_t items = (int64_t)min(*src.list.count, src.list.room) * groups;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int64_t row = item / groups;
+    const int e = (int)(item % groups) * 2 * kSelWaves + 2 * wave;
+    if (e >= E) continue;
+    const int64_t t = src.list.tokens[row];
+    const int pair[2] = {e, min(e + 1, E - 1)};
+    double part[2][kSelWaves];
+#pragma unroll
+    for (int quarter = 0; quarter < kSelWaves; ++quarter) {
+      double sum[2];
+      quarter_dots<2, 4>(src, t, pair, quarter, lane, sum);
+      part[0][quarter] = sum[0];
+      part[1][quarter] = sum[1];
+    }
+    if (lane < 2 && e + lane < E) {
+      const double(&p)[kSelWaves] = part[0];
+      const double(&q)[kSelWaves] = part[1];
+      keys[row * E + e + lane] = lane == 0 ? ((p[0] + p[1]) + p[2]) + p[3]
+                                           : ((q[0] + q[1]) + q[2]) + q[3];
+    }
   }
 }
 
@@ -1114,7 +1234,7 @@ hipError_t launch_select_sl(const SRC& src, const float* bias, int M, int E, int
                             const GroupRule& rule, int32_t* ids, float* w, hipStream_t s) {
   constexpr bool BOUNDS = std::is_same<SRC, BoundedSource>::value;
   const size_t lds = (size_t)kSelWaves * select_lds_doubles(BOUNDS, E, top_k) * sizeof(double);
-  const dim3 grid((unsigned)((M + kSelWaves - 1) / kSelWaves));
+  const dim3 grid((unsigned)((M + kSelWaves - 1) / kSelWaves));   // M: rows of the source at most
   hipLaunchKernelGGL((select_groups_kernel<SL, SRC>), grid, dim3(kSelWaves* kWave), lds, s, src, bias,
                      M, E, top_k, rule, ids, w);
   return hipGetLastError();
@@ -1127,7 +1247,7 @@ hipError_t launch_select(const SRC& src, const float* bias, int M, int E, int to
   if (E <= 128) return launch_select_sl<2>(src, bias, M, E, top_k, rule, ids, w, s);
   if (E <= 256) return launch_select_sl<4>(src, bias, M, E, top_k, rule, ids, w, s);
   if (E <= 512) return launch_select_sl<8>(src, bias, M, E, top_k, rule, ids, w, s);
-  if constexpr (!std::is_same<SRC, BoundedSource>::value)
+  if constexpr (std::is_same<SRC, KeySource>::value || std::is_same<SRC, LogitSource>::value)
     return launch_select_sl<16>(src, bias, M, E, top_k, rule, ids, w, s);
   return hipErrorInvalidValue;
 }
@@ -1137,7 +1257,7 @@ hipError_t launch_select(const SRC& src, const float* bias, int M, int E, int to
 hipError_t launch_route_logits(const float* logits, int64_t ld, const float* bias, int M, int E,
                                int top_k, const GroupRule& rule, int32_t* ids, float* w,
                                hipStream_t s) {
-  return launch_select(LogitSource{logits, ld}, bias, M, E, top_k, rule, ids, w, s);
+  return launch_select(LogitSource{{}, logits, ld}, bias, M, E, top_k, rule, ids, w, s);
 }
 
 namespace {
@@ -1161,16 +1281,20 @@ size_t route_groups_scratch_bytes(int M, int E) {
   return rows * E * 2 * sizeof(float);
 }
 
-// From this many tokens on bounded fp32 MFMA logits replace fp64 ones for every (token,
-// expert).  Not for softmax scores with a bias, whose choices hang on the divisor and so on
-// every expert's exact logit, for more experts than 512 (registers), or where a pick of
-// nearly all experts leaves most choices open.
-constexpr int kBoundedMinTokens = 256, kBoundedMaxExperts = 512;
+// From this many logits on bounded fp32 MFMA sums replace fp64 ones for every (token, expert).
+// Measured at H=7168, bounded against fp64, us: E=256 M=64 25 / 22, M=128 29 / 32, M=255 31 /
+// 54; E=512 M=64 41 / 35, M=128 41 / 57; E=64 M=255 21 / 19.  Softmax scores with a bias, with
+// the listed tokens' two launches: E=512 M=255 66 / 94, M=128 58 / 52, M=4096 145 / 1,322.  Not
+// for few experts (a tile of 64 stays mostly empty), more than 512 (registers), or a pick of
+// nearly all, which leaves most choices open.
+constexpr int kBoundedMinLogits = 40000, kBoundedMinExperts = 32, kBoundedMaxExperts = 512;
 
 hipError_t launch_route_groups(const uint16_t* x, const uint16_t* wr, const float* bias, int M,
                                int H, int E, int top_k, const GroupRule& rule, int32_t* ids,
                                float* w, void* scratch, hipStream_t s) {
-  if (M >= kBoundedMinTokens && E <= kBoundedMaxExperts && top_k <= 64 && !(rule.softmax && bias)) {
+  const bool divisor = rule.softmax && bias;   // choices hang on every expert's logit
+  if ((int64_t)M * E >= (divisor ? 2 : 1) * kBoundedMinLogits && E >= kBoundedMinExperts &&
+      E <= kBoundedMaxExperts && top_k <= 64) {
     const int64_t tiles = (int64_t)((E + kBlTile - 1) / kBlTile) * ((M + kBlTile - 1) / kBlTile);
     const int pieces = (H + 255) / 256;
     int parts = std::min(bounded_parts(M, E), pieces);
@@ -1179,13 +1303,29 @@ hipError_t launch_route_groups(const uint16_t* x, const uint16_t* wr, const floa
     const int per_xcd = (int)((tiles * parts + kXcds - 1) / kXcds);
     float* logits = static_cast<float*>(scratch);
     float* absdot = logits + (size_t)parts * M * E;
+    // behind them (8 bytes for a value are there, about 5 used): exact logits of one token in
+    // eight, their list and its length
+    const size_t used = ((size_t)parts * M * (E + (E + 3) / 4) * sizeof(float) + 7) / 8 * 8;
+    double* keys = reinterpret_cast<double*>(static_cast<char*>(scratch) + used);
+    TokenList list{nullptr, nullptr, 0};
+    if (divisor) {
+      const size_t left = route_groups_scratch_bytes(M, E) - used - sizeof(int);
+      list.room = (int)std::min((size_t)M / 8, left / ((size_t)E * sizeof(double) + sizeof(int)));
+      list.tokens = reinterpret_cast<int*>(keys + (size_t)list.room * E);
+      list.count = list.tokens + list.room;
+    }
     hipLaunchKernelGGL(bounded_logits_kernel, dim3((unsigned)per_xcd * kXcds), dim3(256), 0, s, x,
-                       wr, M, H, E, parts, kpart, per_xcd, logits, absdot);
-    const hipError_t err = hipGetLastError();
+                       wr, M, H, E, parts, kpart, per_xcd, logits, absdot, list.count);
+    hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
     const double rel = kBlRounds * 0x1p-23 * (1.0 + 0x1p-9);
-    return launch_select(BoundedSource{logits, absdot, x, wr, parts, M, H, rel}, bias, M, E,
-                         top_k, rule, ids, w, s);
+    const BoundedSource src{{}, logits, absdot, x, wr, parts, M, H, rel, list};
+    err = launch_select(src, bias, M, E, top_k, rule, ids, w, s);
+    if (err != hipSuccess || !divisor) return err;
+    hipLaunchKernelGGL(exact_rows_kernel, dim3(1024), dim3(kSelWaves* kWave), 0, s, src, E, keys);
+    err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    return launch_select(ListSource{keys, E, list}, bias, list.room, E, top_k, rule, ids, w, s);
   }
   double* keys = static_cast<double*>(scratch);
   constexpr int kMost = 1 << 17;   // tokens of one launch (its grid has them in y)
@@ -1194,7 +1334,7 @@ hipError_t launch_route_groups(const uint16_t* x, const uint16_t* wr, const floa
                                               keys + (size_t)t0 * E, s);
     if (err != hipSuccess) return err;
   }
-  return launch_select(KeySource{keys, E}, bias, M, E, top_k, rule, ids, w, s);
+  return launch_select(KeySource{{}, keys, E}, bias, M, E, top_k, rule, ids, w, s);
 }
 
 }  // namespace moe

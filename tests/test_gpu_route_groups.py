@@ -162,14 +162,15 @@ def _inputs(M, H, E, dev, seed=0, std=1.7):
 @pytest.mark.parametrize("rule", RULES)
 @pytest.mark.parametrize("M,H,E,k", [(1, 256, 8, 2), (7, 1032, 60, 4), (8, 7168, 256, 16),
                                      (300, 520, 64, 7), (515, 1024, 160, 6), (1025, 2048, 256, 16),
-                                     (260, 264, 512, 16), (257, 8, 1024, 8)])
+                                     (260, 264, 512, 16), (257, 8, 1024, 8), (701, 520, 64, 7),
+                                     (130, 7168, 320, 8), (1300, 1032, 36, 5)])
 @pytest.mark.parametrize("biased", [False, True])
 def test_hidden_states(B, dev, M, H, E, k, rule, biased):
     x, wr, bias = _inputs(M, H, E, dev)
     _check_x(B, x, wr, bias if biased else None, k, rule, dev)
 
 
-@pytest.mark.parametrize("M", [9, 400])
+@pytest.mark.parametrize("M", [9, 400, 900])
 @pytest.mark.parametrize("rule", RULES)
 def test_equal_and_nearly_equal_router_rows(B, dev, M, rule):
     """Exact ties, rows one bf16 step apart in one value, zero tokens."""
@@ -185,7 +186,7 @@ def test_equal_and_nearly_equal_router_rows(B, dev, M, rule):
         _check_x(B, x, wr, b, 8, rule, dev)
 
 
-@pytest.mark.parametrize("M", [6, 300])
+@pytest.mark.parametrize("M", [6, 300, 1300])
 def test_all_router_rows_equal(B, dev, M):
     x, wr, bias = _inputs(M, 256, 64, dev, seed=8)
     wr[:] = wr[0]
@@ -193,7 +194,7 @@ def test_all_router_rows_equal(B, dev, M):
         _check_x(B, x, wr, None, 4, rule, dev)
 
 
-@pytest.mark.parametrize("M", [5, 300])
+@pytest.mark.parametrize("M", [5, 300, 2600])
 def test_tokens_that_are_not_finite_get_valid_ids(B, dev, M):
     x, wr, bias = _inputs(M, 256, 32, dev, seed=9)
     x[1, 3] = float("nan")
@@ -210,9 +211,10 @@ def test_tokens_that_are_not_finite_get_valid_ids(B, dev, M):
             assert torch.equal(ids[clean], ids2) and torch.equal(w[clean], w2)
 
 
-def test_large_values(B, dev):
+@pytest.mark.parametrize("M", [300, 1300])
+def test_large_values(B, dev, M):
     """Logits in the hundreds: sigmoids at 1, softmax with one expert at 1."""
-    x, wr, bias = _inputs(300, 1024, 64, dev, seed=10, std=150.0)
+    x, wr, bias = _inputs(M, 1024, 64, dev, seed=10, std=150.0)
     for rule in (dict(softmax=True), dict(), dict(n_group=4, topk_group=2)):
         _check_x(B, x, wr, None, 4, rule, dev)
 
@@ -222,11 +224,12 @@ def test_large_values(B, dev):
                                   dict(n_group=4, topk_group=2, group_top=2)])
 @pytest.mark.parametrize("size", [100.0, 20000.0])
 @pytest.mark.parametrize("biased", [False, True])
-def test_weights_where_large_terms_cancel(B, dev, rule, size, biased):
+@pytest.mark.parametrize("M", [300, 1300])
+def test_weights_where_large_terms_cancel(B, dev, M, rule, size, biased):
     """Two halves of the row whose products cancel but for ordinary logits: the fp32 sums are
     off by parts of the terms' size.  A weight may be off by twice 2^-9 of itself: 2^-9 from
     its own logit, 2^-9 from those of what it is divided by."""
-    x, wr, bias = _inputs(300, 1024, 64, dev, seed=12)
+    x, wr, bias = _inputs(M, 1024, 64, dev, seed=12)
     x[:, 256:512] = size / 256
     x[:, 768:] = -size / 256
     wr[:, 256:512] = wr[:, 768:] = 1.0
@@ -238,9 +241,10 @@ def test_weights_where_large_terms_cancel(B, dev, rule, size, biased):
     assert (np.abs(w.cpu().numpy() - rw) <= 2 * 2 ** -9 * np.abs(rw) * (1 + 2 ** -6)).all()
 
 
-@pytest.mark.parametrize("M", [8, 512])
-def test_graph_replays_equal_eager_calls(B, dev, M):
-    rule = dict(n_group=4, topk_group=2, group_top=2, scale=2.5)
+@pytest.mark.parametrize("softmax", [False, True])
+@pytest.mark.parametrize("M", [8, 512, 1300])
+def test_graph_replays_equal_eager_calls(B, dev, M, softmax):
+    rule = dict(n_group=4, topk_group=2, group_top=2, scale=2.5, softmax=softmax)
     _, api = _rule(rule)
     x, wr, bias = _inputs(M, 512, 64, dev, seed=1)
     k = 6
@@ -265,9 +269,11 @@ def test_graph_replays_equal_eager_calls(B, dev, M):
         assert torch.equal(ids, want[0]) and torch.equal(w, want[1])
 
 
-def test_two_streams_at_once(B, dev):
-    rule = dict(n_group=4, topk_group=2, group_top=2)
-    a, b = _inputs(700, 1024, 64, dev, seed=1), _inputs(300, 1024, 64, dev, seed=2)
+@pytest.mark.parametrize("more", [0, 1000])
+@pytest.mark.parametrize("softmax", [False, True])
+def test_two_streams_at_once(B, dev, more, softmax):
+    rule = dict(n_group=4, topk_group=2, group_top=2, softmax=softmax)
+    a, b = _inputs(700 + more, 1024, 64, dev, seed=1), _inputs(300 + more, 1024, 64, dev, seed=2)
     want = [_run_x(B, v[0], v[1], v[2], 6, rule, dev) for v in (a, b)]
     torch.cuda.synchronize()
     _, api = _rule(rule)
@@ -284,3 +290,18 @@ def test_two_streams_at_once(B, dev):
     torch.cuda.synchronize()
     for o, wv in zip(outs, want):
         assert torch.equal(o[0], wv[0]) and torch.equal(o[1], wv[1])
+
+
+@pytest.mark.parametrize("rule", [dict(softmax=True), dict(softmax=True, n_group=4, topk_group=1)])
+@pytest.mark.parametrize("same", [1400, 60])
+def test_softmax_divisor_decides(B, dev, rule, same):
+    """A bias that makes up for the difference of two experts' scores to fp32's last bit: their
+    order hangs on every logit of the token, in few tokens and in nearly all."""
+    x, wr, _ = _inputs(1400, 1024, 64, dev, seed=14)
+    x[:same] = x[0]
+    l = bf16_to_f64(bits(x[:1])) @ bf16_to_f64(bits(wr)).T
+    p = np.exp(l[0] - l.max())
+    p /= p.sum()
+    bias = torch.zeros(64, device=dev)
+    bias[int(p.argmin())] = float(p.max() - p.min())
+    _check_x(B, x, wr, bias, 8, rule, dev)
