@@ -142,6 +142,15 @@ __device__ __forceinline__ void store_act(const I8Args& p, int row, int c, const
   if ((c & 31) == 0 && c < p.ncols) p.act_exps[block_row * 4 + ((c >> 5) & 3)] = (uint8_t)E;
 }
 
+// 16 results of pick i, columns n0 on: every pick in fp32 in y0, or (with y) the first of each
+// token there and the others in bf16 in y.
+__device__ __forceinline__ void store_y(const I8Args& p, int i, int n0, const float (&v)[16]) {
+  const YRow yr = y_row(i, p.top_k, p.ncols);
+  if (!p.y) store16(p.y0 + (size_t)i * p.ncols + n0, v);
+  else if (yr.first) store16(p.y0 + yr.off + n0, v);
+  else store16(p.y + yr.off + n0, v);
+}
+
 // 16 results of a dense row that starts at `row` (in values), columns n0 on
 template <bool F32>
 __device__ __forceinline__ void store_dense(const I8Args& p, size_t row, int n0,
@@ -335,9 +344,7 @@ __global__ __launch_bounds__(64 * WN * WM) void i8_gemm_kernel(I8Args p) {
         if (MODE == kDense) {
           store_dense<F32>(p, (size_t)row * p.ncols, n0, v);
         } else {
-          const YRow yr = y_row(p.sorted_ids[row], p.top_k, p.ncols);
-          if (yr.first) store16(p.y0 + yr.off + n0, v);
-          else store16(p.y + yr.off + n0, v);
+          store_y(p, p.sorted_ids[row], n0, v);
         }
       }
     }
@@ -580,9 +587,7 @@ __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char*
           store_dense<F32>(p, (size_t)(it.start + r) * p.ncols, n0, v);
           continue;
         }
-        const YRow yr = y_row(id[s], p.top_k, p.ncols);
-        if (yr.first) store16(p.y0 + yr.off + n0, v);
-        else store16(p.y + yr.off + n0, v);
+        store_y(p, id[s], n0, v);
       }
     }
   };
@@ -857,8 +862,8 @@ hipError_t launch_i8_up(const int8_t* x, const float* x_scale, const int8_t* w13
 hipError_t launch_i8_down(const int8_t* act, const float* act_scale, const int8_t* w2,
                           const float* w2_scale, const int32_t* sorted_ids,
                           const int32_t* block_expert, const int2* tiles,
-                          const int32_t* num_tiles, int max_tiles, int tile_rows, int H, int I, int top_k, int block, uint16_t* y,
-                          float* y0, hipStream_t s) {
+                          const int32_t* num_tiles, int max_tiles, int tile_rows, int H, int I,
+                          int top_k, int block, uint16_t* y, float* y0, hipStream_t s) {
   I8Args p = grouped(act, act_scale, w2, w2_scale, sorted_ids, block_expert, tiles, num_tiles, I,
                      H, top_k, block);
   p.y = y;

@@ -381,7 +381,7 @@ struct Candidate {
 constexpr int kAsk = 32;
 struct ExactQueue {
   int expert[kSelWaves][kAsk];   // -1: none
-  int asked[kSelWaves];
+  alignas(16) int asked[kSelWaves];
   double part[kSelWaves][kAsk][kSelWaves];
 };
 
@@ -448,13 +448,18 @@ __device__ __forceinline__ bool exact_round(const BoundedSource& q, ExactQueue& 
   }
   if (lane == 0) queue.asked[wave] = min(asked, kAsk);
   if (!__syncthreads_or(asked)) return false;
-  int pairs = 0;
-  for (int w = 0; w < kSelWaves; ++w) pairs += (queue.asked[w] + 1) / 2;
-  const bool split = pairs < 2 * kSelWaves;   // each pair over the waves, or a pair per wave
+  const int4 n4 = *reinterpret_cast<const int4*>(queue.asked);
+  const int n[kSelWaves] = {
+      __builtin_amdgcn_readfirstlane(n4.x), __builtin_amdgcn_readfirstlane(n4.y),
+      __builtin_amdgcn_readfirstlane(n4.z), __builtin_amdgcn_readfirstlane(n4.w)};
+  // each pair over the waves, or a pair per wave
+  const bool split = n[0] + n[1] + n[2] + n[3] < 4 * kSelWaves;
   int pair = 0;
+#pragma unroll 1
   for (int w = 0; w < kSelWaves; ++w) {
     const int64_t t = min(t0 + w, M - 1);
-    for (int i = 0; i < queue.asked[w]; i += 2, ++pair) {
+    const int asks = w == 0 ? n[0] : w == 1 ? n[1] : w == 2 ? n[2] : n[3];
+    for (int i = 0; i < asks; i += 2, ++pair) {
       if (!split && pair % kSelWaves != wave) continue;
       for (int quarter = split ? wave : 0; quarter < (split ? wave + 1 : kSelWaves); ++quarter) {
         double sum[2];

@@ -256,6 +256,9 @@ LAYERS = [  # M, H, E, I, k, block, rule: tokens per expert from 0.1 to over 128
     (40, 656, 4, 768, 2, 16, dict()), (77, 1024, 8, 640, 4, 32, GROUPED),
     (205, 768, 4, 1408, 1, 16, dict()), (333, 896, 8, 640, 4, 64, GROUPED),
     (450, 784, 4, 768, 2, 16, dict(softmax=True)), (290, 1280, 4, 896, 3, 64, dict(scale=2.5)),
+    # more results of the down product than are held in fp32
+    (1100, 4096, 4, 640, 4, 64, dict()), (1030, 4096, 4, 48, 4, 16, dict(scale=2.5)),
+    (200, 16384, 8, 16, 8, 16, dict(softmax=True)),
 ]
 
 
