@@ -25,11 +25,19 @@ __device__ __forceinline__ uint32_t max_bits(uint32_t m, u32x4 v) {
   return m;
 }
 
-__device__ __forceinline__ uint32_t code_of(float v, float a) {
-  return (uint32_t)(int)rintf((127.0f * v) / a) & 0xffu;
+// 127 and a, both by 2^-8 where 127 a may pass the largest number (values that this makes
+// subnormal have code 0 either way).
+struct Quotient {
+  float k, a;
+};
+__device__ __forceinline__ Quotient quotient_of(float a) {
+  return a >= 0x1p120f ? Quotient{127.0f * 0x1p-8f, a * 0x1p-8f} : Quotient{127.0f, a};
+}
+__device__ __forceinline__ uint32_t code_of(float v, Quotient q) {
+  return (uint32_t)(int)rintf((q.k * v) / q.a) & 0xffu;
 }
 
-__device__ __forceinline__ uint2 codes8(u32x4 v, float a) {
+__device__ __forceinline__ uint2 codes8(u32x4 v, Quotient a) {
   uint2 c;
   c.x = code_of(bf16lo(v[0]), a) | code_of(bf16hi(v[0]), a) << 8 | code_of(bf16lo(v[1]), a) << 16 |
         code_of(bf16hi(v[1]), a) << 24;
@@ -75,23 +83,24 @@ __global__ __launch_bounds__(kQThreads) void i8_rows_kernel(const uint16_t* __re
   const float top = __uint_as_float(m << 16);
   if (lane == 0) scales[row] = top / 127.0f;
   const bool zero = m == 0 || m >= 0x7f80u;
+  const Quotient q = quotient_of(top);
   int8_t* dst = codes + row * K;
 #pragma unroll
   for (int i = 0; i < KEEP; ++i) {
     const int ch = lane + LANES * i;
     if (ch < nchunk)
-      *reinterpret_cast<uint2*>(dst + (size_t)ch * 8) = zero ? uint2{0u, 0u} : codes8(keep[i], top);
+      *reinterpret_cast<uint2*>(dst + (size_t)ch * 8) = zero ? uint2{0u, 0u} : codes8(keep[i], q);
   }
   for (int ch = lane + LANES * KEEP; ch < nchunk; ch += LANES)
     *reinterpret_cast<uint2*>(dst + (size_t)ch * 8) =
-        zero ? uint2{0u, 0u} : codes8(ld16(src + (size_t)ch * 8), top);
+        zero ? uint2{0u, 0u} : codes8(ld16(src + (size_t)ch * 8), q);
 }
 
 // Rows of a plan (one wave each) from the block floats of the up GEMM: 32 values share the
-// byte E, value = int16 * 2^(E - 140); E = 255 marks a block that is not finite.  Rows that
+// byte E, value = int16 * 2^(E - 141); E = 255 marks a block that is not finite.  Rows that
 // hold no real entry are skipped.  The row's maximum and the codes come from the stored
-// values, whose rounding (2^-14 of the block's largest value at most) moves a code by one
-// only where 127 v / a lies within 127 * 2^-14 of a border.
+// values, whose rounding (2^-15 of the block's largest value at most) moves a code by one
+// only where 127 v / a lies within 127 * 2^-15 of a border.
 __global__ __launch_bounds__(kQThreads) void i8_act_kernel(
     const int16_t* __restrict__ act, const uint8_t* __restrict__ exps, int64_t rows, int I,
     const int32_t* __restrict__ plan, const int32_t* __restrict__ num_padded, int n_ids,
@@ -136,13 +145,14 @@ __global__ __launch_bounds__(kQThreads) void i8_act_kernel(
   bad = __any(bad);
   if (lane == 0) scales[row] = bad ? __uint_as_float(0x7fc00000u) : top / 127.0f;
   const bool zero = bad || top == 0.0f;
+  const Quotient q = quotient_of(top);
   auto put = [&](int ch, u32x4 v, uint32_t ex) {
     const float u = unit(ex);
     uint32_t c[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      c[2 * j] = code_of((float)(int16_t)v[j] * u, top);
-      c[2 * j + 1] = code_of((float)((int)v[j] >> 16) * u, top);
+      c[2 * j] = code_of((float)(int16_t)v[j] * u, q);
+      c[2 * j + 1] = code_of((float)((int)v[j] >> 16) * u, q);
     }
     const uint2 out = {c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24,
                        c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24};

@@ -61,7 +61,7 @@ def test_quantize(B, dev, rows, K):
     assert (np.abs(scales.cpu().numpy() - ws) <= 2 ** -24 * ws).all()
 
 
-@pytest.mark.parametrize("power", [-120, -60, 60, 119])
+@pytest.mark.parametrize("power", [-131, -120, -60, 60, 119, 121, 126])
 def test_quantize_small_and_large_values(B, dev, power):
     v = torch.randn(6, 256, generator=torch.Generator().manual_seed(1)).mul(2.0 ** power).bfloat16().to(dev)
     codes, scales = _quantize(B, v)
