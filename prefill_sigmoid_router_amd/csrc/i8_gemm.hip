@@ -363,7 +363,7 @@ hipError_t launch(I8Args& a, long token_tiles, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Grouped products, and dense ones of many rows, over whole 128-wide chunks (K % 128 == 0).
+// Grouped products, and dense ones of many rows, of more than 4 chunks.
 //
 // 256 weight rows (UP: 128 act columns) per workgroup of 8 waves, 4 along the weight rows and
 // 2 along the tokens, against up to ROWS token rows of an expert at once, so that its weights
@@ -409,7 +409,7 @@ struct GroupedItem {
   int start, nlive, e, col0;
 };
 
-template <Mode MODE, typename R, int WPOL, bool F32>
+template <Mode MODE, typename R, int WPOL, bool F32, bool RAGGED>
 __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char* lds) {
   constexpr bool UP = MODE == kUp;
   constexpr int D = R::D, PW = R::PW, TPW = R::TPW, MTW = R::MTW;
@@ -446,6 +446,8 @@ __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char*
   // flight.)
   const int rr = lane >> 3;
   constexpr int SPAN = UP ? 8 : 16;
+  auto wpart = [&](int i) { return 16 * ((lane & 7) ^ weight_swizzle<SPAN>(32 * wave + 8 * i + rr)); };
+  auto tpart = [&](int i) { return 16 * ((lane & 7) ^ token_swizzle((wave * TPW + i) * 8 + rr)); };
   struct Src {
     __amdgpu_buffer_rsrc_t w, t;
     uint32_t woff[PW], toff[TPW];
@@ -458,30 +460,48 @@ __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char*
     q.t = buffer_of(UP ? p.tok : p.tok + (size_t)it.start * K);
 #pragma unroll
     for (int i = 0; i < PW; ++i)
-      q.woff[i] = (uint32_t)max(0, min(8 * i + rr, p.ncols - 1 - wcol)) * (uint32_t)K +
-                  16 * ((lane & 7) ^ weight_swizzle<SPAN>(32 * wave + 8 * i + rr));
+      q.woff[i] = (uint32_t)max(0, min(8 * i + rr, p.ncols - 1 - wcol)) * (uint32_t)K + wpart(i);
 #pragma unroll
     for (int i = 0; i < TPW; ++i) {
       const int lr = (wave * TPW + i) * 8 + rr;
       const int r = min(lr, it.nlive - 1);
       const uint32_t row = UP ? (uint32_t)p.sorted_ids[it.start + r] / (uint32_t)p.top_k : r;
-      q.toff[i] = row * (uint32_t)K + 16 * ((lane & 7) ^ token_swizzle(lr));
+      q.toff[i] = row * (uint32_t)K + tpart(i);
     }
   };
 
-  const int nch = K / kKC;
+  const int nch = (K + kKC - 1) / kKC;
   const int steps = (nch + D - 1) / D * D;
+  // RAGGED, a partial last chunk (a variant of its own: 256-row tiles have no registers to spare
+  // for it): parts behind column K repeat the chunk's first part, and those of the weights
+  // become zeros on their way to LDS.
+  const int rest = K - (nch - 1) * kKC;
+  auto partial = [&](int c) { return RAGGED && c >= nch - 1; };
+  auto behind = [&](int part) { return part >= rest ? part : 0; };
   u32x4 wreg[D][PW];
   int tput = 0;   // token stage that the next copy fills
   int tget = 0;   // token stage of the present step
   auto load_w = [&](const Src& q, int c, u32x4 (&dst)[PW]) {
     const int off = min(c, nch - 1) * kKC;
+    uint32_t o[PW];
+#pragma unroll
+    for (int i = 0; i < PW; ++i) o[i] = q.woff[i];
+    if (partial(c)) {
+#pragma unroll
+      for (int i = 0; i < PW; ++i) o[i] -= behind(wpart(i));
+    }
 #pragma unroll
     for (int i = 0; i < PW; ++i)
-      dst[i] = __builtin_amdgcn_raw_buffer_load_b128(q.w, q.woff[i], off, WPOL);
+      dst[i] = __builtin_amdgcn_raw_buffer_load_b128(q.w, o[i], off, WPOL);
   };
-  auto put_w = [&](int stage, const u32x4 (&v)[PW]) {
+  auto put_w = [&](int stage, int c, const u32x4 (&v)[PW]) {   // v: chunk c
     unsigned char* base = lds + stage * R::WSTAGE + wave * PW * 1024 + lane * 16;
+    if (partial(c)) {
+#pragma unroll
+      for (int i = 0; i < PW; ++i)
+        *reinterpret_cast<u32x4*>(base + i * 1024) = wpart(i) >= rest ? u32x4{0, 0, 0, 0} : v[i];
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < PW; ++i) *reinterpret_cast<u32x4*>(base + i * 1024) = v[i];
   };
@@ -489,10 +509,16 @@ __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char*
     const int off = min(c, nch - 1) * kKC;
     unsigned char* base = tlds + tput * R::TSTAGE + wave * TPW * 1024;
     tput = tput == D ? 0 : tput + 1;
+    uint32_t o[TPW];
+#pragma unroll
+    for (int i = 0; i < TPW; ++i) o[i] = q.toff[i];
+    if (partial(c)) {
+#pragma unroll
+      for (int i = 0; i < TPW; ++i) o[i] -= behind(tpart(i));
+    }
 #pragma unroll
     for (int i = 0; i < TPW; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(q.t, (lds_void*)(base + i * 1024), 16, q.toff[i],
-                                               off, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(q.t, (lds_void*)(base + i * 1024), 16, o[i], off, 0, 0);
   };
   const int wrow = (UP ? 32 : 64) * wn + SPAN * (li >> 2) + (li & 3);
   const int woff16 = wrow * 128 + 16 * (lg ^ weight_swizzle<SPAN>(wrow));
@@ -608,7 +634,7 @@ __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char*
       copy_t(qc, d);
       load_w(qc, 1 + d, wreg[d]);
     }
-    put_w(0, first);
+    put_w(0, 0, first);
   }
   clear();
   publish();   // (the first stage of weights too: older than the tokens)
@@ -622,7 +648,7 @@ __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char*
       for (int d = 0; d < D; ++d) {
         compute(cur, c + d, [&] {
           copy_t(qc, c + d + D);
-          put_w((d + 1) & 1, wreg[d]);
+          put_w((d + 1) & 1, c + d + 1, wreg[d]);
           load_w(qc, c + d + 1 + D, wreg[d]);
         });
         publish();
@@ -633,7 +659,7 @@ __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char*
     for (int d = 0; d < D; ++d) {
       compute(cur, c + d, [&] {
         copy_t(qc, c + d + D);
-        put_w((d + 1) & 1, wreg[d]);
+        put_w((d + 1) & 1, c + d + 1, wreg[d]);
         if (d + 1 < D) load_w(qc, c + d + 1 + D, wreg[d]);
         else load_w(qn, 0, wreg[d]);
       });
@@ -644,7 +670,7 @@ __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char*
     for (int d = 0; d < D; ++d) {
       compute(cur, c + d, [&] {
         copy_t(qn, d);
-        put_w((d + 1) & 1, wreg[d]);
+        put_w((d + 1) & 1, d + 1 < D ? c + d + 1 : 0, wreg[d]);
         load_w(qn, d + 1, wreg[d]);
       });
       publish();
@@ -661,12 +687,12 @@ __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char*
 
 constexpr int kGroupedLds = 160 * 1024;
 
-template <Mode MODE, typename R, int WPOL, bool F32>
+template <Mode MODE, typename R, int WPOL, bool F32, bool RAGGED>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void i8_grouped_kernel(
     I8Args p) {
   __shared__ __align__(16) unsigned char lds[R::LDS];
 #ifdef __HIP_DEVICE_COMPILE__
-  grouped_products<MODE, R, WPOL, F32>(p, lds);
+  grouped_products<MODE, R, WPOL, F32, RAGGED>(p, lds);
 #endif
 }
 
@@ -680,7 +706,12 @@ hipError_t launch_grouped(I8Args& a, long token_tiles, hipStream_t s) {
   a.n_ntiles = (a.ncols + per - 1) / per;
   // one workgroup per CU, whatever its LDS would allow: 512 threads of up to 256 registers
   const long grid = walk_grid(token_tiles * a.n_ntiles, kGroupedLds);
-  hipLaunchKernelGGL((i8_grouped_kernel<MODE, R, WPOL, F32>), dim3((unsigned)grid), dim3(512), 0, s, a);
+  if (a.K % kKC == 0)
+    hipLaunchKernelGGL((i8_grouped_kernel<MODE, R, WPOL, F32, false>), dim3((unsigned)grid), dim3(512),
+                       0, s, a);
+  else
+    hipLaunchKernelGGL((i8_grouped_kernel<MODE, R, WPOL, F32, true>), dim3((unsigned)grid), dim3(512),
+                       0, s, a);
   return hipGetLastError();
 }
 
@@ -784,7 +815,7 @@ hipError_t launch_dense(I8Args& a, hipStream_t s) {
     }
   };
   offer(1, 0.08 + 0.29 * tiles(64, 16) / 256);
-  if (a.K % kKC == 0 && a.K / kKC > 4) {
+  if (a.K > 4 * kKC) {   // (the stream needs 2 D chunks per item)
     offer(64, 0.88 * ceil(tiles(64, 256) / 256));
     offer(128, 1.33 * ceil(tiles(128, 256) / 256));
     offer(256, 2.09 * ceil(tiles(256, 256) / 256));
@@ -800,8 +831,7 @@ hipError_t launch_dense(I8Args& a, hipStream_t s) {
 
 template <Mode MODE>
 hipError_t launch_expert(I8Args& a, long tiles, int tile_rows, hipStream_t s) {
-  // the stream needs 2 D whole chunks per item
-  if (a.K % kKC == 0 && a.K / kKC > 4) {
+  if (a.K > 4 * kKC) {   // the stream needs 2 D chunks per item
     if (tile_rows == 64) return launch_grouped<MODE, RingFew, kStreamPolicy>(a, tiles, s);
     if (tile_rows == 128) return launch_grouped<MODE, RingMid, kStreamPolicy>(a, tiles, s);
     return launch_grouped<MODE, RingMany, kStreamPolicy>(a, tiles, s);

@@ -115,7 +115,8 @@ def _check_matmul(B, M, N, K, f32, dev, ops=None):
     (1, 1, 16), (1, 16, 128), (1, 4096, 7168), (2, 3, 48), (7, 129, 144), (8, 4096, 2048),
     (16, 1000, 1040), (17, 64, 64), (31, 333, 272), (33, 257, 1024), (64, 512, 4112), (65, 255, 80),
     (77, 1537, 2064), (127, 128, 128), (129, 1024, 7168), (200, 96, 8192), (256, 256, 256),
-    (257, 513, 400), (300, 2048, 1408), (511, 300, 16), (1030, 1300, 528), (2100, 260, 7168)])
+    (257, 513, 400), (300, 2048, 1408), (511, 300, 16), (1030, 1300, 528), (2100, 260, 7168),
+    (600, 700, 2064), (1500, 1100, 528), (3000, 2300, 1040), (4100, 513, 656), (900, 4097, 2032)])
 def test_matmul(B, dev, M, N, K, f32):
     _check_matmul(B, M, N, K, f32, dev)
 
@@ -256,6 +257,9 @@ LAYERS = [  # M, H, E, I, k, block, rule: tokens per expert from 0.1 to over 128
     (40, 656, 4, 768, 2, 16, dict()), (77, 1024, 8, 640, 4, 32, GROUPED),
     (205, 768, 4, 1408, 1, 16, dict()), (333, 896, 8, 640, 4, 64, GROUPED),
     (450, 784, 4, 768, 2, 16, dict(softmax=True)), (290, 1280, 4, 896, 3, 64, dict(scale=2.5)),
+    # and with a partial last chunk of K
+    (60, 528, 4, 656, 2, 16, dict()), (205, 784, 4, 1360, 1, 16, dict()),
+    (450, 656, 4, 592, 2, 32, dict(softmax=True)), (300, 1040, 2, 624, 2, 64, dict()),
     # more results of the down product than are held in fp32
     (1100, 4096, 4, 640, 4, 64, dict()), (1030, 4096, 4, 48, 4, 16, dict(scale=2.5)),
     (200, 16384, 8, 16, 8, 16, dict(softmax=True)),
