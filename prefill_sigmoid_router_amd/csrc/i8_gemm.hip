@@ -170,7 +170,6 @@ __device__ __forceinline__ void store_dense(const I8Args& p, size_t row, int n0,
 
 template <int BM, int WN, int WM>
 struct I8Cfg {
-  static constexpr int THREADS = 64 * WN * WM;
   static constexpr int WT = 4 * WN;              // weight row tiles of 16
   static constexpr int MT = BM / 16;             // token row tiles
   static constexpr int MTW = MT / WM;            // token row tiles per wave
