@@ -457,8 +457,8 @@ int moe_i8_matmul(const int8_t* a, const float* a_scales, const int8_t* w, const
  * moe_forward with int8 expert weights (moe_i8_quantize: w13_codes [E, 2I, H] + w13_scales
  * [E, 2I], w2_codes [E, H, I] + w2_scales [E, H]) and the router of moe_route_groups in place
  * of step 1.  x is quantized row by row (a scale per token); the up GEMM runs on the codes,
- * SwiGLU in fp32; act is quantized row by row (a scale per token and pick; between the two
- * it is held to 2^-15 of the largest of 32 neighbours); the down GEMM runs on the codes;
+ * SwiGLU in fp32; act (fp32) is quantized row by row (a scale per token and pick); the down
+ * GEMM runs on the codes;
  * finalize as in moe_forward.  Other arguments, stage events (quantizing x counts to step 1,
  * quantizing act to step 4) and outputs are those of moe_forward.  H % 16 == 0 and
  * I % 16 == 0, I <= 131072; M below 2^22, M * H below 2^32 and moe_align_capacity below 2^26

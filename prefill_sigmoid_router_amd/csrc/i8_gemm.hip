@@ -10,7 +10,7 @@
 // publishes them.  Only a partial last chunk goes through registers (zero-filled).
 //
 // UP: tokens gathered through the plan, gate and up rows of 32 WN act columns, SwiGLU, act
-// as block floats (below).  DOWN: act rows of the plan, results to the split y rows.  DENSE: plain rows.
+// in fp32 (below).  DOWN: act rows of the plan, results to the split y rows.  DENSE: plain rows.
 #include <math.h>
 
 #include <type_traits>
@@ -45,8 +45,7 @@ struct I8Args {
   const int32_t* num_tiles;
   int act_rows;   // rows of a 128-column block of act
   int n_ntiles, M, K, ncols, top_k, block;   // ncols: act columns (UP), output columns
-  int16_t* act;
-  uint8_t* act_exps;
+  float* act;
   uint16_t* y;
   float* y0;
   void* out;
@@ -113,33 +112,19 @@ __device__ __forceinline__ void scaled_act(i32x4 g0, i32x4 g1, i32x4 u0, i32x4 u
   }
 }
 
-// act leaves the up product as block floats: 32 columns of a row share a power of two (byte
-// E: value = int16 * 2^(E - 141), the largest up to 2^15 - 1), because rounding act to bf16
-// first moves one int8 code in ten by one (the layer's output 0.6 % off in relative L2 instead
-// of 0.2 %) and fp32 is twice the bytes; these 16 bits move one code in 2,000.  Four lanes (lane / 16) hold the 32 columns, 8 each;
-// they call it together.  a: act of this lane's columns, 0 past the last; c: its first column.
+// act leaves the up product in fp32: the codes that it is quantized to next are roundings of
+// its quotients, and a shorter act would move them (bf16 one in ten by one, 16 bits under an
+// exponent of 32 columns one in 2,000: layer outputs 0.6 % and 0.12 % off in relative L2).
+// a: act of this lane's 8 columns from c on.
 // Layout [ceil(I / 128)][rows][128]: what a workgroup writes is one piece of memory.
 __device__ __forceinline__ void store_act(const I8Args& p, int row, int c, const float (&a)[8]) {
-  uint32_t m = 0;   // magnitudes' bits order as they do, infinities and NaN last
+  float* dst = p.act + ((size_t)(c >> 7) * p.act_rows + row) * 128 + (c & 127);
+  if (c < p.ncols) {   // nontemporal: kept out of the way of the weights' stream
 #pragma unroll
-  for (int q = 0; q < 8; ++q) m = max(m, __float_as_uint(a[q]) & 0x7fffffffu);
-  m = max(m, (uint32_t)__shfl_xor((int)m, 16, kWave));
-  m = max(m, (uint32_t)__shfl_xor((int)m, 32, kWave));
-  const uint32_t E = max(m >> 23, 15u);
-  const float mult = E == 255u ? 0.0f : __uint_as_float((268u - E) << 23);   // 2^(141 - E)
-  uint32_t v[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    // (32768 from the last few values below 2^15: 32767; -32768 the same by symmetry)
-    const int lo = E == 255u ? 0 : (int)fminf(fmaxf(rintf(a[2 * q] * mult), -32767.0f), 32767.0f);
-    const int hi = E == 255u ? 0 : (int)fminf(fmaxf(rintf(a[2 * q + 1] * mult), -32767.0f), 32767.0f);
-    v[q] = (uint32_t)(lo & 0xffff) | (uint32_t)hi << 16;
+    for (int h = 0; h < 2; ++h)
+      __builtin_nontemporal_store(f32x4{a[4 * h], a[4 * h + 1], a[4 * h + 2], a[4 * h + 3]},
+                                  reinterpret_cast<f32x4*>(dst) + h);
   }
-  const size_t block_row = (size_t)(c >> 7) * p.act_rows + row;
-  if (c < p.ncols)   // nontemporal: 60 us less of 1,660 beside the weights' stream
-    __builtin_nontemporal_store(u32x4{v[0], v[1], v[2], v[3]},
-                                reinterpret_cast<u32x4*>(p.act + block_row * 128 + (c & 127)));
-  if ((c & 31) == 0 && c < p.ncols) p.act_exps[block_row * 4 + ((c >> 5) & 3)] = (uint8_t)E;
 }
 
 // 16 results of pick i, columns n0 on: every pick in fp32 in y0, or (with y) the first of each
@@ -882,12 +867,11 @@ hipError_t launch_i8_up(const int8_t* x, const float* x_scale, const int8_t* w13
                         const float* w13_scale, const int32_t* sorted_ids,
                         const int32_t* block_expert, const int2* tiles, const int32_t* num_tiles,
                         int max_tiles, int tile_rows, int H, int I, int top_k,
-                        int block, int16_t* act, uint8_t* act_exps, int act_rows,
+                        int block, float* act, int act_rows,
                         hipStream_t s) {
   I8Args p = grouped(x, x_scale, w13, w13_scale, sorted_ids, block_expert, tiles, num_tiles, H, I,
                      top_k, block);
   p.act = act;
-  p.act_exps = act_exps;
   p.act_rows = act_rows;
   return launch_expert<kUp>(p, max_tiles, tile_rows, s);
 }

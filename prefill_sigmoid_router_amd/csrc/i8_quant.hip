@@ -96,82 +96,69 @@ __global__ __launch_bounds__(kQThreads) void i8_rows_kernel(const uint16_t* __re
         zero ? uint2{0u, 0u} : codes8(ld16(src + (size_t)ch * 8), q);
 }
 
-// Rows of a plan (one wave each) from the block floats of the up GEMM: 32 values share the
-// byte E, value = int16 * 2^(E - 141); E = 255 marks a block that is not finite.  Rows that
-// hold no real entry are skipped.  The row's maximum and the codes come from the stored
-// values, whose rounding (2^-15 of the block's largest value at most) moves a code by one
-// only where 127 v / a lies within 127 * 2^-15 of a border.
+// Rows of a plan (one wave each) from the act of the up GEMM.  Rows that hold no real entry
+// are skipped.  127 v and the quotient round once each in fp32, which moves a code by one only
+// where 127 v / a lies within 127 * 2^-23 of a border.
 __global__ __launch_bounds__(kQThreads) void i8_act_kernel(
-    const int16_t* __restrict__ act, const uint8_t* __restrict__ exps, int64_t rows, int I,
-    const int32_t* __restrict__ plan, const int32_t* __restrict__ num_padded, int n_ids,
-    int8_t* __restrict__ codes, float* __restrict__ scales) {
+    const float* __restrict__ act, int64_t rows, int I, const int32_t* __restrict__ plan,
+    const int32_t* __restrict__ num_padded, int n_ids, int8_t* __restrict__ codes,
+    float* __restrict__ scales) {
   constexpr int KEEP = 4;       // 8-value chunks per lane kept in registers (I <= 2048)
   const int lane = threadIdx.x & 63;
   const int64_t row = (int64_t)blockIdx.x * (kQThreads / kWave) + (threadIdx.x >> 6);
   if (row >= *num_padded || (uint32_t)plan[row] >= (uint32_t)n_ids) return;
-  auto value8 = [&](int ch) { return act + ((ch >> 4) * rows + row) * 128 + (ch & 15) * 8; };
-  auto exp8 = [&](int ch) { return exps[((ch >> 4) * rows + row) * 4 + ((ch >> 2) & 3)]; };
   const int nchunk = I >> 3;
-  auto unit = [](uint32_t e) { return __uint_as_float((e - 14u) << 23); };   // 2^(e - 141)
-  auto largest = [](u32x4 v) {
-    int m = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) m = max(m, max(abs((int)(int16_t)v[j]), abs((int)v[j] >> 16)));
-    return (float)m;
+  struct Chunk {
+    u32x4 lo, hi;
   };
-  u32x4 keep[KEEP];
-  uint32_t e[KEEP];
-  float top = 0.0f;
-  bool bad = false;
+  auto load = [&](int ch) {
+    const float* v = act + ((ch >> 4) * rows + row) * 128 + (ch & 15) * 8;
+    return Chunk{ld16(v), ld16(v + 4)};
+  };
+  auto largest = [](uint32_t m, const Chunk& v) {   // magnitudes' bits order as they do
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = max(m, max(v.lo[j] & 0x7fffffffu, v.hi[j] & 0x7fffffffu));
+    return m;
+  };
+  Chunk keep[KEEP];
+  uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < KEEP; ++i) {
     const int ch = lane + kWave * i;
-    const bool in = ch < nchunk;
-    keep[i] = in ? ld16(value8(ch)) : u32x4{0, 0, 0, 0};
-    e[i] = in ? exp8(ch) : 15u;
+    keep[i] = ch < nchunk ? load(ch) : Chunk{u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}};
   }
 #pragma unroll
-  for (int i = 0; i < KEEP; ++i) {
-    bad |= e[i] == 255u;
-    top = fmaxf(top, largest(keep[i]) * unit(e[i]));
-  }
-  for (int ch = lane + kWave * KEEP; ch < nchunk; ch += kWave) {
-    const uint32_t ex = exp8(ch);
-    bad |= ex == 255u;
-    top = fmaxf(top, largest(ld16(value8(ch))) * unit(ex));
-  }
+  for (int i = 0; i < KEEP; ++i) m = largest(m, keep[i]);
+  for (int ch = lane + kWave * KEEP; ch < nchunk; ch += kWave) m = largest(m, load(ch));
 #pragma unroll
-  for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, kWave));
-  bad = __any(bad);
+  for (int off = 32; off > 0; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, kWave));
+  const float top = __uint_as_float(m);
+  const bool bad = m >= 0x7f800000u;   // an infinity or a NaN
   if (lane == 0) scales[row] = bad ? __uint_as_float(0x7fc00000u) : top / 127.0f;
-  const bool zero = bad || top == 0.0f;
+  const bool zero = bad || m == 0;
   const Quotient q = quotient_of(top);
-  auto put = [&](int ch, u32x4 v, uint32_t ex) {
-    const float u = unit(ex);
-    uint32_t c[8];
+  auto put = [&](int ch, const Chunk& v) {
+    uint2 c = {0u, 0u};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      c[2 * j] = code_of((float)(int16_t)v[j] * u, q);
-      c[2 * j + 1] = code_of((float)((int)v[j] >> 16) * u, q);
+      c.x |= code_of(__uint_as_float(v.lo[j]), q) << (8 * j);
+      c.y |= code_of(__uint_as_float(v.hi[j]), q) << (8 * j);
     }
-    const uint2 out = {c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24,
-                       c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24};
-    *reinterpret_cast<uint2*>(codes + row * I + (size_t)ch * 8) = zero ? uint2{0u, 0u} : out;
+    *reinterpret_cast<uint2*>(codes + row * I + (size_t)ch * 8) = zero ? uint2{0u, 0u} : c;
   };
 #pragma unroll
   for (int i = 0; i < KEEP; ++i)
-    if (lane + kWave * i < nchunk) put(lane + kWave * i, keep[i], e[i]);
-  for (int ch = lane + kWave * KEEP; ch < nchunk; ch += kWave)
-    put(ch, ld16(value8(ch)), exp8(ch));
+    if (lane + kWave * i < nchunk) put(lane + kWave * i, keep[i]);
+  for (int ch = lane + kWave * KEEP; ch < nchunk; ch += kWave) put(ch, load(ch));
 }
 
 }  // namespace
 
-hipError_t launch_i8_act(const int16_t* act, const uint8_t* exps, int64_t rows, int I,
-                         const int32_t* plan, const int32_t* num_padded, int n_ids, int8_t* codes,
-                         float* scales, hipStream_t s) {
+hipError_t launch_i8_act(const float* act, int64_t rows, int I, const int32_t* plan,
+                         const int32_t* num_padded, int n_ids, int8_t* codes, float* scales,
+                         hipStream_t s) {
   const dim3 grid((unsigned)((rows + 3) / 4));
-  hipLaunchKernelGGL(i8_act_kernel, grid, dim3(kQThreads), 0, s, act, exps, rows, I, plan,
+  hipLaunchKernelGGL(i8_act_kernel, grid, dim3(kQThreads), 0, s, act, rows, I, plan,
                      num_padded, n_ids, codes, scales);
   return hipGetLastError();
 }

@@ -189,29 +189,27 @@ hipError_t launch_expert_down_frag_mx(const uint16_t* act, const uint8_t* w2c, c
                                      hipStream_t s);
 
 // int8 rows (i8_quant.hip): bf16 [rows, K] (K % 8 == 0) -> codes and the scale of each row;
-// and from the block floats of the up GEMM (int16 [ceil(I / 128)][rows][128], bytes
-// [ceil(I / 128)][rows][4], one per 32 values), for the plan rows below *num_padded whose id
-// is in [0, n_ids).
+// and from the act of the up GEMM (fp32 [ceil(I / 128)][rows][128]), for the plan rows below
+// *num_padded whose id is in [0, n_ids).
 hipError_t launch_i8_rows(const uint16_t* v, int64_t rows, int K, int8_t* codes, float* scales,
                           hipStream_t s);
-hipError_t launch_i8_act(const int16_t* act, const uint8_t* exps, int64_t rows, int I,
-                         const int32_t* plan, const int32_t* num_padded, int n_ids, int8_t* codes,
-                         float* scales, hipStream_t s);
+hipError_t launch_i8_act(const float* act, int64_t rows, int I, const int32_t* plan,
+                         const int32_t* num_padded, int n_ids, int8_t* codes, float* scales,
+                         hipStream_t s);
 
 // int8 products (i8_gemm.hip); K % 16 == 0.  Dense: out [M, N] (bf16, or fp32 with f32) =
 // a_scale[m] w_scale[n] sum_k a[m,k] w[n,k].
 hipError_t launch_i8_matmul(const int8_t* a, const float* a_scale, const int8_t* w,
                             const float* w_scale, int M, int N, int K, void* out, bool f32,
                             hipStream_t s);
-// Grouped over the tiles (height tile_rows, 64, 128 or 256) of a plan: up + SwiGLU -> act as
-// block floats (act_rows = capacity rows) from the tokens' codes [M, H]; down from act's codes
+// Grouped over the tiles (height tile_rows, 64, 128 or 256) of a plan: up + SwiGLU -> act
+// (fp32, act_rows = capacity rows) from the tokens' codes [M, H]; down from act's codes
 // [capacity, I] to the split rows y / y0 of moe_forward, or, without y, to fp32 rows y0.
 hipError_t launch_i8_up(const int8_t* x, const float* x_scale, const int8_t* w13,
                         const float* w13_scale, const int32_t* sorted_ids,
                         const int32_t* block_expert, const int2* tiles, const int32_t* num_tiles,
                         int max_tiles, int tile_rows, int H, int I, int top_k,
-                        int block, int16_t* act, uint8_t* act_exps, int act_rows,
-                        hipStream_t s);
+                        int block, float* act, int act_rows, hipStream_t s);
 hipError_t launch_i8_down(const int8_t* act, const float* act_scale, const int8_t* w2,
                           const float* w2_scale, const int32_t* sorted_ids,
                           const int32_t* block_expert, const int2* tiles,

@@ -703,14 +703,11 @@ bool make_rule(int32_t E, int32_t top_k, int32_t score, int32_t n_group, int32_t
 // the int8 act with their scales.
 struct I8Layout {
   Layout base;
-  size_t keys, xq, xs, am, ae, as, yf, total;   // the codes of act take the place of its bf16
+  size_t keys, xq, xs, af, as, yf, total;   // the codes of act take the place of its bf16
 };
 
 // Results of the down GEMM up to this many stay in fp32 (64 MB): they cost nothing that can be
-// measured there, and bf16 picks add as much to the error of the layer's outputs as the 16-bit
-// act between the products (M=8, H=7168, I=2048, k=16: relative L2 0.24 % with bf16 picks, 0.20 %
-// without, 0.17 % being the outputs' own rounding).  More would double hundreds of MB (M=2048:
-// 0.47 GB).
+// measured there.  More would double hundreds of MB (M=2048: 0.47 GB).
 constexpr int64_t kMaxF32Y = (int64_t)1 << 24;
 
 I8Layout i8_layout_of(int32_t M, int32_t H, int32_t E, int32_t I, int32_t top_k, int32_t block) {
@@ -722,8 +719,7 @@ I8Layout i8_layout_of(int32_t M, int32_t H, int32_t E, int32_t I, int32_t top_k,
   L.keys = off;  off += round_up(moe::route_groups_scratch_bytes(M, E), kAlign);
   L.xq = off;  off += round_up((size_t)M * H, kAlign);
   L.xs = off;  off += round_up((size_t)M * sizeof(float), kAlign);
-  L.am = off;  off += round_up(cap * blocks * 128 * sizeof(int16_t), kAlign);
-  L.ae = off;  off += round_up(cap * blocks * 4, kAlign);
+  L.af = off;  off += round_up(cap * blocks * 128 * sizeof(float), kAlign);
   L.as = off;  off += round_up(cap * sizeof(float), kAlign);
   L.yf = off;  off += (size_t)std::min((int64_t)M * top_k * H, kMaxF32Y) * sizeof(float);
   L.total = round_up(off, kAlign);
@@ -882,8 +878,7 @@ int moe_forward_i8(const uint16_t* x, const uint16_t* router_w, const float* sel
   int32_t* npad = num_padded_out ? num_padded_out : reinterpret_cast<int32_t*>(ws + B.npad);
   int2* tiles = reinterpret_cast<int2*>(ws + B.tiles);
   int32_t* ntiles = reinterpret_cast<int32_t*>(ws + B.ntiles);
-  int16_t* act = reinterpret_cast<int16_t*>(ws + L.am);
-  uint8_t* ae = reinterpret_cast<uint8_t*>(ws + L.ae);
+  float* act = reinterpret_cast<float*>(ws + L.af);
   uint16_t* y = reinterpret_cast<uint16_t*>(ws + B.y);
   float* y0 = reinterpret_cast<float*>(ws + B.y0);
   if ((int64_t)M * top_k * H <= kMaxF32Y) {
@@ -913,10 +908,10 @@ int moe_forward_i8(const uint16_t* x, const uint16_t* router_w, const float* sel
     return MOE_ERR_HIP;
   if (!mark(2)) return MOE_ERR_HIP;
   if (moe::launch_i8_up(xq, xs, w13_codes, w13_scales, sorted, bexp, tiles, ntiles, max_tiles,
-                        trows, H, I, top_k, block, act, ae, (int)cap, s) != hipSuccess)
+                        trows, H, I, top_k, block, act, (int)cap, s) != hipSuccess)
     return MOE_ERR_HIP;
   if (!mark(3)) return MOE_ERR_HIP;
-  if (moe::launch_i8_act(act, ae, (int64_t)cap, I, sorted, npad, n, aq, as, s) != hipSuccess ||
+  if (moe::launch_i8_act(act, (int64_t)cap, I, sorted, npad, n, aq, as, s) != hipSuccess ||
       moe::launch_i8_down(aq, as, w2_codes, w2_scales, sorted, bexp, tiles, ntiles, max_tiles,
                           trows, H, I, top_k, block, y, y0, s) != hipSuccess)
     return MOE_ERR_HIP;

@@ -1,0 +1,115 @@
+"""Grouped routing, int8 products and the int8 layer where they can go wrong by little: tighter
+bounds than the shape grids', sums and scores at the ends of their types, kernels that only large
+sizes reach.  Against the 64-bit oracle."""
+import numpy as np
+import pytest
+import torch
+
+import _bars as bars
+import moe_inputs as mi
+from oracle import i8_oracle as orc
+from oracle import moe_oracle
+from oracle.moe_oracle import bf16_to_f64
+
+pytestmark = pytest.mark.gpu
+bits = mi.bf16_bits
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch.device("cuda:0")
+
+
+@pytest.fixture(scope="module")
+def B(dev):
+    from prefill_sigmoid_router_amd import binding
+    binding.load_library()
+    return binding
+
+
+# ---------------------------------------------------------------------------------------
+# The layer, code by code
+# ---------------------------------------------------------------------------------------
+def _quantize(B, v):
+    codes = torch.full(tuple(v.shape), 99, dtype=torch.int8, device=v.device)
+    scales = torch.full(tuple(v.shape[:-1]), float("nan"), dtype=torch.float32, device=v.device)
+    B.moe_i8_quantize(v, codes, scales)
+    return codes, scales
+
+
+def _layer_reference(xq, xs, ids, weights, w13, s13, w2, s2):
+    """m = sum of the weighted picks, and how far it may be off, for the rows given.
+
+    Relative errors in units of u = 2^-24.  gate and up: the sum, the token's scale, the scales'
+    product and the product of both round once each: 4.  silu(g) = g / (1 + exp(-g)) changes by
+    at most 1 + |g| times what g does; exp is exp2 of a rounded product (log2 e rounded too: 1.5
+    |g|, and 2 of its own), 1 + exp and the product with g round once, the reciprocal is good
+    to 2: 4 (1 + |g|) + 1.5 |g| + 2 + 1 + 1 + 2 = 5.5 |g| + 10.  times up (4, and 1 for the
+    product): act 5.5 |g| + 15.  127 act / a, a an act itself: both, and 2 for the product and
+    the division (the scale a / 127 one more).  A code may be the next one where its quotient is
+    that near to a border.  A result: the sum, the scales' product, and both's product round: 3,
+    the scale's own error, and the code's; the weighted sum rounds 2 k times more, the weight
+    once (and once in the division that made it)."""
+    u = 2.0 ** -24
+    n, k = ids.shape
+    H = xq.shape[1]
+    I = w13.shape[1] // 2
+    m, tol, terms = np.zeros((n, H)), np.zeros((n, H)), np.zeros((n, H))
+    for e in np.unique(ids):
+        t, j = np.nonzero(ids == e)
+        h = orc.matmul(xq[t], xs[t], w13[e], s13[e])
+        g = h[:, :I]
+        act = g / (1.0 + np.exp(-g)) * h[:, I:]
+        off = 5.5 * np.abs(g) + 15.0
+        at = np.abs(act).argmax(axis=1)[:, None]
+        top_off = np.take_along_axis(off, at, 1)
+        q = 127.0 * act / np.abs(np.take_along_axis(act, at, 1))
+        off = np.abs(q) * (off + top_off + 2.0) * u
+        near = np.abs(np.abs(q - np.rint(q)) - 0.5) <= off
+        codes, scale = orc.quantize(act)
+        wt = weights[t, j][:, None]
+        y = orc.matmul(codes, scale, w2[e], s2[e])
+        moved = (near.astype(np.float64) @ np.abs(w2[e].astype(np.float64)).T) * scale[:, None] * s2[e][None, :]
+        np.add.at(m, t, wt * y)
+        np.add.at(terms, t, np.abs(wt * y))
+        np.add.at(tol, t, np.abs(wt) * (np.abs(y) * (top_off + 1 + 3) * u + moved))
+    return m, tol + terms * (2 * k + 3) * u
+
+
+def _check_z(got, m, tol, residual):
+    """z = m + residual, rounded to bf16: half a unit of the last place, at the largest it may be."""
+    z = m + residual
+    tol = tol + 2.0 ** -24 * (np.abs(z) + tol)
+    err = np.abs(got.double().cpu().numpy() - z)
+    bound = tol + 0.5 * bars.bf16_ulp(np.abs(z) + tol)
+    worst = np.unravel_index(np.argmax(err - bound), err.shape)
+    assert (err <= bound).all(), f"{(err > bound).sum()} of {err.size} off, {err[worst]:.3e} at {worst}, bound {bound[worst]:.3e}"
+
+
+@pytest.mark.parametrize("M,H,E,I,k,block", [(3, 256, 8, 2048, 4, 16), (40, 656, 4, 768, 2, 16),
+                                             (64, 272, 12, 48, 3, 32), (205, 768, 4, 1408, 1, 16),
+                                             (450, 784, 4, 784, 2, 16), (300, 400, 8, 256, 3, 64),
+                                             (9, 512, 3, 8208, 2, 16)])
+def test_layer_is_off_only_by_codes_at_a_border(B, dev, M, H, E, I, k, block):
+    """No residual, so that sums near 0 show what the bf16 rounding of others hides."""
+    g = torch.Generator(device=dev).manual_seed(M + I)
+    n = lambda *s, std=1.0: torch.randn(*s, generator=g, device=dev) * std  # noqa: E731
+    x, wr = n(M, H).bfloat16(), n(E, H, std=1.7 / H ** 0.5).bfloat16()
+    w13, s13 = _quantize(B, n(E, 2 * I, H, std=1.0 / H ** 0.5).bfloat16())
+    w2, s2 = _quantize(B, n(E, H, I, std=1.0 / I ** 0.5).bfloat16())
+    zero, one = torch.zeros(M, H, dtype=torch.bfloat16, device=dev), torch.ones(H, dtype=torch.bfloat16, device=dev)
+    out, z = torch.empty_like(zero), torch.full_like(zero, float("nan"))
+    ids = torch.full((M, k), -7, dtype=torch.int32, device=dev)
+    w = torch.full((M, k), float("nan"), device=dev)
+    ws = torch.full((B.moe_i8_workspace_bytes(M, H, E, I, k, block),), 0xFF, dtype=torch.uint8, device=dev)
+    B.moe_forward_i8(x, wr, None, w13, s13, w2, s2, zero, one, 1e-5, k, block, out, ws, residual_out=z,
+                     topk_ids_out=ids, topk_w_out=w)
+    torch.cuda.synchronize()
+    f64 = lambda t: t.double().cpu().numpy()  # noqa: E731
+    rid, rw = orc.route(bits(x), bits(wr), None, k)
+    assert np.array_equal(ids.cpu().numpy(), rid)
+    xq, xs = orc.quantize(bf16_to_f64(bits(x)))
+    m, tol = _layer_reference(xq, xs, rid, f64(w), w13.cpu().numpy(), f64(s13), w2.cpu().numpy(), f64(s2))
+    _check_z(z, m, tol, 0.0)
