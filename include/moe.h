@@ -458,12 +458,12 @@ int moe_i8_matmul(const int8_t* a, const float* a_scales, const int8_t* w, const
  * [E, 2I], w2_codes [E, H, I] + w2_scales [E, H]) and the router of moe_route_groups in place
  * of step 1.  x is quantized row by row (a scale per token); the up GEMM runs on the codes,
  * SwiGLU in fp32; act (fp32) is quantized row by row (a scale per token and pick); the down
- * GEMM runs on the codes;
- * finalize as in moe_forward.  Other arguments, stage events (quantizing x counts to step 1,
- * quantizing act to step 4) and outputs are those of moe_forward.  H % 16 == 0 and
- * I % 16 == 0, I <= 131072; M below 2^22, M * H below 2^32 and moe_align_capacity below 2^26
- * (MOE_ERR_UNSUPPORTED otherwise); codes and their scales 16-byte aligned; workspace of
- * moe_i8_workspace_bytes bytes (0 for sizes that are refused), 256-byte aligned.
+ * GEMM runs on the codes, its results stay in fp32; finalize as in moe_forward.  Other
+ * arguments, stage events (quantizing x counts to step 1, quantizing act to step 4) and
+ * outputs are those of moe_forward.  H % 16 == 0 and I % 16 == 0, I <= 131072; M below 2^22,
+ * M * H below 2^32 and moe_align_capacity below 2^26 (MOE_ERR_UNSUPPORTED otherwise); codes
+ * and their scales 16-byte aligned; workspace of moe_i8_workspace_bytes bytes (0 for sizes
+ * that are refused), 256-byte aligned.
  */
 size_t moe_i8_workspace_bytes(int32_t M, int32_t H, int32_t E, int32_t I, int32_t top_k,
                               int32_t block);

@@ -204,7 +204,7 @@ hipError_t launch_i8_matmul(const int8_t* a, const float* a_scale, const int8_t*
                             hipStream_t s);
 // Grouped over the tiles (height tile_rows, 64, 128 or 256) of a plan: up + SwiGLU -> act
 // (fp32, act_rows = capacity rows) from the tokens' codes [M, H]; down from act's codes
-// [capacity, I] to the split rows y / y0 of moe_forward, or, without y, to fp32 rows y0.
+// [capacity, I] to the picks' fp32 rows of y.
 hipError_t launch_i8_up(const int8_t* x, const float* x_scale, const int8_t* w13,
                         const float* w13_scale, const int32_t* sorted_ids,
                         const int32_t* block_expert, const int2* tiles, const int32_t* num_tiles,
@@ -214,7 +214,7 @@ hipError_t launch_i8_down(const int8_t* act, const float* act_scale, const int8_
                           const float* w2_scale, const int32_t* sorted_ids,
                           const int32_t* block_expert, const int2* tiles,
                           const int32_t* num_tiles, int max_tiles, int tile_rows, int H, int I,
-                          int top_k, int block, uint16_t* y, float* y0, hipStream_t s);
+                          int top_k, int block, float* y, hipStream_t s);
 
 // Weighted top-k combine + residual add + RMSNorm over fp32 rows of y, or over moe_forward's
 // split rows (first picks in fp32 in y0, the others in bf16 in y).

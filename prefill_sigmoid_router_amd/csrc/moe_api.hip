@@ -699,30 +699,41 @@ bool make_rule(int32_t E, int32_t top_k, int32_t score, int32_t n_group, int32_t
   return true;
 }
 
-// Workspace layout of moe_forward_i8: the routed-MoE layer's regions, the int8 tokens and
-// the int8 act with their scales.
-struct I8Layout {
-  Layout base;
-  size_t keys, xq, xs, af, as, yf, total;   // the codes of act take the place of its bf16
-};
+constexpr int kI8MinTileRows = 64;
 
-// Results of the down GEMM up to this many stay in fp32 (64 MB): they cost nothing that can be
-// measured there.  More would double hundreds of MB (M=2048: 0.47 GB).
-constexpr int64_t kMaxF32Y = (int64_t)1 << 24;
+// Workspace layout of moe_forward_i8.  act (the up GEMM's, fp32) is read for the last time
+// when it is quantized, and y (the down GEMM's, fp32) written after that: they share memory.
+struct I8Layout {
+  size_t route, ids, w, sorted, bexp, npad, tiles, ntiles, xq, xs, aq, as, act, fin, total;
+};
 
 I8Layout i8_layout_of(int32_t M, int32_t H, int32_t E, int32_t I, int32_t top_k, int32_t block) {
   I8Layout L;
-  L.base = layout_of(M, H, E, I, top_k, block);
-  const size_t cap = capacity_of(M, top_k, E, block);
-  const size_t blocks = ((size_t)I + 127) / 128;
-  size_t off = round_up(L.base.total, kAlign);
-  L.keys = off;  off += round_up(moe::route_groups_scratch_bytes(M, E), kAlign);
-  L.xq = off;  off += round_up((size_t)M * H, kAlign);
-  L.xs = off;  off += round_up((size_t)M * sizeof(float), kAlign);
-  L.af = off;  off += round_up(cap * blocks * 128 * sizeof(float), kAlign);
-  L.as = off;  off += round_up(cap * sizeof(float), kAlign);
-  L.yf = off;  off += (size_t)std::min((int64_t)M * top_k * H, kMaxF32Y) * sizeof(float);
-  L.total = round_up(off, kAlign);
+  const size_t n = (size_t)M * top_k, cap = capacity_of(M, top_k, E, block);
+  const size_t act = cap * (((size_t)I + 127) / 128) * 128 * sizeof(float);
+  const size_t y = n * (size_t)H * sizeof(float);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += round_up(bytes, kAlign);
+    return at;
+  };
+  L.route = take(moe::route_groups_scratch_bytes(M, E));
+  L.ids = take(n * sizeof(int32_t));
+  L.w = take(n * sizeof(float));
+  L.sorted = take(cap * sizeof(int32_t));
+  L.bexp = take(cap / block * sizeof(int32_t));
+  L.npad = take(sizeof(int32_t));
+  L.tiles = take((size_t)moe::tile_capacity((int)n, E, kI8MinTileRows) * sizeof(int2));
+  L.ntiles = take(sizeof(int32_t));
+  L.xq = take((size_t)M * H);
+  L.xs = take((size_t)M * sizeof(float));
+  L.aq = take(cap * (size_t)I);
+  L.as = take(cap * sizeof(float));
+  L.act = take(std::max(act, y));
+  // (sized for fewer tokens too, so that a workspace does for any smaller M)
+  L.fin = take(moe::finalize_slices_scratch_bytes(std::min(M, moe::kFinSlicesMaxTokens - 1), H));
+  L.total = off;
   return L;
 }
 
@@ -743,7 +754,7 @@ bool i8_grids_ok(int32_t M, int32_t H, int32_t E, int32_t top_k, int32_t block) 
 // 204, 128 306 / 258 / 228, 256 481 / 393 / 345).
 int i8_tile_rows(int32_t M, int32_t E, int32_t top_k) {
   const int64_t per_expert = (int64_t)M * top_k / E;
-  return per_expert < 32 ? 64 : per_expert < 96 ? 128 : 256;
+  return per_expert < 32 ? kI8MinTileRows : per_expert < 96 ? 128 : 256;
 }
 
 }  // namespace
@@ -870,25 +881,19 @@ int moe_forward_i8(const uint16_t* x, const uint16_t* router_w, const float* sel
   if (!workspace || !aligned(workspace, kAlign) || workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
 
   char* ws = static_cast<char*>(workspace);
-  const Layout& B = L.base;
-  int32_t* ids = topk_ids_out ? topk_ids_out : reinterpret_cast<int32_t*>(ws + B.ids);
-  float* w = topk_w_out ? topk_w_out : reinterpret_cast<float*>(ws + B.w);
-  int32_t* sorted = sorted_ids_out ? sorted_ids_out : reinterpret_cast<int32_t*>(ws + B.sorted);
-  int32_t* bexp = block_expert_out ? block_expert_out : reinterpret_cast<int32_t*>(ws + B.bexp);
-  int32_t* npad = num_padded_out ? num_padded_out : reinterpret_cast<int32_t*>(ws + B.npad);
-  int2* tiles = reinterpret_cast<int2*>(ws + B.tiles);
-  int32_t* ntiles = reinterpret_cast<int32_t*>(ws + B.ntiles);
-  float* act = reinterpret_cast<float*>(ws + L.af);
-  uint16_t* y = reinterpret_cast<uint16_t*>(ws + B.y);
-  float* y0 = reinterpret_cast<float*>(ws + B.y0);
-  if ((int64_t)M * top_k * H <= kMaxF32Y) {
-    y = nullptr;
-    y0 = reinterpret_cast<float*>(ws + L.yf);
-  }
+  int32_t* ids = topk_ids_out ? topk_ids_out : reinterpret_cast<int32_t*>(ws + L.ids);
+  float* w = topk_w_out ? topk_w_out : reinterpret_cast<float*>(ws + L.w);
+  int32_t* sorted = sorted_ids_out ? sorted_ids_out : reinterpret_cast<int32_t*>(ws + L.sorted);
+  int32_t* bexp = block_expert_out ? block_expert_out : reinterpret_cast<int32_t*>(ws + L.bexp);
+  int32_t* npad = num_padded_out ? num_padded_out : reinterpret_cast<int32_t*>(ws + L.npad);
+  int2* tiles = reinterpret_cast<int2*>(ws + L.tiles);
+  int32_t* ntiles = reinterpret_cast<int32_t*>(ws + L.ntiles);
   int8_t* xq = reinterpret_cast<int8_t*>(ws + L.xq);
   float* xs = reinterpret_cast<float*>(ws + L.xs);
-  int8_t* aq = reinterpret_cast<int8_t*>(ws + B.act);
+  float* act = reinterpret_cast<float*>(ws + L.act);
+  int8_t* aq = reinterpret_cast<int8_t*>(ws + L.aq);
   float* as = reinterpret_cast<float*>(ws + L.as);
+  float* y = reinterpret_cast<float*>(ws + L.act);
   hipStream_t s = (hipStream_t)stream;
 
   const int n = M * top_k;
@@ -898,7 +903,7 @@ int moe_forward_i8(const uint16_t* x, const uint16_t* router_w, const float* sel
     return !stage_events || hipEventRecord((hipEvent_t)stage_events[i], s) == hipSuccess;
   };
   if (!mark(0)) return MOE_ERR_HIP;
-  if (moe::launch_route_groups(x, router_w, select_bias, M, H, E, top_k, rule, ids, w, ws + L.keys,
+  if (moe::launch_route_groups(x, router_w, select_bias, M, H, E, top_k, rule, ids, w, ws + L.route,
                                s) != hipSuccess ||
       moe::launch_i8_rows(x, M, H, xq, xs, s) != hipSuccess)
     return MOE_ERR_HIP;
@@ -913,20 +918,14 @@ int moe_forward_i8(const uint16_t* x, const uint16_t* router_w, const float* sel
   if (!mark(3)) return MOE_ERR_HIP;
   if (moe::launch_i8_act(act, (int64_t)cap, I, sorted, npad, n, aq, as, s) != hipSuccess ||
       moe::launch_i8_down(aq, as, w2_codes, w2_scales, sorted, bexp, tiles, ntiles, max_tiles,
-                          trows, H, I, top_k, block, y, y0, s) != hipSuccess)
+                          trows, H, I, top_k, block, y, s) != hipSuccess)
     return MOE_ERR_HIP;
   if (!mark(4)) return MOE_ERR_HIP;
-  float* fin = reinterpret_cast<float*>(ws + B.fin);
-  const bool slices = M < moe::kFinSlicesMaxTokens;
   const hipError_t fin_err =
-      y && slices ? moe::launch_finalize_slices(y, y0, w, residual, norm_w, eps, M, H, top_k, out,
-                                                residual_out, fin, s)
-      : y         ? moe::launch_finalize(y, y0, w, residual, norm_w, eps, M, H, top_k, out,
-                                         residual_out, s)
-      : slices    ? moe::launch_finalize_slices(y0, w, residual, norm_w, eps, M, H, top_k, out,
-                                                residual_out, fin, s)
-                  : moe::launch_finalize(y0, w, residual, norm_w, eps, M, H, top_k, out,
-                                         residual_out, s);
+      M < moe::kFinSlicesMaxTokens
+          ? moe::launch_finalize_slices(y, w, residual, norm_w, eps, M, H, top_k, out, residual_out,
+                                        reinterpret_cast<float*>(ws + L.fin), s)
+          : moe::launch_finalize(y, w, residual, norm_w, eps, M, H, top_k, out, residual_out, s);
   if (fin_err != hipSuccess) return MOE_ERR_HIP;
   if (!mark(5)) return MOE_ERR_HIP;
   return MOE_OK;

@@ -91,9 +91,12 @@ def _check_z(got, m, tol, residual):
 @pytest.mark.parametrize("M,H,E,I,k,block", [(3, 256, 8, 2048, 4, 16), (40, 656, 4, 768, 2, 16),
                                              (64, 272, 12, 48, 3, 32), (205, 768, 4, 1408, 1, 16),
                                              (450, 784, 4, 784, 2, 16), (300, 400, 8, 256, 3, 64),
-                                             (9, 512, 3, 8208, 2, 16)])
+                                             (9, 512, 3, 8208, 2, 16),
+                                             # more than 2^24 results of the down product
+                                             (1100, 4096, 4, 640, 4, 64), (200, 16384, 8, 16, 8, 16)])
 def test_layer_is_off_only_by_codes_at_a_border(B, dev, M, H, E, I, k, block):
-    """No residual, so that sums near 0 show what the bf16 rounding of others hides."""
+    """No residual, so that sums near 0 show what the bf16 rounding of others hides.  Of many
+    tokens the first, the last and some between are compared."""
     g = torch.Generator(device=dev).manual_seed(M + I)
     n = lambda *s, std=1.0: torch.randn(*s, generator=g, device=dev) * std  # noqa: E731
     x, wr = n(M, H).bfloat16(), n(E, H, std=1.7 / H ** 0.5).bfloat16()
@@ -110,6 +113,7 @@ def test_layer_is_off_only_by_codes_at_a_border(B, dev, M, H, E, I, k, block):
     f64 = lambda t: t.double().cpu().numpy()  # noqa: E731
     rid, rw = orc.route(bits(x), bits(wr), None, k)
     assert np.array_equal(ids.cpu().numpy(), rid)
-    xq, xs = orc.quantize(bf16_to_f64(bits(x)))
-    m, tol = _layer_reference(xq, xs, rid, f64(w), w13.cpu().numpy(), f64(s13), w2.cpu().numpy(), f64(s2))
-    _check_z(z, m, tol, 0.0)
+    at = np.unique(np.linspace(0, M - 1, 60).astype(int)) if M * H > 1 << 20 else np.arange(M)
+    xq, xs = orc.quantize(bf16_to_f64(bits(x))[at])
+    m, tol = _layer_reference(xq, xs, rid[at], f64(w)[at], w13.cpu().numpy(), f64(s13), w2.cpu().numpy(), f64(s2))
+    _check_z(z[torch.from_numpy(at).to(dev)], m, tol, 0.0)
