@@ -557,7 +557,8 @@ __device__ __forceinline__ Fast collect_fast(const double (&l)[SL], const double
       for (int s = 0; s < SL; ++s) {
         const float z = v[s] - top;
         c[s] = live >> s & 1 ? __expf(z) : 0.0f;
-        dc[s] = c[s] * (dv[s] + 0.6f * dv[s] * dv[s] + (4.0f - z) * u);
+        // (below the smallest normal number, 87.3 under the top, __expf gives 0)
+        dc[s] = c[s] * (dv[s] + 0.6f * dv[s] * dv[s] + (4.0f - z) * u) + 0x1p-125f;
         total += c[s];
       }
       if (bias) {

@@ -117,3 +117,71 @@ def test_layer_is_off_only_by_codes_at_a_border(B, dev, M, H, E, I, k, block):
     xq, xs = orc.quantize(bf16_to_f64(bits(x))[at])
     m, tol = _layer_reference(xq, xs, rid[at], f64(w)[at], w13.cpu().numpy(), f64(s13), w2.cpu().numpy(), f64(s2))
     _check_z(z[torch.from_numpy(at).to(dev)], m, tol, 0.0)
+
+
+# ---------------------------------------------------------------------------------------
+# Routing: scores and sums at the ends of their types
+# ---------------------------------------------------------------------------------------
+def _rule(rule):
+    r = dict(softmax=False, n_group=1, topk_group=1, group_top=1, renormalize=True, scale=1.0)
+    r.update(rule)
+    return r, dict({n: v for n, v in r.items() if n != "softmax"}, score=1 if r["softmax"] else 0)
+
+
+def _picks(M, k, dev):
+    return (torch.full((M, k), -7, dtype=torch.int32, device=dev),
+            torch.full((M, k), float("nan"), dtype=torch.float32, device=dev))
+
+
+def _from_logits(B, l, bias, k, rule):
+    ids, w = _picks(l.shape[0], k, l.device)
+    B.moe_route_logits(l, bias, k, ids, w, **_rule(rule)[1])
+    torch.cuda.synchronize()
+    return ids.cpu().numpy(), w.double().cpu().numpy()
+
+
+def _from_hidden(B, x, wr, bias, k, rule):
+    M, E = x.shape[0], wr.shape[0]
+    ids, w = _picks(M, k, x.device)
+    ws = torch.full((B.moe_route_groups_workspace_bytes(M, E),), 0xFF, dtype=torch.uint8, device=x.device)
+    B.moe_route_groups(x, wr, bias, k, ids, w, ws, **_rule(rule)[1])
+    torch.cuda.synchronize()
+    return ids.cpu().numpy(), w.double().cpu().numpy()
+
+
+def test_softmax_groups_far_below_the_top_by_hand(B, dev):
+    """exp(-87.5) is no normal number in fp32 any more, but a fifth of group 2's sum, which
+    makes it the larger one: exp(-86) (1 + exp(-1.5)) against exp(-85.95) (1 + exp(-9.05))."""
+    l = torch.tensor([[0.0, -300.0, -300.0, -301.0, -86.0, -87.5, -85.95, -95.0]], device=dev) + 3.0
+    ids, _ = _from_logits(B, l, None, 4, dict(softmax=True, n_group=4, topk_group=2, group_top=2))
+    assert ids.tolist() == [[0, 4, 5, 1]]
+
+
+@pytest.mark.parametrize("group_top", [1, 2])
+@pytest.mark.parametrize("renormalize", [False, True])
+def test_softmax_groups_far_below_the_top(B, dev, group_top, renormalize):
+    rule = dict(softmax=True, n_group=8, topk_group=3, group_top=group_top, renormalize=renormalize)
+    g = torch.Generator().manual_seed(5 + group_top)
+    l = torch.rand(400, 64, generator=g) * 3.0 + (3.0 - 88.8)
+    l[:, 9] = 3.0
+    ids, w = _from_logits(B, l.to(dev), None, 20, rule)
+    rid, rw = orc.route_logits(l.numpy(), None, 20, **_rule(rule)[0])
+    assert np.array_equal(ids, rid)
+    assert (np.abs(w - rw) <= 2.0 ** -23 * rw + 2.0 ** -149).all()
+
+
+@pytest.mark.parametrize("M", [200, 1300])
+def test_softmax_groups_far_below_the_top_from_hidden_states(B, dev, M):
+    """The first values of x raise expert 9's logit to about 87 above the others' at M from fp64
+    sums and from bounded ones."""
+    rule = dict(softmax=True, n_group=8, topk_group=3, group_top=2)
+    g = torch.Generator(device=dev).manual_seed(M)
+    x = torch.randn(M, 264, generator=g, device=dev)
+    x[:, :8] = 1.0
+    wr = torch.randn(64, 264, generator=g, device=dev) * (0.7 / 16)
+    wr[:, :8] = 0.0
+    wr[9, :8] = 87.0 / 8
+    x, wr = x.bfloat16(), wr.bfloat16()
+    ids, _ = _from_hidden(B, x, wr, None, 20, rule)
+    rid, _ = orc.route(bits(x), bits(wr), None, 20, **_rule(rule)[0])
+    assert np.array_equal(ids, rid)
