@@ -855,10 +855,9 @@ __device__ __forceinline__ Fast rank_fast(const double (&l)[SL], const double (&
       if (__any(redo != 0)) return kRedo;
     }
   }
-  const double factor = divisor > 0.0 ? (double)rule.scale / divisor : 0.0;
-  if (picked) {
+  if (picked) {   // (1 / divisor may be past the largest number where score / divisor is not)
     ids[t * top_k + rank] = mine.id;
-    weights[t * top_k + rank] = (float)(score * factor);
+    weights[t * top_k + rank] = divisor > 0.0 ? (float)(score / divisor * (double)rule.scale) : 0.0f;
   }
   return kDone;
 }
@@ -1096,16 +1095,15 @@ __device__ __forceinline__ Fast select_fp64(const double (&l)[SL], const double 
     wave_lds_fence();
     if (__any(redo != 0)) return kRedo;
   }
-  double factor = (double)rule.scale / divisor;
   if (rule.renorm) {
     double total = 0.0;
     for (int r = lane; r < top_k; r += kWave) total += s_pick[r];
-    total = wave_sum(total);
-    factor = total > 0.0 ? (double)rule.scale / total : 0.0;
+    divisor = wave_sum(total);
   }
   for (int r = lane; r < top_k; r += kWave) {
     ids[t * top_k + r] = s_id[r];
-    weights[t * top_k + r] = s_pick[r] > 0.0 ? (float)(s_pick[r] * factor) : 0.0f;
+    weights[t * top_k + r] =
+        s_pick[r] > 0.0 ? (float)(s_pick[r] / divisor * (double)rule.scale) : 0.0f;
   }
   return kDone;
 }

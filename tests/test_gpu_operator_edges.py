@@ -185,3 +185,30 @@ def test_softmax_groups_far_below_the_top_from_hidden_states(B, dev, M):
     ids, _ = _from_hidden(B, x, wr, None, 20, rule)
     rid, _ = orc.route(bits(x), bits(wr), None, 20, **_rule(rule)[0])
     assert np.array_equal(ids, rid)
+
+
+@pytest.mark.parametrize("E,masked", [(8, 0), (96, 0), (96, 90), (512, 0)])
+@pytest.mark.parametrize("scale", [1.0, 2.5, -3.0])
+def test_weights_of_scores_next_to_zero(B, dev, E, masked, scale):
+    """Scores of e^-709 to e^-716 are numbers in 64 bits, but 1 over their sum is none: sigmoid
+    scores, and softmax scores of picks that a bias prefers to the token's best expert."""
+    g = torch.Generator().manual_seed(E)
+    k = min(E - masked, 4)
+    l = torch.full((50, E), -float("inf"))
+    l[:, masked:] = torch.rand(50, E - masked, generator=g) * 0.5 - 709.4
+    rule = dict(scale=scale)
+    for kk in {1, k, k + (1 if masked else 0)}:
+        ids, w = _from_logits(B, l.to(dev), None, kk, rule)
+        rid, rw = orc.route_logits(l.numpy(), None, kk, **_rule(rule)[0])
+        assert np.array_equal(ids, rid)
+        assert (np.abs(w - rw) <= 2.0 ** -23 * np.abs(rw)).all()
+    l[:, masked:] = torch.rand(50, E - masked, generator=g) * 5.0 - 716.0
+    l[:, E - 1] = 0.0
+    bias = torch.zeros(E)
+    bias[E - 1] = -2.0
+    bias[:E - 1] = torch.rand(E - 1, generator=g)
+    rule = dict(softmax=True, scale=scale)
+    ids, w = _from_logits(B, l.to(dev), bias.to(dev), k - 1, rule)
+    rid, rw = orc.route_logits(l.numpy(), bias.numpy(), k - 1, **_rule(rule)[0])
+    assert np.array_equal(ids, rid)
+    assert (np.abs(w - rw) <= 2.0 ** -23 * np.abs(rw)).all()
