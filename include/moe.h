@@ -440,9 +440,9 @@ int moe_route_logits(const float* logits, int64_t ld, const float* select_bias,
  *   finite.  Weights [N, K] quantized so have a scale per output channel, tokens [M, K] one
  *   per token.  K % 16 == 0, 16 <= K <= 131072; v and codes 16-byte, scales 4-byte aligned.
  * moe_i8_matmul: out[m, n] = a_scales[m] * w_scales[n] * sum_k a[m, k] * w[n, k] for a [M, K]
- *   and w [N, K] int8 (K as above); the sums are exact (int32), the scaling fp32: the scales'
- *   product, to be a normal number or 0, times the sum.  out [M, N]
- *   is bf16, or fp32 with out_f32 = 1.  0 <= M <= 2^30, 1 <= N <= 2^26.  a, w, w_scales and out
+ *   and w [N, K] int8 (any codes, K as above); the sums are exact (int32), the scaling fp32:
+ *   the scales' product, to be a normal number or 0, times the sum.  out [M, N] is bf16, or
+ *   fp32 with out_f32 = 1.  0 <= M <= 2^30, 1 <= N <= 2^26.  a, w, w_scales and out
  *   16-byte, a_scales 4-byte aligned.  The workspace holds moe_i8_matmul_workspace_bytes
  *   bytes, 256-byte aligned (it may be NULL where that is 0); its contents are not kept.
  */

@@ -1,5 +1,5 @@
 // int8 matrix products on MFMA (v_mfma_i32_16x16x64_i8): sums in int32, exact for
-// K <= 131,072 (127^2 K < 2^31), scaled once at the end in fp32 by the scale of the token
+// K <= 131,072 (mend_wrapped), scaled once at the end in fp32 by the scale of the token
 // row and the scale of the weight row (output channel).
 //
 // Workgroup tile: BM token rows x 64 WN weight rows, K in chunks of 128 values (one
@@ -29,6 +29,18 @@ typedef __attribute__((ext_vector_type(4))) int i32x4;
 __device__ __forceinline__ i32x4 mfma_i8(u32x4 a, u32x4 b, i32x4 c) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a),
                                                __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+}
+
+// Sums of K <= 131,072 products of any two int8 codes in int32.  They reach from -128 * 127 K
+// > -2^31 to 128^2 K <= 2^31: only that last one, at K = kWrapK, wraps, to a value that no other
+// sum has.  (A test of K, not one of every sum: 253 against 256 us at 8192 x 4096 x 7168.)
+constexpr int kWrapK = 131072;
+template <int N>
+__device__ __forceinline__ void mend_wrapped(int K, const i32x4 (&sum)[N], float (&v)[4 * N]) {
+  if (K != kWrapK) return;
+#pragma unroll
+  for (int q = 0; q < 4 * N; ++q)
+    if (sum[q >> 2][q & 3] == INT32_MIN) v[q] = 0x1p31f;
 }
 
 constexpr int kKC = 128;   // K values per chunk
@@ -322,7 +334,10 @@ __global__ __launch_bounds__(64 * WN * WM) void i8_gemm_kernel(I8Args p) {
           for (int q = 0; q < 16; ++q) w[q] = ws[min(n0 + q, p.ncols - 1)];
         }
 #pragma unroll
-        for (int q = 0; q < 16; ++q) v[q] = (float)v4[q >> 2][q & 3] * (xs * w[q]);
+        for (int q = 0; q < 16; ++q) v[q] = (float)v4[q >> 2][q & 3];
+        if (MODE == kDense) mend_wrapped(K, v4, v);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) v[q] *= xs * w[q];
         if (MODE == kDense) {
           store_dense<F32>(p, (size_t)row * p.ncols, n0, v);
         } else {
@@ -592,9 +607,13 @@ __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char*
       for (int s = 0; s < MTW; ++s) {
         const int r = 16 * (2 * s + wm) + li;
         if (r >= it.nlive) continue;
+        const i32x4 v4[4] = {acc[0][s], acc[1][s], acc[2][s], acc[3][s]};
         float v[16];
 #pragma unroll
-        for (int q = 0; q < 16; ++q) v[q] = (float)acc[q >> 2][s][q & 3] * (xs[s] * w[q]);
+        for (int q = 0; q < 16; ++q) v[q] = (float)v4[q >> 2][q & 3];
+        if (MODE == kDense) mend_wrapped(K, v4, v);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) v[q] *= xs[s] * w[q];
         if (MODE == kDense) {
           store_dense<F32>(p, (size_t)(it.start + r) * p.ncols, n0, v);
           continue;
@@ -751,10 +770,12 @@ __global__ __launch_bounds__(512) void i8_skinny_kernel(I8Args p, int mblocks, i
   for (int i = threadIdx.x; i < 256 * MT; i += 64 * WAVES) {
     const int r = i >> 4, c = i & 15;
     if (m0 + r >= p.M || n0 + c >= p.ncols) continue;
-    int sum = 0;
+    uint32_t sum = 0;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) sum += part[w][r >> 4][c & 3][16 * (c >> 2) + (r & 15)];
-    const float v = (float)sum * (p.tok_scale[m0 + r] * p.w_scale[n0 + c]);
+    for (int w = 0; w < WAVES; ++w)
+      sum += (uint32_t)part[w][r >> 4][c & 3][16 * (c >> 2) + (r & 15)];
+    const float all = K == kWrapK && (int)sum == INT32_MIN ? 0x1p31f : (float)(int)sum;
+    const float v = all * (p.tok_scale[m0 + r] * p.w_scale[n0 + c]);
     const size_t o = (size_t)(m0 + r) * p.ncols + n0 + c;
     if (F32) static_cast<float*>(p.out)[o] = v;
     else static_cast<uint16_t*>(p.out)[o] = (uint16_t)f32_to_bf16_rne(v);

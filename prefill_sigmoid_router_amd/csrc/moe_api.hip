@@ -683,7 +683,7 @@ namespace {
 
 constexpr int kMaxGroups = 64;
 constexpr int kMaxRouteTokens = 1 << 24;   // a wave per token: 2^30 threads
-constexpr int kMaxI8K = 131072;   // 127^2 * kMaxI8K < 2^31: int32 sums are exact
+constexpr int kMaxI8K = 131072;   // 128^2 * kMaxI8K = 2^31: int32 sums are exact
 constexpr int kMaxI8Rows = 1 << 30, kMaxI8Columns = 1 << 26;   // a tile's end fits in 32 bits
 
 bool make_rule(int32_t E, int32_t top_k, int32_t score, int32_t n_group, int32_t topk_group,

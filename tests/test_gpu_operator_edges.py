@@ -212,3 +212,28 @@ def test_weights_of_scores_next_to_zero(B, dev, E, masked, scale):
     rid, rw = orc.route_logits(l.numpy(), bias.numpy(), k - 1, **_rule(rule)[0])
     assert np.array_equal(ids, rid)
     assert (np.abs(w - rw) <= 2.0 ** -23 * np.abs(rw)).all()
+
+
+# ---------------------------------------------------------------------------------------
+# Products
+# ---------------------------------------------------------------------------------------
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("M,N", [(3, 40), (20, 40), (70, 300), (300, 300), (2112, 1024)])
+def test_matmul_sums_of_the_lowest_codes(B, dev, M, N, f32):
+    """Rows of one code each, -128 among them, at the largest K: 128^2 K is 2^31.  (2112 x 1024
+    takes the step stream.)  Roundings as in the other products: three of 2^-24, and the result's."""
+    K = 131072
+    av = (torch.arange(M, device=dev) % 3 - 1) * 127 - (torch.arange(M, device=dev) % 3 == 0).long()
+    wv = (torch.arange(N, device=dev) % 5 - 2) * 63
+    wv[::2] = -128
+    wv[1::4] = 127
+    a = av.to(torch.int8)[:, None].expand(M, K).contiguous()
+    w = wv.to(torch.int8)[:, None].expand(N, K).contiguous()
+    sa, sw = torch.rand(M, device=dev) + 0.5, torch.rand(N, device=dev) * 1e-4 + 1e-4
+    out = torch.full((M, N), float("nan"), dtype=torch.float32 if f32 else torch.bfloat16, device=dev)
+    B.moe_i8_matmul(a, sa, w, sw, out)
+    torch.cuda.synchronize()
+    want = av.double()[:, None] * wv.double()[None, :] * K * sa.double()[:, None] * sw.double()[None, :]
+    assert (want > 2.0 ** 31 * 0.5e-4).any()
+    tol = (3.01 * 2.0 ** -24 + (0 if f32 else 2.0 ** -8)) * want.abs()
+    assert ((out.double() - want).abs() <= tol).all()
