@@ -402,6 +402,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const int8_t* base) 
   return __builtin_amdgcn_make_buffer_rsrc((void*)((uint64_t)hi << 32 | lo), 0, -1, 0x00020000);
 }
 
+// Vector memory operations stay on their side of it; the mask lets everything else (ALU, MFMA,
+// LDS reads and writes) pass.
+__device__ __forceinline__ void keep_memory_order() { __builtin_amdgcn_sched_barrier(0x78f); }
+
 struct GroupedItem {
   int start, nlive, e, col0;
 };
@@ -490,6 +494,7 @@ __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char*
 #pragma unroll
     for (int i = 0; i < PW; ++i)
       dst[i] = __builtin_amdgcn_raw_buffer_load_b128(q.w, o[i], off, WPOL);
+    keep_memory_order();
   };
   auto put_w = [&](int stage, int c, const u32x4 (&v)[PW]) {   // v: chunk c
     unsigned char* base = lds + stage * R::WSTAGE + wave * PW * 1024 + lane * 16;
@@ -516,6 +521,7 @@ __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char*
 #pragma unroll
     for (int i = 0; i < TPW; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(q.t, (lds_void*)(base + i * 1024), 16, o[i], off, 0, 0);
+    keep_memory_order();
   };
   const int wrow = (UP ? 32 : 64) * wn + SPAN * (li >> 2) + (li & 3);
   const int woff16 = wrow * 128 + 16 * (lg ^ weight_swizzle<SPAN>(wrow));
@@ -568,7 +574,10 @@ __device__ __forceinline__ void grouped_products(const I8Args& p, unsigned char*
       else if (s + 1 < MTW && s >= active) break;
     }
   };
-  // the next step's tokens have to be in LDS: all but the copies issued after them
+  // The next step's tokens have to be in LDS: all but what was issued after them, which is the
+  // weights of their own step and the tokens and weights of the D - 1 steps that follow it.  A
+  // load issued before its step's copies would make this count too large, so keep_memory_order
+  // holds the order of the source.
   auto publish = [&] {
     wait_vmcnt<PW + (D - 1) * (TPW + PW)>();
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
