@@ -214,6 +214,71 @@ def test_weights_of_scores_next_to_zero(B, dev, E, masked, scale):
     assert (np.abs(w - rw) <= 2.0 ** -23 * np.abs(rw)).all()
 
 
+@pytest.mark.parametrize("rule", [dict(), dict(renormalize=False, scale=2.5), dict(softmax=True),
+                                  dict(softmax=True, renormalize=False),
+                                  dict(n_group=8, topk_group=4, group_top=2, scale=2.5),
+                                  dict(n_group=8, topk_group=3, softmax=True, renormalize=False)])
+@pytest.mark.parametrize("M,H,E,k", [(8, 7168, 256, 16), (300, 7168, 256, 16), (1300, 264, 64, 6), (170, 1032, 480, 8)])
+@pytest.mark.parametrize("biased", [False, True])
+def test_weights_of_logits_that_fp32_holds(B, dev, M, H, E, k, rule, biased):
+    """Whole numbers times 2^-7 whose sums stay below 2^24 of it: fp32 sums are exact in any
+    order, so the weights may be off by their own rounding only (2^-24, doubled for the 64-bit
+    arithmetic before it), from fp64 logits and from bounded ones.  Many logits tie."""
+    g = torch.Generator(device=dev).manual_seed(M + E)
+    n = lambda *s: torch.randint(-4, 5, s, generator=g, device=dev).float()  # noqa: E731
+    x, wr = n(M, H).bfloat16(), (n(E, H) * 2.0 ** -7).bfloat16()
+    bias = torch.randn(E, generator=g, device=dev) * 0.05 if biased else None
+    ids, w = _from_hidden(B, x, wr, bias, k, rule)
+    rid, rw = orc.route(bits(x), bits(wr), None if bias is None else bias.cpu().numpy(), k, **_rule(rule)[0])
+    assert np.array_equal(ids, rid)
+    assert (np.abs(w - rw) <= 2.0 ** -23 * np.abs(rw) + 2.0 ** -149).all()
+
+
+@pytest.mark.parametrize("M", [5, 300, 1300, 2600])
+@pytest.mark.parametrize("rule", [dict(), dict(softmax=True), dict(n_group=4, topk_group=2, group_top=2),
+                                  dict(n_group=4, topk_group=2, softmax=True, renormalize=False)])
+@pytest.mark.parametrize("biased", [False, True])
+def test_tokens_that_are_not_finite_stay_by_themselves(B, dev, M, rule, biased):
+    """The other tokens get what they get beside finite ones, bit by bit, and the exact ids (M * 32
+    logits: from 64-bit sums and, of 1,300 and 2,600 tokens, from bounded ones)."""
+    g = torch.Generator(device=dev).manual_seed(M)
+    x = torch.randn(M, 256, generator=g, device=dev).bfloat16()
+    wr = (torch.randn(32, 256, generator=g, device=dev) * (1.7 / 16)).bfloat16()
+    bias = torch.randn(32, generator=g, device=dev) * 0.05 if biased else None
+    ids, w = _from_hidden(B, x, wr, bias, 5, rule)
+    rid, _ = orc.route(bits(x), bits(wr), None if bias is None else bias.cpu().numpy(), 5, **_rule(rule)[0])
+    assert np.array_equal(ids, rid)
+    odd = [t for t in (1, 2, 3, 65, 66, 129, 1290) if t < M]
+    for i, t in enumerate(odd):
+        if i % 3 == 0:
+            x[t, 3] = float("nan")
+        elif i % 3 == 1:
+            x[t, :] = float("inf")
+        else:
+            x[t, 7] = -float("inf")
+    ids2, w2 = _from_hidden(B, x, wr, bias, 5, rule)
+    keep = np.setdiff1d(np.arange(M), odd)
+    assert np.array_equal(ids2[keep], ids[keep]) and np.array_equal(w2[keep], w[keep])
+    assert all(len(set(ids2[t])) == 5 and (0 <= ids2[t]).all() and (ids2[t] < 32).all() for t in odd)
+
+
+@pytest.mark.parametrize("M", [200, 1300])
+@pytest.mark.parametrize("power", [-130, -126, 100])
+def test_hidden_states_next_to_zero(B, dev, M, power):
+    """Subnormal bf16 values times large weights make ordinary logits; so do large ones.  From
+    bounded logits a weight is within 2^-9 of itself by its own logit and by its divisor's each."""
+    g = torch.Generator(device=dev).manual_seed(M)
+    x = (torch.randn(M, 264, generator=g, device=dev) * 2.0 ** power).bfloat16()
+    wr = ((torch.randn(64, 264, generator=g, device=dev) / 16).double() * 2.0 ** -power).bfloat16()
+    if power == -130:
+        wr = (torch.randn(64, 264, generator=g, device=dev) * 2.0 ** 124).bfloat16()
+    for rule in (dict(), dict(softmax=True), dict(n_group=4, topk_group=2)):
+        ids, w = _from_hidden(B, x, wr, None, 6, rule)
+        rid, rw = orc.route(bits(x), bits(wr), None, 6, **_rule(rule)[0])
+        assert np.array_equal(ids, rid)
+        assert (np.abs(w - rw) <= 2 * 2.0 ** -9 * np.abs(rw) * (1 + 2.0 ** -6)).all()
+
+
 # ---------------------------------------------------------------------------------------
 # Products
 # ---------------------------------------------------------------------------------------
@@ -237,3 +302,57 @@ def test_matmul_sums_of_the_lowest_codes(B, dev, M, N, f32):
     assert (want > 2.0 ** 31 * 0.5e-4).any()
     tol = (3.01 * 2.0 ** -24 + (0 if f32 else 2.0 ** -8)) * want.abs()
     assert ((out.double() - want).abs() <= tol).all()
+
+
+def _codes(M, N, K, dev, seed):
+    g = torch.Generator(device=dev).manual_seed(seed)
+    code = lambda *s: torch.randint(-128, 128, s, generator=g, device=dev, dtype=torch.int8)  # noqa: E731
+    return (code(M, K), torch.rand(M, generator=g, device=dev) + 0.01, code(N, K),
+            torch.rand(N, generator=g, device=dev) * 1e-4 + 1e-6)
+
+
+# step streams of 64, 128 and 256 token rows, whole last chunks of K and partial ones
+STREAMS = [(4100, 513, 640), (900, 4097, 2048), (3000, 2300, 1024), (5000, 1537, 2048), (3500, 2500, 768),
+           (2500, 1300, 656), (3000, 2300, 1040), (5000, 1537, 2064)]
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("M,N,K", STREAMS)
+def test_matmul_step_streams(B, dev, M, N, K, f32):
+    """Exact sums (in float64), three roundings of 2^-24 and the result's; nothing written
+    around the result."""
+    a, sa, w, sw = _codes(M, N, K, dev, M + K)
+    guard = 64
+    flat = torch.full((M * N + 2 * guard,), 77.0, dtype=torch.float32 if f32 else torch.bfloat16, device=dev)
+    out = flat[guard:guard + M * N].view(M, N)
+    B.moe_i8_matmul(a, sa, w, sw, out)
+    torch.cuda.synchronize()
+    want = (a.double() @ w.double().T.contiguous()) * sa.double()[:, None] * sw.double()[None, :]
+    tol = (3.01 * 2.0 ** -24 + (0 if f32 else 2.0 ** -8)) * want.abs()
+    assert ((out.double() - want).abs() <= tol).all()
+    assert (flat[:guard] == 77.0).all() and (flat[-guard:] == 77.0).all()
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("M,N,K", [(2500, 1300, 640), (3000, 2300, 1024), (3500, 2500, 768), (3000, 2300, 1040)])
+def test_matmul_step_streams_in_a_graph(B, dev, M, N, K, f32):
+    a, sa, w, sw = _codes(M, N, K, dev, 1)
+    out = torch.zeros(M, N, dtype=torch.float32 if f32 else torch.bfloat16, device=dev)
+    other = torch.empty_like(out)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        B.moe_i8_matmul(a, sa, w, sw, out)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.moe_i8_matmul(a, sa, w, sw, out)
+    for seed in range(4):
+        fresh = _codes(M, N, K, dev, 30 + seed)
+        a.copy_(fresh[0])
+        sa.copy_(fresh[1])
+        out.zero_()
+        B.moe_i8_matmul(fresh[0], fresh[1], w, sw, other)     # eager work between replays
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, other)
