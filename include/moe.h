@@ -443,8 +443,9 @@ int moe_route_logits(const float* logits, int64_t ld, const float* select_bias,
  *   and w [N, K] int8 (any codes, K as above); the sums are exact (int32), the scaling fp32:
  *   the scales' product, to be a normal number or 0, times the sum.  out [M, N] is bf16, or
  *   fp32 with out_f32 = 1.  0 <= M <= 2^30, 1 <= N <= 2^26.  a, w, w_scales and out
- *   16-byte, a_scales 4-byte aligned.  The workspace holds moe_i8_matmul_workspace_bytes
- *   bytes, 256-byte aligned (it may be NULL where that is 0); its contents are not kept.
+ *   16-byte, a_scales 4-byte aligned.  No kernel of today's needs a workspace:
+ *   moe_i8_matmul_workspace_bytes is 0 for every size, and workspace and workspace_bytes are
+ *   not looked at (NULL and 0 will do).
  */
 int moe_i8_quantize(const uint16_t* v, int64_t rows, int32_t K, int8_t* codes, float* scales,
                     moe_stream_t stream);

@@ -816,16 +816,11 @@ int moe_i8_quantize(const uint16_t* v, int64_t rows, int32_t K, int8_t* codes, f
   return hip_status(moe::launch_i8_rows(v, rows, K, codes, scales, (hipStream_t)stream));
 }
 
-size_t moe_i8_matmul_workspace_bytes(int32_t M, int32_t N, int32_t K) {
-  (void)M;
-  (void)N;
-  (void)K;
-  return 0;
-}
+size_t moe_i8_matmul_workspace_bytes(int32_t, int32_t, int32_t) { return 0; }
 
 int moe_i8_matmul(const int8_t* a, const float* a_scales, const int8_t* w, const float* w_scales,
-                  int32_t M, int32_t N, int32_t K, void* out, int32_t out_f32, void* workspace,
-                  size_t workspace_bytes, moe_stream_t stream) {
+                  int32_t M, int32_t N, int32_t K, void* out, int32_t out_f32, void*, size_t,
+                  moe_stream_t stream) {
   if (M < 0 || M > kMaxI8Rows || N < 1 || N > kMaxI8Columns || K < 16 || K % 16 != 0 ||
       K > kMaxI8K || (out_f32 != 0 && out_f32 != 1))
     return MOE_ERR_INVALID_ARG;
@@ -833,9 +828,6 @@ int moe_i8_matmul(const int8_t* a, const float* a_scales, const int8_t* w, const
   if (!a || !a_scales || !w || !w_scales || !out || !aligned(a, 16) || !aligned(a_scales, 4) ||
       !aligned(w, 16) || !aligned(w_scales, 16) || !aligned(out, 16))
     return MOE_ERR_INVALID_ARG;
-  const size_t need = moe_i8_matmul_workspace_bytes(M, N, K);
-  if (need > 0 && (!workspace || !aligned(workspace, kAlign) || workspace_bytes < need))
-    return MOE_ERR_WORKSPACE;
   return hip_status(moe::launch_i8_matmul(a, a_scales, w, w_scales, M, N, K, out, out_f32 == 1,
                                           (hipStream_t)stream));
 }
