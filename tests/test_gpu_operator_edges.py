@@ -356,3 +356,62 @@ def test_matmul_step_streams_in_a_graph(B, dev, M, N, K, f32):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, other)
+
+
+# ---------------------------------------------------------------------------------------
+# Offsets that pass 32 bits
+# ---------------------------------------------------------------------------------------
+def test_quantize_more_than_four_billion_values(B, dev):
+    K, part = 65536, 4097
+    v = torch.randn(part, K, generator=torch.Generator(device=dev).manual_seed(1), device=dev).bfloat16()
+    want = _quantize(B, v)
+    codes, scales = _quantize(B, v.repeat(17, 1))
+    for i in range(17):
+        at = slice(i * part, (i + 1) * part)
+        assert torch.equal(codes[at], want[0]) and torch.equal(scales[at], want[1])
+
+
+@pytest.mark.parametrize("M,N,K", [(70000, 256, 65536), (40, 70000, 65536), (70000, 65536, 64)])
+def test_matmul_past_32_bits(B, dev, M, N, K):
+    """More than 2^32 codes of tokens, of weights, and results: rows that repeat give the results
+    of the rows that they repeat."""
+    a, sa, w, sw = _codes(min(M, 7000), min(N, 7000), K, dev, 5)
+    want = (a.double() @ w.double().T.contiguous()) * sa.double()[:, None] * sw.double()[None, :]
+    ra, rw = -(-M // a.shape[0]), -(-N // w.shape[0])
+    big = (a.repeat(ra, 1)[:M].contiguous(), sa.repeat(ra)[:M].contiguous(), w.repeat(rw, 1)[:N].contiguous(),
+           sw.repeat(rw)[:N].contiguous())
+    out = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device=dev)
+    B.moe_i8_matmul(*big, out)
+    torch.cuda.synchronize()
+    tol = (3.01 * 2.0 ** -24 + 2.0 ** -8) * want.abs()
+    for m in range(0, M, a.shape[0]):
+        for n in range(0, N, w.shape[0]):
+            got = out[m:m + a.shape[0], n:n + w.shape[0]].double()
+            i, j = got.shape
+            assert ((got - want[:i, :j]).abs() <= tol[:i, :j]).all()
+
+
+def test_layer_next_to_its_most_values(B, dev):
+    """M * H just below 2^32, and more than that many bytes of everything between."""
+    part, times, H, E, I, k, block = 65535, 16, 4096, 4, 16, 1, 64
+    g = torch.Generator(device=dev).manual_seed(3)
+    n = lambda *s, std=1.0: torch.randn(*s, generator=g, device=dev) * std  # noqa: E731
+    x, wr = n(part, H).bfloat16(), n(E, H, std=1.7 / H ** 0.5).bfloat16()
+    w13, s13 = _quantize(B, n(E, 2 * I, H, std=1.0 / H ** 0.5).bfloat16())
+    w2, s2 = _quantize(B, n(E, H, I, std=1.0 / I ** 0.5).bfloat16())
+    one = torch.ones(H, dtype=torch.bfloat16, device=dev)
+
+    def run(x):
+        M = x.shape[0]
+        out, ids = torch.full_like(x, float("nan")), torch.full((M, k), -7, dtype=torch.int32, device=dev)
+        ws = torch.empty(B.moe_i8_workspace_bytes(M, H, E, I, k, block), dtype=torch.uint8, device=dev)
+        B.moe_forward_i8(x, wr, None, w13, s13, w2, s2, x, one, 1e-5, k, block, out, ws, topk_ids_out=ids)
+        torch.cuda.synchronize()
+        return out, ids
+
+    want, wids = run(x)
+    assert torch.isfinite(want.float()).all()
+    out, ids = run(x.repeat(times, 1))
+    for i in range(times):
+        at = slice(i * part, (i + 1) * part)
+        assert torch.equal(ids[at], wids) and torch.equal(out[at], want)
