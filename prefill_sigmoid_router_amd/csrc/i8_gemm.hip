@@ -100,7 +100,9 @@ __device__ __forceinline__ void store16(uint16_t* dst, const float (&v)[16]) {
   }
 }
 
-__device__ __forceinline__ float silu_fast(float z) {   // both steps within 2 units in the last place
+// __expf is exp2 of a rounded product: within about (1.5 |z| + 2) 2^-24 of itself; the reciprocal
+// within 2^-23.
+__device__ __forceinline__ float silu_fast(float z) {
   return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
 }
 
@@ -376,10 +378,13 @@ hipError_t launch(I8Args& a, long token_tiles, hipStream_t s) {
 // step ahead, whose L2 latency then set the pace).  Without the stream each item paid about
 // 12 us of latencies: item data, first chunks, scales (M=2048, H=7168, I=2048, E=256, 29
 // items a workgroup in the down product).
-// Measured: dense 8192 x 4096 x 7168 220 to 227 us (2.1 POP/s, MFMAs busy half the cycles: a
-// step's fragment reads and its barrier stand beside them); the layer at M=8 455 + 225 us (6.7
-// TB/s of weights), at M=2048 1,590 + 945 us (7.5 and 3.8 GB of weights, with the tokens' lines
-// from the L2 and 134 MB of act or 0.53 GB of results at the same time).
+// Measured: dense 8192 x 4096 x 7168 215 to 220 us (2.2 POP/s, MFMAs busy half the cycles: a
+// step's fragment reads and its barrier stand beside them), 224 with a partial last chunk (K =
+// 7152); the layer at M=8 450 + 232 us (6.7 TB/s of weights), at M=2048 1,640 + 1,020 us (7.5 and
+// 3.8 GB of weights, 8.2 and 4.1 read in all, with the tokens' lines from the L2 and 0.29 GB of act
+// or 0.94 GB of results written at the same time; MFMAs busy 28 and 24 %).
+// The 256-row up kernels spill 3 registers a lane, and 17 with a partial last chunk: reloads that
+// wait for all copies in flight, once an item.
 template <int ROWS_, int D_>
 struct Ring {
   static constexpr int ROWS = ROWS_, D = D_;
@@ -810,6 +815,10 @@ hipError_t launch_skinny(I8Args& a, hipStream_t s) {
 //     (M=256: 28 us against 41; M=512: 36 against 49; M=1024: 69 against 54)
 //   step streams of 64, 128, 256 tokens x 256 weight rows: 0.88, 1.33, 2.09 per 256
 //     (M=1024: 54, 61, 88 us; M=2048: 98, 74, 92; M=3500: 178, 136, 117)
+// At 63 sizes (M 64 to 8192; N x K 4096 x 7168, 4096 x 2048, 1024 x 7168, 1024 x 2048, 7168 x
+// 2048, 2048 x 640, 8192 x 1024, 4096 x 512, 4096 x 256) the pick is the fastest or within 8 % of
+// it in 58, within 15 % in four (M=2048, N=4096, K=7168 72 us against 62.5 for 128 tokens), and
+// 27 % slower in one (M=512, N=8192, K=1024: 19.4 us against 15.2 for 64 x 64 tiles).
 template <bool F32>
 hipError_t launch_dense(I8Args& a, hipStream_t s) {
   if (a.M <= 16) return launch_skinny<1, F32>(a, s);

@@ -750,8 +750,8 @@ bool i8_grids_ok(int32_t M, int32_t H, int32_t E, int32_t top_k, int32_t block) 
 
 // Token-tile height of the grouped int8 GEMMs, by the tokens that an expert can expect: the
 // lowest that takes them at once, mostly (layer at H=2048, I=1408, E=60, k=4 with 64 / 128 / 256
-// rows, us: 24 tokens 154 / 159 / 159, 40 172 / 172 / 177, 64 205 / 179 / 182, 96 256 / 203 /
-// 204, 128 306 / 258 / 228, 256 481 / 393 / 345).
+// rows, us: 24 tokens 154 / 156 / 157, 40 171 / 173 / 173, 64 204 / 179 / 180, 96 255 / 201 /
+// 201, 128 301 / 258 / 225, 256 490 / 409 / 361).
 int i8_tile_rows(int32_t M, int32_t E, int32_t top_k) {
   const int64_t per_expert = (int64_t)M * top_k / E;
   return per_expert < 32 ? kI8MinTileRows : per_expert < 96 ? 128 : 256;

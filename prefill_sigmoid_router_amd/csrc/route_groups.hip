@@ -1293,9 +1293,10 @@ size_t route_groups_scratch_bytes(int M, int E) {
 // From this many logits on bounded fp32 MFMA sums replace fp64 ones for every (token, expert).
 // Measured at H=7168, bounded against fp64, us: E=256 M=64 25 / 22, M=128 29 / 32, M=255 31 /
 // 54; E=512 M=64 41 / 35, M=128 41 / 57; E=64 M=255 21 / 19.  Softmax scores with a bias, with
-// the listed tokens' two launches: E=512 M=255 66 / 94, M=128 58 / 52, M=4096 145 / 1,322.  Not
-// for few experts (a tile of 64 stays mostly empty), more than 512 (registers), or a pick of
-// nearly all, which leaves most choices open.
+// the listed tokens' two launches: E=512 M=255 66 / 94, M=128 58 / 52, M=4096, k=8 154 / 1,322
+// (k=16 205).  Not for few experts (a tile of 64 stays mostly empty), more than 512 (the selection
+// spills 66 registers a lane from 257 on, and 16 slots a lane would spill twice as many), or a pick
+// of nearly all, which leaves most choices open.
 constexpr int kBoundedMinLogits = 40000, kBoundedMinExperts = 32, kBoundedMaxExperts = 512;
 
 hipError_t launch_route_groups(const uint16_t* x, const uint16_t* wr, const float* bias, int M,
