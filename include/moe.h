@@ -481,6 +481,87 @@ int moe_forward_i8(const uint16_t* x, const uint16_t* router_w, const float* sel
                    void* workspace, size_t workspace_bytes,
                    const moe_event_t* stage_events, moe_stream_t stream);
 
+/*
+ * The norms around a block, in one pass:
+ *   u   = N_post(y), or y                                        (the norm after the block)
+ *   z   = residual_scale * residual + block_scale * gate * u     (the residual stream)
+ *   out = N_pre(z), or z                                         (the norm before the next block)
+ * post and pre choose N: MOE_NORM_NONE; MOE_NORM_RMS, v * (mean v^2 + eps)^-1/2 * (offset + w) + b;
+ * MOE_NORM_LAYER, the same of v - mean v.  offset is weight_offset (1 for weights stored around 0);
+ * w and b are bf16 [H] or NULL (w NULL: no factor, no offset).  Everything is fp32 between the
+ * loads and the stores (out comes from the unrounded z); a row's squares have to have an fp32 sum.
+ *   y            [M, H] bf16, or fp32 with y_f32 = 1; NULL: no block (post MOE_NORM_NONE, no gate)
+ *   residual     [M, H] bf16, or fp32 with residual_f32 = 1; NULL: none
+ *   gate         bf16 or NULL: gate_cols = H, a value for each channel (gate_ld = 0: of all tokens,
+ *                else row t at gate + t * gate_ld), or gate_cols = 1, one value for each token
+ *                (token t's at gate + t * gate_ld)
+ *   z_out        [M, H] of residual_f32's type, or NULL
+ *   out          [M, H] bf16, or NULL (not both NULL)
+ * Row t of a tensor starts at t * its ld (in values): at least H, a multiple of 8 (gate_cols = 1:
+ * any ld).  z_out may be residual and out may be y, with the same ld and type; tensors overlap in
+ * no other way.  8 <= H <= 16384, H % 8 == 0, 0 <= M <= 2^30.
+ */
+enum { MOE_NORM_NONE = 0, MOE_NORM_RMS = 1, MOE_NORM_LAYER = 2 };
+int moe_block_norm(const void* y, int32_t y_f32, int64_t y_ld,
+                   const void* residual, int32_t residual_f32, int64_t residual_ld,
+                   const uint16_t* gate, int32_t gate_cols, int64_t gate_ld,
+                   int32_t post, const uint16_t* post_w, const uint16_t* post_b,
+                   int32_t pre, const uint16_t* pre_w, const uint16_t* pre_b,
+                   float eps, float weight_offset, float residual_scale, float block_scale,
+                   int32_t M, int32_t H, void* z_out, int64_t z_ld, uint16_t* out, int64_t out_ld,
+                   moe_stream_t stream);
+
+/*
+ * Dense bf16 product with an epilogue (a shared expert, a dense FFN, a projection):
+ *   h = x . w^T + bias;  out = act(h) + residual             (gated = 0, w [N, K])
+ *   out[:, n] = act(h[:, n]) * h[:, N + n] + residual[:, n]  (gated = 1, w [2N, K], the gate rows
+ *                                                             first, as W13 of an expert)
+ * MOE_ACT_GELU is h Phi(h), MOE_ACT_GELU_TANH its form with tanh.  Sums and epilogue are fp32; the
+ * result is rounded once.
+ *   x        [M, K] bf16, row t at x + t * x_ld (x_ld >= K, a multiple of 8)
+ *   bias     bf16 [N] ([2N] gated) or NULL
+ *   residual [M, N] bf16, or fp32 with residual_f32 = 1, or NULL; row t at t * residual_ld
+ *   out      [M, N] bf16, or fp32 with out_f32 = 1; row t at t * out_ld.  Any ld >= N.
+ * out may be residual, with the same ld and type; tensors overlap in no other way.  Columns go
+ * 16 bytes at a time where N, out_ld and residual_ld are multiples of 8, else one by one.
+ * K % 8 == 0, 8 <= K <= 2^20, 1 <= N <= 2^24, 0 <= M <= 2^24, M * N below 2^38 (larger:
+ * MOE_ERR_UNSUPPORTED).  workspace of moe_matmul_workspace_bytes bytes (0 for many sizes, then it
+ * may be NULL, and for invalid ones), 16-byte aligned.
+ */
+enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3, MOE_ACT_GELU_TANH = 4 };
+size_t moe_matmul_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t gated);
+int moe_matmul(const uint16_t* x, int64_t x_ld, const uint16_t* w, const uint16_t* bias,
+               int32_t M, int32_t N, int32_t K, int32_t act, int32_t gated,
+               const void* residual, int32_t residual_f32, int64_t residual_ld,
+               void* out, int32_t out_f32, int64_t out_ld,
+               void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/*
+ * The layer for a few tokens in two kernels: the steps of moe_forward on at most
+ * MOE_FEW_MAX_TOKENS tokens and MOE_FEW_MAX_PICKS picks M * top_k (more: MOE_ERR_UNSUPPORTED),
+ * without a plan.  The router is that of moe_route_groups on logits with an additive bias,
+ * x . Wr + router_bias (fp64 sums; router_bias fp32 [E] or NULL): sigmoid scores, one group,
+ * renormalize = 1, scale = 1 and no select_bias give moe_forward's picks and weights.  act and the
+ * picks' rows stay in fp32, so results differ from moe_forward's by its roundings.
+ *   residual     may be NULL (nothing is added)
+ *   out          may be NULL if residual_out is not (norm_w and eps are not looked at then)
+ * Any I % 16 == 0 up to 32768 (larger: MOE_ERR_UNSUPPORTED).  workspace of
+ * moe_few_workspace_bytes bytes (0 for sizes that are refused), 256-byte aligned; it needs no
+ * clearing.  Results do not depend on the number of CUs or on the order of events.
+ */
+#define MOE_FEW_MAX_TOKENS 16
+#define MOE_FEW_MAX_PICKS 512
+size_t moe_few_workspace_bytes(int32_t M, int32_t H, int32_t E, int32_t I, int32_t top_k);
+int moe_forward_few(const uint16_t* x, const uint16_t* router_w, const float* router_bias,
+                    const float* select_bias, const uint16_t* w13, const uint16_t* w2,
+                    const uint16_t* residual, const uint16_t* norm_w, float eps,
+                    int32_t M, int32_t H, int32_t E, int32_t I, int32_t top_k,
+                    int32_t score, int32_t n_group, int32_t topk_group, int32_t group_top,
+                    int32_t renormalize, float scale,
+                    uint16_t* out, uint16_t* residual_out,
+                    int32_t* topk_ids_out, float* topk_w_out,
+                    void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -27,6 +27,10 @@ __all__ = [
     "moe_route_groups_workspace_bytes", "moe_route_groups", "moe_route_logits",
     "SCORE_SIGMOID", "SCORE_SOFTMAX", "moe_i8_quantize", "moe_i8_matmul_workspace_bytes",
     "moe_i8_matmul", "moe_i8_workspace_bytes", "moe_forward_i8",
+    "moe_block_norm", "NORM_NONE", "NORM_RMS", "NORM_LAYER",
+    "moe_matmul_workspace_bytes", "moe_matmul", "ACT_NONE", "ACT_RELU", "ACT_SILU", "ACT_GELU",
+    "ACT_GELU_TANH", "moe_few_workspace_bytes", "moe_forward_few", "FEW_MAX_TOKENS",
+    "FEW_MAX_PICKS",
     "HipEvent",
 ]
 
@@ -37,6 +41,7 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP
 
 _p = ctypes.c_void_p
 _i32 = ctypes.c_int32
+_i64 = ctypes.c_int64
 _sz = ctypes.c_size_t
 
 # name -> (restype, argtypes); the C prototypes of include/moe.h
@@ -106,6 +111,18 @@ _PROTOS = {
                                       _i32, _i32, _i32, _i32, _i32, _i32,
                                       _i32, _i32, _i32, _i32, _i32, ctypes.c_float,
                                       _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p, _p]),
+    "moe_block_norm": (ctypes.c_int, [_p, _i32, _i64, _p, _i32, _i64, _p, _i32, _i64,
+                                      _i32, _p, _p, _i32, _p, _p,
+                                      ctypes.c_float, ctypes.c_float, ctypes.c_float,
+                                      ctypes.c_float, _i32, _i32, _p, _i64, _p, _i64, _p]),
+    "moe_matmul_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32]),
+    "moe_matmul": (ctypes.c_int, [_p, _i64, _p, _p, _i32, _i32, _i32, _i32, _i32,
+                                  _p, _i32, _i64, _p, _i32, _i64, _p, _sz, _p]),
+    "moe_few_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32]),
+    "moe_forward_few": (ctypes.c_int, [_p, _p, _p, _p, _p, _p, _p, _p, ctypes.c_float,
+                                       _i32, _i32, _i32, _i32, _i32,
+                                       _i32, _i32, _i32, _i32, _i32, ctypes.c_float,
+                                       _p, _p, _p, _p, _p, _sz, _p]),
 }
 EXPORTED_SYMBOLS = tuple(_PROTOS)
 
@@ -864,6 +881,140 @@ def moe_forward_i8(x, router_w, select_bias, w13_codes, w13_scales, w2_codes, w2
         _opt_arg(dev, block_expert_out, "block_expert_out", torch.int32),
         _opt_arg(dev, num_padded_out, "num_padded_out", torch.int32),
         _arg(dev, workspace, "workspace", torch.uint8), workspace.numel(), ev,
+        _stream_on(dev, stream)))
+
+
+# ---------------------------------------------------------------------------------------
+# Around and inside a block: norms, dense products, the layer for a few tokens
+# ---------------------------------------------------------------------------------------
+NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2                                       # MOE_NORM_*
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2, 3, 4           # MOE_ACT_*
+FEW_MAX_TOKENS, FEW_MAX_PICKS = 16, 512                                         # MOE_FEW_MAX_*
+
+
+def _rows_arg(device: int, t, name: str, dtypes, shape):
+    """Address and row stride of a matrix on the current device whose rows may lie apart (a
+    slice of the columns of a wider tensor); 0, 0 for None."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device (GPU) tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the current device (cuda:{device}), where the library "
+                         f"launches, got one on {t.device}")
+    M, n = shape
+    ld, step = t.stride()
+    if (n > 1 and step != 1) or (M > 1 and ld < n):
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return t.data_ptr(), ld if M > 1 else (n + 7) // 8 * 8
+
+
+_BF16, _ANY_FLOAT = (torch.bfloat16,), (torch.bfloat16, torch.float32)
+
+
+def _is_f32(t) -> int:
+    return 1 if t is not None and t.dtype is torch.float32 else 0
+
+
+def moe_block_norm(y, residual, out, z_out=None, gate=None, post: int = NORM_NONE, post_w=None,
+                   post_b=None, pre: int = NORM_RMS, pre_w=None, pre_b=None, eps: float = 1e-5,
+                   weight_offset: float = 0.0, residual_scale: float = 1.0,
+                   block_scale: float = 1.0, stream=None):
+    """z_out = residual_scale * residual + block_scale * gate * N_post(y); out = N_pre(z).
+
+    y, residual [M, H] bf16 or fp32 (either may be None), z_out of residual's type (y's without
+    a residual), out bf16 (one of the two may be None); gate bf16 [H], [M, H] or [M, 1]
+    (one row serves all tokens)."""
+    some = y if y is not None else residual
+    if some is None:
+        raise ValueError("y or residual has to be given")
+    dev = _device_of(some, "y" if y is not None else "residual")
+    M, H = some.shape
+    rtype = (residual if residual is not None else y).dtype
+    y_at, y_ld = _rows_arg(dev, y, "y", _ANY_FLOAT, (M, H))
+    r_at, r_ld = _rows_arg(dev, residual, "residual", _ANY_FLOAT, (M, H))
+    z_at, z_ld = _rows_arg(dev, z_out, "z_out", (rtype,), (M, H))
+    o_at, o_ld = _rows_arg(dev, out, "out", _BF16, (M, H))
+    g_at, g_ld, g_cols = None, 0, 0
+    if gate is not None:
+        if not isinstance(gate, torch.Tensor) or gate.dtype is not torch.bfloat16:
+            raise TypeError("gate must be a bfloat16 tensor")
+        rows = gate.view(1, H) if gate.shape == (H,) else gate
+        if rows.dim() != 2 or rows.shape[0] not in (1, M) or rows.shape[1] not in (1, H):
+            raise ValueError(f"gate must have shape ({H},), ({M} or 1, {H}) or ({M} or 1, 1), got "
+                             f"{tuple(gate.shape)}")
+        g_cols = rows.shape[1]
+        g_at, g_ld = _rows_arg(dev, rows, "gate", _BF16, tuple(rows.shape))
+        if rows.shape[0] == 1:
+            g_ld = 0
+    vec = lambda t, name: _opt_arg(dev, t, name, torch.bfloat16, (H,))  # noqa: E731
+    _check("moe_block_norm", load_library().moe_block_norm(
+        y_at, _is_f32(y), y_ld, r_at, 1 if rtype is torch.float32 else 0, r_ld, g_at, g_cols, g_ld,
+        post, vec(post_w, "post_w"), vec(post_b, "post_b"), pre, vec(pre_w, "pre_w"),
+        vec(pre_b, "pre_b"), float(eps), float(weight_offset), float(residual_scale),
+        float(block_scale), M, H, z_at, z_ld, o_at, o_ld, _stream_on(dev, stream)))
+
+
+def moe_matmul_workspace_bytes(M: int, N: int, K: int, gated: bool = False) -> int:
+    return int(load_library().moe_matmul_workspace_bytes(M, N, K, 1 if gated else 0))
+
+
+def moe_matmul(x, w, out, bias=None, act: int = ACT_NONE, gated: bool = False, residual=None,
+               workspace=None, stream=None):
+    """out [M, N] (bf16 or fp32) = act(x [M, K] w^T + bias) + residual, w [N, K]; gated: w [2N, K],
+    act of the first N columns times the others.  Rows of x, residual and out may lie apart."""
+    dev = _device_of(x, "x")
+    M, K = x.shape
+    rows = w.shape[0]
+    N = rows // 2 if gated else rows
+    x_at, x_ld = _rows_arg(dev, x, "x", _BF16, (M, K))
+    r_at, r_ld = _rows_arg(dev, residual, "residual", _ANY_FLOAT, (M, N))
+    o_at, o_ld = _rows_arg(dev, out, "out", _ANY_FLOAT, (M, N))
+    _check("moe_matmul", load_library().moe_matmul(
+        x_at, x_ld, _arg(dev, w, "w", torch.bfloat16, (2 * N if gated else N, K)),
+        _opt_arg(dev, bias, "bias", torch.bfloat16, (rows,)), M, N, K, act, 1 if gated else 0,
+        r_at, _is_f32(residual), r_ld, o_at, _is_f32(out), o_ld,
+        _opt_arg(dev, workspace, "workspace", torch.uint8),
+        0 if workspace is None else workspace.numel(), _stream_on(dev, stream)))
+
+
+def moe_few_workspace_bytes(M: int, H: int, E: int, I: int, top_k: int) -> int:
+    return int(load_library().moe_few_workspace_bytes(M, H, E, I, top_k))
+
+
+def moe_forward_few(x, router_w, router_bias, w13, w2, residual, norm_w, eps: float, top_k: int,
+                    out, workspace, residual_out=None, topk_ids_out=None, topk_w_out=None,
+                    select_bias=None, score: int = SCORE_SIGMOID, n_group: int = 1,
+                    topk_group: int = 1, group_top: int = 1, renormalize: bool = True,
+                    scale: float = 1.0, stream=None):
+    """The layer for at most FEW_MAX_TOKENS tokens in two kernels.  router_bias is added to the
+    logits (as moe_forward's), select_bias to the scores for the selection only; residual may be
+    None, and so may out with norm_w if residual_out is given."""
+    M, H = x.shape
+    E, two_i, _ = w13.shape
+    I = two_i // 2
+    dev = _device_of(x, "x")
+    _check("moe_forward_few", load_library().moe_forward_few(
+        _arg(dev, x, "x", torch.bfloat16),
+        _arg(dev, router_w, "router_w", torch.bfloat16, (E, H)),
+        _opt_arg(dev, router_bias, "router_bias", torch.float32, (E,)),
+        _opt_arg(dev, select_bias, "select_bias", torch.float32, (E,)),
+        _arg(dev, w13, "w13", torch.bfloat16, (E, 2 * I, H)),
+        _arg(dev, w2, "w2", torch.bfloat16, (E, H, I)),
+        _opt_arg(dev, residual, "residual", torch.bfloat16, (M, H)),
+        _opt_arg(dev, norm_w, "norm_w", torch.bfloat16, (H,)), float(eps), M, H, E, I, top_k,
+        score, n_group, topk_group, group_top, 1 if renormalize else 0, float(scale),
+        _opt_arg(dev, out, "out", torch.bfloat16, (M, H)),
+        _opt_arg(dev, residual_out, "residual_out", torch.bfloat16, (M, H)),
+        _opt_arg(dev, topk_ids_out, "topk_ids_out", torch.int32, (M, top_k)),
+        _opt_arg(dev, topk_w_out, "topk_w_out", torch.float32, (M, top_k)),
+        _arg(dev, workspace, "workspace", torch.uint8), workspace.numel(),
         _stream_on(dev, stream)))
 
 

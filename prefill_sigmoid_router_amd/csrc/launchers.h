@@ -216,6 +216,53 @@ hipError_t launch_i8_down(const int8_t* act, const float* act_scale, const int8_
                           const int32_t* num_tiles, int max_tiles, int tile_rows, int H, int I,
                           int top_k, int block, float* y, hipStream_t s);
 
+// The norms around a block (block_norm.hip): kinds, and what moe_block_norm takes.
+constexpr int kNormNone = 0, kNormRms = 1, kNormLayer = 2;
+struct BlockNormArgs {
+  const void *y, *residual;        // bf16, or fp32 with the flags below; or NULL
+  const uint16_t* gate;            // [H], [M, H] or [M, 1]
+  const uint16_t *post_w, *post_b, *pre_w, *pre_b;
+  int64_t y_ld, residual_ld, gate_ld, z_ld, out_ld;
+  int y_f32, residual_f32, gate_cols, post, pre, M, H;
+  float eps, weight_offset, residual_scale, block_scale;
+  void* z_out;                     // of residual's type
+  uint16_t* out;
+};
+hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t s);
+
+// bf16 products with an epilogue (bf16_gemm.hip); K % 8 == 0.
+constexpr int kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4;
+struct GemmArgs {
+  const uint16_t *x, *w, *bias;
+  const void* residual;
+  void* out;
+  int64_t x_ld, residual_ld, out_ld;
+  int M, N, K, act, gated, residual_f32, out_f32;
+  int wide;   // N, residual_ld and out_ld are multiples of 8: columns 16 bytes at a time
+};
+hipError_t launch_bf16_matmul(const GemmArgs& a, hipStream_t s);
+
+// The layer for a few tokens (few_layer.hip).
+constexpr int kFewMaxTokens = 16, kFewMaxPicks = 512;
+struct FewArgs {
+  const uint16_t *x, *router_w, *w13, *w2, *residual, *norm_w;
+  const float *router_bias, *select_bias;
+  float eps;
+  int M, H, E, I, top_k;
+  GroupRule rule;
+  uint16_t *out, *residual_out;
+  int32_t* ids_out;
+  float* w_out;
+  // filled in by the launcher
+  double* keys;     // logits [M, E]
+  int* sync;        // counters
+  float *act, *y;   // [M top_k, I], [M top_k, H]
+  int up_tiles, down_tiles, group_rows;
+};
+bool few_sizes_ok(int H, int I);
+size_t few_scratch_bytes(int M, int H, int E, int I, int top_k);
+hipError_t launch_few_layer(FewArgs a, void* scratch, hipStream_t s);
+
 // Weighted top-k combine + residual add + RMSNorm over fp32 rows of y, or over moe_forward's
 // split rows (first picks in fp32 in y0, the others in bf16 in y).
 hipError_t launch_finalize(const float* y, const float* topk_w, const uint16_t* residual,

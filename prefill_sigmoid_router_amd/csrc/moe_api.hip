@@ -924,3 +924,181 @@ int moe_forward_i8(const uint16_t* x, const uint16_t* router_w, const float* sel
 }
 
 }  // extern "C"
+
+namespace {
+
+constexpr int32_t kMaxNormRows = 1 << 30;
+constexpr int32_t kMaxGemmRows = 1 << 24, kMaxGemmK = 1 << 20;
+
+bool row_ld_ok(int64_t ld, int32_t H) { return ld >= H && ld % 8 == 0; }
+bool flag_ok(int32_t f) { return f == 0 || f == 1; }
+bool norm_kind_ok(int32_t k) { return k >= MOE_NORM_NONE && k <= MOE_NORM_LAYER; }
+
+bool gemm_sizes_ok(int32_t M, int32_t N, int32_t K, int32_t gated) {
+  return M >= 0 && M <= kMaxGemmRows && N >= 1 && N <= kMaxGemmRows && K >= 8 && K <= kMaxGemmK &&
+         K % 8 == 0 && flag_ok(gated);
+}
+
+bool few_sizes_ok(int32_t M, int32_t H, int32_t I, int32_t top_k) {
+  return M <= moe::kFewMaxTokens && M * top_k <= moe::kFewMaxPicks && moe::few_sizes_ok(H, I);
+}
+
+static_assert(moe::kFewMaxTokens == MOE_FEW_MAX_TOKENS && moe::kFewMaxPicks == MOE_FEW_MAX_PICKS, "");
+static_assert(moe::kNormRms == MOE_NORM_RMS && moe::kNormLayer == MOE_NORM_LAYER, "");
+static_assert(moe::kActRelu == MOE_ACT_RELU && moe::kActSilu == MOE_ACT_SILU &&
+                  moe::kActGelu == MOE_ACT_GELU && moe::kActGeluTanh == MOE_ACT_GELU_TANH, "");
+
+}  // namespace
+
+extern "C" {
+
+int moe_block_norm(const void* y, int32_t y_f32, int64_t y_ld, const void* residual,
+                   int32_t residual_f32, int64_t residual_ld, const uint16_t* gate,
+                   int32_t gate_cols, int64_t gate_ld, int32_t post, const uint16_t* post_w,
+                   const uint16_t* post_b, int32_t pre, const uint16_t* pre_w,
+                   const uint16_t* pre_b, float eps, float weight_offset, float residual_scale,
+                   float block_scale, int32_t M, int32_t H, void* z_out, int64_t z_ld,
+                   uint16_t* out, int64_t out_ld, moe_stream_t stream) {
+  if (M < 0 || M > kMaxNormRows || H < 8 || H > kMaxH || H % 8 != 0 || !flag_ok(y_f32) ||
+      !flag_ok(residual_f32) || !norm_kind_ok(post) || !norm_kind_ok(pre) || !(eps > 0.0f) ||
+      !isfinite(eps) || !isfinite(weight_offset) || !isfinite(residual_scale) ||
+      !isfinite(block_scale))
+    return MOE_ERR_INVALID_ARG;
+  if (M == 0) return MOE_OK;
+  if ((!y && !residual) || (!z_out && !out) || (!y && (post != MOE_NORM_NONE || gate)))
+    return MOE_ERR_INVALID_ARG;
+  if ((y && !row_ld_ok(y_ld, H)) || (residual && !row_ld_ok(residual_ld, H)) ||
+      (z_out && !row_ld_ok(z_ld, H)) || (out && !row_ld_ok(out_ld, H)))
+    return MOE_ERR_INVALID_ARG;
+  if (gate && !(gate_cols == H && (gate_ld == 0 || row_ld_ok(gate_ld, H))) &&
+      !(gate_cols == 1 && gate_ld >= 0))
+    return MOE_ERR_INVALID_ARG;
+  if ((y && !aligned(y, 16)) || (residual && !aligned(residual, 16)) ||
+      (gate && !aligned(gate, gate_cols == 1 ? 2 : 16)) || (z_out && !aligned(z_out, 16)) ||
+      (out && !aligned(out, 16)) || (post_w && !aligned(post_w, 16)) ||
+      (post_b && !aligned(post_b, 16)) || (pre_w && !aligned(pre_w, 16)) ||
+      (pre_b && !aligned(pre_b, 16)))
+    return MOE_ERR_INVALID_ARG;
+  moe::BlockNormArgs a{};
+  a.y = y;
+  a.residual = residual;
+  a.gate = gate;
+  a.post_w = post_w;
+  a.post_b = post_b;
+  a.pre_w = pre_w;
+  a.pre_b = pre_b;
+  a.y_ld = y_ld;
+  a.residual_ld = residual_ld;
+  a.gate_ld = gate_ld;
+  a.z_ld = z_ld;
+  a.out_ld = out_ld;
+  a.y_f32 = y_f32;
+  a.residual_f32 = residual_f32;
+  a.gate_cols = gate_cols;
+  a.post = post;
+  a.pre = pre;
+  a.M = M;
+  a.H = H;
+  a.eps = eps;
+  a.weight_offset = weight_offset;
+  a.residual_scale = residual_scale;
+  a.block_scale = block_scale;
+  a.z_out = z_out;
+  a.out = out;
+  return hip_status(moe::launch_block_norm(a, (hipStream_t)stream));
+}
+
+size_t moe_matmul_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t gated) {
+  if (!gemm_sizes_ok(M, N, K, gated)) return 0;
+  return 0;
+}
+
+int moe_matmul(const uint16_t* x, int64_t x_ld, const uint16_t* w, const uint16_t* bias, int32_t M,
+               int32_t N, int32_t K, int32_t act, int32_t gated, const void* residual,
+               int32_t residual_f32, int64_t residual_ld, void* out, int32_t out_f32,
+               int64_t out_ld, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  if (!gemm_sizes_ok(M, N, K, gated) || act < MOE_ACT_NONE || act > MOE_ACT_GELU_TANH ||
+      !flag_ok(residual_f32) || !flag_ok(out_f32))
+    return MOE_ERR_INVALID_ARG;
+  if ((int64_t)M * N >= (int64_t)1 << 38) return MOE_ERR_UNSUPPORTED;
+  if (M == 0) return MOE_OK;
+  if (!x || !w || !out || x_ld < K || x_ld % 8 != 0 || out_ld < N || (residual && residual_ld < N) ||
+      !aligned(x, 16) || !aligned(w, 16) || !aligned(out, 16) || (bias && !aligned(bias, 16)) ||
+      (residual && !aligned(residual, 16)))
+    return MOE_ERR_INVALID_ARG;
+  const size_t need = moe_matmul_workspace_bytes(M, N, K, gated);
+  if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
+    return MOE_ERR_WORKSPACE;
+  moe::GemmArgs a{};
+  a.x = x;
+  a.w = w;
+  a.bias = bias;
+  a.residual = residual;
+  a.out = out;
+  a.x_ld = x_ld;
+  a.residual_ld = residual_ld;
+  a.out_ld = out_ld;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.act = act;
+  a.gated = gated;
+  a.residual_f32 = residual_f32;
+  a.out_f32 = out_f32;
+  a.wide = N % 8 == 0 && out_ld % 8 == 0 && (!residual || residual_ld % 8 == 0);
+  return hip_status(moe::launch_bf16_matmul(a, (hipStream_t)stream));
+}
+
+size_t moe_few_workspace_bytes(int32_t M, int32_t H, int32_t E, int32_t I, int32_t top_k) {
+  if (!sizes_ok(M, H, E, I, top_k) || !few_sizes_ok(M, H, I, top_k)) return 0;
+  return moe::few_scratch_bytes(M, H, E, I, top_k);
+}
+
+int moe_forward_few(const uint16_t* x, const uint16_t* router_w, const float* router_bias,
+                    const float* select_bias, const uint16_t* w13, const uint16_t* w2,
+                    const uint16_t* residual, const uint16_t* norm_w, float eps, int32_t M,
+                    int32_t H, int32_t E, int32_t I, int32_t top_k, int32_t score, int32_t n_group,
+                    int32_t topk_group, int32_t group_top, int32_t renormalize, float scale,
+                    uint16_t* out, uint16_t* residual_out, int32_t* topk_ids_out,
+                    float* topk_w_out, void* workspace, size_t workspace_bytes,
+                    moe_stream_t stream) {
+  moe::GroupRule rule;
+  if (!sizes_ok(M, H, E, I, top_k) || (out && (!(eps > 0.0f) || !isfinite(eps))) ||
+      !make_rule(E, top_k, score, n_group, topk_group, group_top, renormalize, scale, &rule))
+    return MOE_ERR_INVALID_ARG;
+  if (!few_sizes_ok(M, H, I, top_k)) return MOE_ERR_UNSUPPORTED;
+  if (M == 0) return MOE_OK;
+  if (!x || !router_w || !w13 || !w2 || (!out && !residual_out) || (out && !norm_w) ||
+      !aligned(x, 16) || !aligned(router_w, 16) || !aligned(w13, 16) || !aligned(w2, 16) ||
+      (residual && !aligned(residual, 16)) || (out && !aligned(norm_w, 16)) ||
+      (out && !aligned(out, 16)) || (residual_out && !aligned(residual_out, 16)) ||
+      (router_bias && !aligned(router_bias, 4)) || (select_bias && !aligned(select_bias, 4)) ||
+      (topk_ids_out && !aligned(topk_ids_out, 4)) || (topk_w_out && !aligned(topk_w_out, 4)))
+    return MOE_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, kAlign) ||
+      workspace_bytes < moe::few_scratch_bytes(M, H, E, I, top_k))
+    return MOE_ERR_WORKSPACE;
+  moe::FewArgs a{};
+  a.x = x;
+  a.router_w = router_w;
+  a.w13 = w13;
+  a.w2 = w2;
+  a.residual = residual;
+  a.norm_w = norm_w;
+  a.router_bias = router_bias;
+  a.select_bias = select_bias;
+  a.eps = eps;
+  a.M = M;
+  a.H = H;
+  a.E = E;
+  a.I = I;
+  a.top_k = top_k;
+  a.rule = rule;
+  a.out = out;
+  a.residual_out = residual_out;
+  a.ids_out = topk_ids_out;
+  a.w_out = topk_w_out;
+  return hip_status(moe::launch_few_layer(a, workspace, (hipStream_t)stream));
+}
+
+}  // extern "C"
