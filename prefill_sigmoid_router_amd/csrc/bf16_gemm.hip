@@ -24,71 +24,45 @@ __device__ __forceinline__ float sigmoid_fast(float z) {
   return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
 }
 
-template <int N>
-__device__ __forceinline__ void activate(int act, float (&v)[N]) {
+// h Phi(h).  With t = 1 / (1 + |h| / 8^1/2), erfc(|h| / 2^1/2) = t 2^(P(t) - h^2 log2(e) / 2); P is a
+// Chebyshev fit over t in [1/8, 1] of log2(erfc(z) e^(z^2) / t), z = 2 / t - 2, good to 2^-23.  With
+// the exponent's roundings the result is within (1.25 h^2 + 14) 2^-24 of itself (erfcf of the device
+// library takes four times the instructions).
+__device__ __forceinline__ float gelu_exact(float h) {
+  const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(h), 0.35355339f, 1.0f));
+  float s = 0.2387803f;
+  s = fmaf(s, t, -1.1418399f);
+  s = fmaf(s, t, 2.0388212f);
+  s = fmaf(s, t, -1.4883672f);
+  s = fmaf(s, t, 0.27622172f);
+  s = fmaf(s, t, -0.20144565f);
+  s = fmaf(s, t, 0.117095776f);
+  s = fmaf(s, t, 0.54421836f);
+  s = fmaf(s, t, 1.4422425f);
+  s = fmaf(s, t, -1.825727f);
+  const float e = t * __builtin_amdgcn_exp2f(fmaf(h * h, -0.72134752f, s));
+  return h < 0.0f ? 0.5f * h * e : h * fmaf(e, -0.5f, 1.0f);
+}
+
+template <int R, int C>
+__device__ __forceinline__ void activate(int act, float (&v)[R][C]) {
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int q = 0; q < C; ++q) v[k][q] = f(v[k][q]);
+  };
   switch (act) {   // the same for every lane
-    case kActRelu:
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];   // (NaN stays)
-      break;
-    case kActSilu:
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] *= sigmoid_fast(v[i]);
-      break;
-    case kActGelu:
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = 0.5f * v[i] * erfcf(-0.70710678f * v[i]);
-      break;
+    case kActRelu: each([](float z) { return z < 0.0f ? 0.0f : z; }); break;   // (NaN stays)
+    case kActSilu: each([](float z) { return z * sigmoid_fast(z); }); break;
+    case kActGelu: each([](float z) { return gelu_exact(z); }); break;
     case kActGeluTanh:   // 1/2 (1 + tanh u) = sigmoid(2 u)
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        v[i] *= sigmoid_fast(1.5957691f * fmaf(0.044715f * v[i] * v[i], v[i], v[i]));
+      each([](float z) { return z * sigmoid_fast(1.5957691f * fmaf(0.044715f * z * z, z, z)); });
       break;
     default: break;
   }
 }
 
-// N consecutive bf16 or fp32 values from element i on (16-byte aligned).
-template <int N>
-__device__ __forceinline__ void load_values(const void* p, bool f32, size_t i, float (&v)[N]) {
-  if (f32) {
-#pragma unroll
-    for (int q = 0; q < N; q += 4) {
-      const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i + q);
-      v[q] = a.x;
-      v[q + 1] = a.y;
-      v[q + 2] = a.z;
-      v[q + 3] = a.w;
-    }
-  } else {
-#pragma unroll
-    for (int q = 0; q < N; q += 8) {
-      const u32x4 a = ld16(static_cast<const uint16_t*>(p) + i + q);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[q + 2 * j] = bf16lo(a[j]);
-        v[q + 2 * j + 1] = bf16hi(a[j]);
-      }
-    }
-  }
-}
-template <int N>
-__device__ __forceinline__ void store_values(void* p, bool f32, size_t i, const float (&v)[N]) {
-  if (f32) {
-#pragma unroll
-    for (int q = 0; q < N; q += 4)
-      *reinterpret_cast<float4*>(static_cast<float*>(p) + i + q) =
-          make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
-  } else {
-#pragma unroll
-    for (int q = 0; q < N; q += 8) {
-      u32x4 a;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) a[j] = pack_bf16x2(v[q + 2 * j], v[q + 2 * j + 1]);
-      st16(static_cast<uint16_t*>(p) + i + q, a);
-    }
-  }
-}
 __device__ __forceinline__ float load_value(const void* p, bool f32, size_t i) {
   return f32 ? static_cast<const float*>(p)[i] : bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
 }
@@ -97,58 +71,127 @@ __device__ __forceinline__ void store_value(void* p, bool f32, size_t i, float v
   else static_cast<uint16_t*>(p)[i] = (uint16_t)f32_to_bf16_rne(v);
 }
 
-// One result: sums h (gate) and u (up rows, GATED) of token m, column n.
-template <bool GATED>
-__device__ __forceinline__ void finish_one(const GemmArgs& p, int m, int n, float h, float u) {
-  if (p.bias) {
-    h += bf16_to_f32(p.bias[n]);
-    if (GATED) u += bf16_to_f32(p.bias[p.N + n]);
-  }
-  float v[1] = {h};
-  activate(p.act, v);
-  if (GATED) v[0] *= u;
-  if (p.residual) v[0] += load_value(p.residual, p.residual_f32, (size_t)m * p.residual_ld + n);
-  store_value(p.out, p.out_f32, (size_t)m * p.out_ld + n, v[0]);
+// C values of a row from column n on (a multiple of 8) go 16 bytes at a time, or one by one.
+template <int C>
+__device__ __forceinline__ bool wide_at(const GemmArgs& p, int n) {
+  return p.wide && n + C <= p.N;
 }
 
-// C results of token m, columns n .. n + C - 1 (n a multiple of 8).
-template <bool GATED, int C>
-__device__ __forceinline__ void finish(const GemmArgs& p, int m, int n, float (&h)[C], float (&u)[C]) {
-  if (!p.wide || n + C > p.N) {
-#pragma unroll 1
-    for (int i = 0; i < C && n + i < p.N; ++i) {
-      float a = h[0], b = u[0];   // (no indexed registers)
+// C values of bias for the columns n ..; gated: those of the up rows, `from` = N values on.
+template <int C>
+__device__ __forceinline__ void load_bias(const GemmArgs& p, int n, int from, float (&b)[C]) {
 #pragma unroll
-      for (int q = 1; q < C; ++q) {
-        a = q == i ? h[q] : a;
-        b = q == i ? u[q] : b;
+  for (int q = 0; q < C; ++q) b[q] = 0.0f;
+  if (!p.bias) return;
+  const uint16_t* src = p.bias + from + n;
+  if (wide_at<C>(p, n)) {
+#pragma unroll
+    for (int q = 0; q < C; q += 8) {
+      const u32x4 a = ld16(src + q);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        b[q + 2 * j] = bf16lo(a[j]);
+        b[q + 2 * j + 1] = bf16hi(a[j]);
       }
-      finish_one<GATED>(p, m, n + i, a, b);
     }
-    return;
+  } else {
+#pragma unroll
+    for (int q = 0; q < C; ++q)
+      if (n + q < p.N) b[q] = bf16_to_f32(src[q]);
   }
-  float t[C];
-  if (p.bias) {
-    load_values(p.bias, false, n, t);
+}
+
+// C values of the residual's row m, as they come: in flight until they are needed.
+template <int C>
+struct Residual {
+  uint32_t r[C];
+  __device__ __forceinline__ void load(const GemmArgs& p, int m, int n) {
+    const size_t i = (size_t)m * p.residual_ld + n;
+    if (wide_at<C>(p, n)) {
+      const char* src = static_cast<const char*>(p.residual) + i * (p.residual_f32 ? 4 : 2);
 #pragma unroll
-    for (int i = 0; i < C; ++i) h[i] += t[i];
-    if (GATED) {
-      load_values(p.bias, false, (size_t)p.N + n, t);
+      for (int q = 0; q < C / 4; ++q)
+        if (q < C / 8 || p.residual_f32) {
+          const u32x4 a = ld16(src + 16 * q);
 #pragma unroll
-      for (int i = 0; i < C; ++i) u[i] += t[i];
+          for (int j = 0; j < 4; ++j) r[4 * q + j] = a[j];
+        }
+    } else {
+#pragma unroll
+      for (int q = 0; q < C; ++q)
+        r[q] = n + q < p.N ? __float_as_uint(load_value(p.residual, p.residual_f32, i + q)) : 0u;
     }
+  }
+  __device__ __forceinline__ void add(const GemmArgs& p, int n, float (&v)[C]) const {
+    if (wide_at<C>(p, n) && !p.residual_f32) {
+#pragma unroll
+      for (int q = 0; q < C; q += 2) {
+        v[q] += bf16lo(r[q / 2]);
+        v[q + 1] += bf16hi(r[q / 2]);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < C; ++q) v[q] += __uint_as_float(r[q]);
+    }
+  }
+};
+
+// C results each of R tokens m (those from p.M on are left out), columns n ..: sums h (of the gate
+// rows) and u (of the up rows, GATED), and what is added to them.
+template <bool GATED, int R, int C>
+__device__ __forceinline__ void finish(const GemmArgs& p, const int (&m)[R], int n, float (&h)[R][C],
+                                       float (&u)[R][C], const float (&bh)[C], const float (&bu)[C],
+                                       const Residual<C> (&res)[R]) {
+  if (p.bias) {
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int q = 0; q < C; ++q) {
+        h[k][q] += bh[q];
+        if (GATED) u[k][q] += bu[q];
+      }
   }
   activate(p.act, h);
   if (GATED) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) h[i] *= u[i];
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int q = 0; q < C; ++q) h[k][q] *= u[k][q];
   }
   if (p.residual) {
-    load_values(p.residual, p.residual_f32, (size_t)m * p.residual_ld + n, t);
 #pragma unroll
-    for (int i = 0; i < C; ++i) h[i] += t[i];
+    for (int k = 0; k < R; ++k) res[k].add(p, n, h[k]);
   }
-  store_values(p.out, p.out_f32, (size_t)m * p.out_ld + n, h);
+  if (wide_at<C>(p, n)) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      if (m[k] >= p.M) continue;
+      const size_t o = (size_t)m[k] * p.out_ld + n;
+      if (p.out_f32) {
+#pragma unroll
+        for (int q = 0; q < C; q += 4)
+          *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o + q) =
+              make_float4(h[k][q], h[k][q + 1], h[k][q + 2], h[k][q + 3]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < C; q += 8) {
+          u32x4 a;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) a[j] = cvt_bf16x2(h[k][q + 2 * j], h[k][q + 2 * j + 1]);
+          st16(static_cast<uint16_t*>(p.out) + o + q, a);
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      if (m[k] >= p.M) continue;
+      const size_t o = (size_t)m[k] * p.out_ld + n;
+#pragma unroll
+      for (int q = 0; q < C; ++q)
+        if (n + q < p.N) store_value(p.out, p.out_f32, o + q, h[k][q]);
+    }
+  }
 }
 
 // LDS rows are one 128-byte line of a chunk each; 16-byte slot q of row r holds the part
@@ -278,17 +321,29 @@ __global__ __launch_bounds__(64 * WN * WM) void ring_kernel(GemmArgs p) {
     }
     // lane (li, lg) holds token row li of each token tile and SPAN columns from n0 on
     const int n0 = col0 + (GATED ? 32 : 64) * wn + SPAN * lg;
+    if (n0 < p.N && my_active > 0) {
+      float bh[SPAN], bu[SPAN];
+      load_bias(p, n0, 0, bh);
+      if (GATED) load_bias(p, n0, p.N, bu);
+      Residual<SPAN> res[C::MTW];
+      if (p.residual) {
 #pragma unroll
-    for (int s = 0; s < C::MTW; ++s) {
-      const int r = 16 * (wm * C::MTW + s) + li;
-      if (s >= my_active || r >= nlive || n0 >= p.N) continue;
-      float h[SPAN], u[SPAN];
-#pragma unroll
-      for (int q = 0; q < SPAN; ++q) {
-        h[q] = acc[q >> 2][s][q & 3];
-        u[q] = GATED ? acc[2 + (q >> 2 & 1)][s][q & 3] : 0.0f;
+        for (int s = 0; s < C::MTW; ++s)
+          res[s].load(p, start + min(16 * (wm * C::MTW + s) + li, nlive - 1), n0);
       }
-      finish<GATED>(p, start + r, n0, h, u);
+      float h[C::MTW][SPAN], u[C::MTW][SPAN];
+      int m[C::MTW];
+#pragma unroll
+      for (int s = 0; s < C::MTW; ++s) {
+        const int r = 16 * (wm * C::MTW + s) + li;
+        m[s] = r < nlive ? start + r : p.M;
+#pragma unroll
+        for (int q = 0; q < SPAN; ++q) {
+          h[s][q] = acc[q >> 2][s][q & 3];
+          u[s][q] = GATED ? acc[2 + (q >> 2 & 1)][s][q & 3] : 0.0f;
+        }
+      }
+      finish<GATED>(p, m, n0, h, u, bh, bu, res);
     }
     __syncthreads();   // the next item's first copies reuse the ring
   }
@@ -354,18 +409,27 @@ __global__ __launch_bounds__(512) void skinny_kernel(GemmArgs p, int n_ntiles, i
 #pragma unroll
     for (int q = 0; q < 4; ++q) part[wave][t][q][lane] = acc[t][q];
   __syncthreads();
-  // thread -> token r, column c: weight row c is result c % 4 of lane 16 (c / 4) + r % 16 of
+  // thread -> token r, column c, with the residual in flight beside the sums: weight row c is result c % 4 of lane 16 (c / 4) + r % 16 of
   // token tile r / 16
   for (int i = threadIdx.x; i < COLS * 16 * MT; i += 64 * WAVES) {
     const int r = i / COLS, c = i % COLS;
     if (m0 + r >= p.M || n0 + c >= p.N) continue;
-    float h = 0.0f, u = 0.0f;
+    const int n = n0 + c;
+    const float bh = p.bias ? bf16_to_f32(p.bias[n]) : 0.0f;
+    const float bu = GATED && p.bias ? bf16_to_f32(p.bias[p.N + n]) : 0.0f;
+    const float res =
+        p.residual ? load_value(p.residual, p.residual_f32, (size_t)(m0 + r) * p.residual_ld + n) : 0.0f;
+    float h[1][1] = {{0.0f}}, u = 0.0f;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) {
-      h += part[w][r >> 4][c & 3][16 * (c >> 2) + (r & 15)];
+      h[0][0] += part[w][r >> 4][c & 3][16 * (c >> 2) + (r & 15)];
       if (GATED) u += part[w][r >> 4][c & 3][16 * ((c + 8) >> 2) + (r & 15)];
     }
-    finish_one<GATED>(p, m0 + r, n0 + c, h, u);
+    h[0][0] += bh;
+    activate(p.act, h);
+    if (GATED) h[0][0] *= u + bu;
+    if (p.residual) h[0][0] += res;
+    store_value(p.out, p.out_f32, (size_t)(m0 + r) * p.out_ld + n, h[0][0]);
   }
 }
 
@@ -379,11 +443,290 @@ hipError_t launch_skinny(const GemmArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Many tokens: 256 tokens x 256 weight rows (GATED: 128 gate and 128 up rows) per workgroup of 4
+// waves, a wave 128 x 128 on v_mfma_f32_32x32x16_bf16, whose 256 sums a lane fill the
+// accumulation registers: fragment reads then take half of the LDS's rate (8 waves of 64 x 128:
+// three quarters, and with the copies' writes all of it).
+//
+// K in chunks of 64, a panel of 256 weight rows and one of 256 token rows each, in a ring of five
+// LDS slots of 32 KiB: two of the present chunk, two of the next, one more.  A chunk is 4 steps of
+// 16 values; a step's 16 MFMAs run on one of two sets of fragment registers while the next step's
+// fragments are read into the other.  Before the last step of chunk c every wave has read all of it
+// and its copies of chunk c + 1 have landed: one barrier, which frees two slots, for the tokens of
+// chunk c + 2 (copied in that step and the next) and the weights of chunk c + 3 (in the two steps
+// after).  So every step copies 16 KiB: with two stages of both and all 64 copies of the waves in
+// one step they wait for the address unit (M = N = 4096, K = 7168: 222 us, in two steps 206, without
+// copies 167).  The stream of chunks runs on into the workgroup's next item; results go through
+// the two slots that an item's last chunk frees.
+//
+// LDS rows as above.  Fragment row r of the weights is row 16 (r / 4 % 2) + 4 (r / 8) + r % 4 of
+// its 32, so that a lane's 16 sums of a fragment are 16 consecutive columns.
+#ifdef __HIP_DEVICE_COMPILE__   // the host pass knows no buffer descriptors
+// Buffer descriptor of raw bytes from a wave-uniform pointer on, without a bound.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint16_t* base) {
+  const uint64_t b = (uint64_t)base;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)b);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc((void*)((uint64_t)hi << 32 | lo), 0, -1, 0x00020000);
+}
+#endif
+
+constexpr int kBig = 256, kBigSlot = kBig * 128, kBigSlots = 5;
+constexpr int kBigMinChunks = 2;
+constexpr int64_t kBigMaxLd = 1 << 23;   // 64 rows within 32-bit byte offsets
+
+typedef __attribute__((ext_vector_type(16))) float f32x16;
+__device__ __forceinline__ f32x16 mfma32x32x16(u32x4 a, u32x4 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
+}
+
+// This workgroup's items: each XCD has a contiguous share of them, in which 32 in a row (what an
+// XCD's CUs work on at once) are 4 column tiles x 8 token tiles: 12 panels for its L2 to hold,
+// where 32 token tiles of one column tile are 33.
+struct BlockWalk {
+  int mtiles, ntiles, items, per_xcd, first, slot, stride;
+  __device__ BlockWalk(int mt, int nt)
+      : mtiles(mt), ntiles(nt), items(mt * nt), per_xcd((items + kXcds - 1) / kXcds),
+        first((blockIdx.x % kXcds) * per_xcd), slot(blockIdx.x / kXcds), stride(gridDim.x / kXcds) {}
+  __device__ bool next(int& mtile, int& ntile) {
+    const int item = first + slot;
+    if (slot >= per_xcd || item >= items) return false;
+    slot += stride;
+    const int group = item / (4 * mtiles), in = item % (4 * mtiles);
+    const int width = min(4, ntiles - 4 * group);
+    mtile = in / width;
+    ntile = 4 * group + in % width;
+    return true;
+  }
+};
+
+template <bool GATED, bool RAGGED>
+__device__ __forceinline__ void big_products(const GemmArgs& p, unsigned char* lds) {
+#ifdef __HIP_DEVICE_COMPILE__
+  constexpr int COLS = GATED ? kBig / 2 : kBig;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wn = wave & 1, wm = wave >> 1, r = lane & 31, h = lane >> 5, rr = lane >> 3;
+  const int K = p.K, nch = (K + kKC - 1) / kKC, whole = K / kKC;
+  // fragment addresses of step 0; step s: ^ 32 s
+  const int wperm = 16 * (r >> 2 & 1) + 4 * (r >> 3) + (r & 3);
+  const int wswz = (wperm >> 1 & 3) | (wperm >> 4) << 2;
+  const int waddr = (GATED ? 64 : 128) * wn * 128 + wperm * 128 + 16 * (h ^ wswz);
+  const int taddr = (128 * wm + r) * 128 + 16 * (h ^ (r >> 1 & 7));
+  f32x16 acc[4][4];
+  u32x4 wa[2][4], tb[2][4];   // fragments of even and odd steps
+  auto slot_at = [&](int slot) { return lds + (slot < kBigSlots ? slot : slot - kBigSlots) * kBigSlot; };
+  auto read = [&](int slot, int s) {   // the weights' slot; the tokens' is the next
+    const unsigned char *wbase = slot_at(slot), *tbase = slot_at(slot + 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      wa[s & 1][i] = *reinterpret_cast<const u32x4*>(
+          wbase + (waddr ^ (32 * s)) + (GATED ? (i & 1) * 4096 + (i >> 1) * 16384 : i * 4096));
+      tb[s & 1][i] = *reinterpret_cast<const u32x4*>(tbase + (taddr ^ (32 * s)) + i * 4096);
+    }
+  };
+  auto multiply = [&](int s) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = mfma32x32x16(wa[s & 1][i], tb[s & 1][j], acc[i][j]);
+  };
+  // A wave copies weight rows 64 wave .. and token rows 64 wave .., 8 pieces of 8 rows each; lane l
+  // slot l % 8 of row l / 8.  Rows past the last repeat it.
+  __amdgpu_buffer_rsrc_t wsrc, tsrc;
+  uint32_t woff[8], toff[8];
+  auto wpart = [&](int i) { return (lane & 7) ^ ((rr >> 1 & 3) | (i >> 1 & 1) << 2); };
+  auto tpart = [&](int i) { return (lane & 7) ^ ((8 * i + rr) >> 1 & 7); };
+  auto sources = [&](int m0, int n0) {
+    int rr = lane >> 3;   // (computed here, not held through the item's loop)
+    asm volatile("" : "+v"(rr));
+    const int wfirst = min(n0 + 64 * (GATED ? wave & 1 : wave), p.N - 1);
+    const int tfirst = min(m0 + 64 * wave, p.M - 1);
+    wsrc = buffer_of(p.w + ((size_t)(GATED && wave >= 2 ? p.N : 0) + wfirst) * K);
+    tsrc = buffer_of(p.x + (size_t)tfirst * p.x_ld);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      woff[i] = 2 * (uint32_t)min(8 * i + rr, p.N - 1 - wfirst) * (uint32_t)K + 16 * wpart(i);
+      toff[i] = 2 * (uint32_t)min(8 * i + rr, p.M - 1 - tfirst) * (uint32_t)p.x_ld + 16 * tpart(i);
+    }
+  };
+  // pieces 4 half .. of a panel of chunk c; a partial last chunk, zero-filled, through registers
+  auto copy = [&](int slot, int c, int half, __amdgpu_buffer_rsrc_t from, const uint32_t (&off)[8],
+                  auto part) {
+    unsigned char* base = slot_at(slot) + wave * 8192;
+#pragma unroll
+    for (int i = 4 * half; i < 4 * half + 4; ++i) {
+      if (RAGGED && c == whole) {
+        u32x4 v = u32x4{0, 0, 0, 0};
+        if (c * kKC + 8 * part(i) < K) v = __builtin_amdgcn_raw_buffer_load_b128(from, off[i], c * 128, 0);
+        *reinterpret_cast<u32x4*>(base + i * 1024 + lane * 16) = v;
+      } else {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_void*)(base + i * 1024), 16, off[i], c * 128, 0, 0);
+      }
+    }
+  };
+  auto copy_w = [&](int slot, int c, int half) { copy(slot, c, half, wsrc, woff, wpart); };
+  auto copy_t = [&](int slot, int c, int half) { copy(slot, c, half, tsrc, toff, tpart); };
+
+  // Results: fragment by token fragment (64 rows of the tile at a time) through two LDS slots, fp32,
+  // 16-byte slots XORed with the row; then 8 columns of a row per thread, whole lines of a row
+  // together, the residuals of the next four rows in flight.
+  constexpr int G = GATED ? 16 : 32, ROWS = 256 / G, PASSES = 64 / ROWS;   // threads of a row, rows of a pass
+  auto barrier = [&] { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+  auto results = [&](unsigned char* low, unsigned char* high, int m0, int n0) {
+    int tid = threadIdx.x;   // (addresses are computed here, not held through the item's loop)
+    asm volatile("" : "+v"(tid));
+    const int group = tid % G, row0 = tid / G, r = tid & 31, h = tid >> 5 & 1;
+    const int n = n0 + 8 * group;
+    const bool on = n < p.N;
+    float bh[8], bu[8];
+    load_bias(p, min(n, p.N - 1), 0, bh);
+    if (GATED) load_bias(p, min(n, p.N - 1), p.N, bu);
+    auto token = [&](int g, int k) {   // row k of this thread's four in group g of passes
+      const int lr = (g * 4 + k) % PASSES * ROWS + row0;
+      return m0 + 128 * (lr >> 5) + 32 * (g * 4 / PASSES) + (lr & 31);
+    };
+    Residual<8> res[4];
+    auto fetch = [&](int g, int k) {
+      if (p.residual && on && token(g, k) < p.M) res[k].load(p, token(g, k), n);
+    };
+#pragma unroll
+    for (int k = 0; k < 4; ++k) fetch(0, k);
+#pragma unroll
+    for (int ph = 0; ph < 4; ++ph) {
+      unsigned char* const mine = (wm ? high : low) + r * 1024;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int col = GATED ? 128 * (i >> 1) + 64 * wn + 32 * (i & 1) + 16 * h + 4 * k
+                                : 128 * wn + 32 * i + 16 * h + 4 * k;
+          *reinterpret_cast<f32x4*>(mine + 16 * ((col >> 2) ^ r)) =
+              f32x4{acc[i][ph][4 * k], acc[i][ph][4 * k + 1], acc[i][ph][4 * k + 2], acc[i][ph][4 * k + 3]};
+        }
+        __builtin_amdgcn_sched_barrier(0);   // (16 sums at a time leave the accumulation registers)
+      }
+      barrier();
+#pragma unroll 1
+      for (int g = ph * (PASSES / 4); g < (ph + 1) * (PASSES / 4); ++g) {
+        float v[4][8], u[4][8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int lr = (g * 4 + k) % PASSES * ROWS + row0;
+          const unsigned char* src = (lr & 32 ? high : low) + (lr & 31) * 1024;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const f32x4 a = *reinterpret_cast<const f32x4*>(src + 16 * ((2 * group + half) ^ (lr & 31)));
+            f32x4 b = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (GATED) b = *reinterpret_cast<const f32x4*>(src + 16 * ((32 + 2 * group + half) ^ (lr & 31)));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              v[k][4 * half + e] = a[e];
+              u[k][4 * half + e] = b[e];
+            }
+          }
+        }
+        int m[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] = on ? token(g, k) : p.M;
+        finish<GATED>(p, m, n, v, u, bh, bu, res);
+        if (g + 1 < PASSES) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) fetch(g + 1, k);
+        }
+      }
+      barrier();
+    }
+  };
+
+  BlockWalk walk((p.M + kBig - 1) / kBig, (p.N + COLS - 1) / COLS);
+  int mtile, ntile;
+  if (!walk.next(mtile, ntile)) return;
+  sources(mtile * kBig, ntile * COLS);
+  int slot = 0;   // of the present chunk's weights
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    copy_w(0, 0, half);
+    copy_t(1, 0, half);
+  }
+#pragma unroll
+  for (int half = 0; half < 2; ++half) copy_w(2, 1, half);   // (nch >= 2)
+  wait_vmcnt<8>();
+  barrier();
+  for (;;) {
+    const int m0 = mtile * kBig, n0 = ntile * COLS;
+    bool more = false;
+    copy_t(slot + 3, 1, 0);
+    read(slot, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < nch; ++c) {
+      const int ahead = c + 2 < nch ? c + 2 : c + 2 - nch;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        if (s == 1 && c == nch - 2) {   // the copies that follow are the next item's (repeats without one)
+          more = walk.next(mtile, ntile);
+          sources(mtile * kBig, ntile * COLS);
+        }
+        if (s == 3) {   // all but the 8 copies of the weights of chunk c + 2 have landed
+          asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+          if (c + 1 < nch) copy_t(slot, ahead, 0);   // (an item's last chunk leaves its slots to the results)
+          read(slot + 2, 0);
+        } else {
+          if (s == 0) copy_t(slot + 3, c + 1 < nch ? c + 1 : 0, 1);
+          else copy_w(slot + 4, ahead, s - 1);
+          read(slot, s + 1);
+        }
+        multiply(s);
+        // one fragment read beside each of the first eight MFMAs, a copy beside every second
+        if (!RAGGED) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      slot = slot + 2 < kBigSlots ? slot + 2 : slot + 2 - kBigSlots;
+    }
+    const int last = slot + 3;   // (two back)
+    results(slot_at(last), slot_at(last + 1), m0, n0);
+    if (!more) break;
+  }
+  wait_vmcnt<0>();   // copies into LDS that are still in flight end with the workgroup
+#endif
+}
+
+template <bool GATED, bool RAGGED>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void big_kernel(GemmArgs p) {
+  __shared__ __align__(16) unsigned char lds[kBigSlots * kBigSlot];
+  big_products<GATED, RAGGED>(p, lds);
+}
+
+template <bool GATED>
+hipError_t launch_big(const GemmArgs& a, hipStream_t s) {
+  const int cols = GATED ? kBig / 2 : kBig;
+  const long items = (long)((a.M + kBig - 1) / kBig) * ((a.N + cols - 1) / cols);
+  const dim3 grid((unsigned)walk_grid(items, kBigSlots * kBigSlot)), threads(256);
+  if (a.K % kKC == 0) hipLaunchKernelGGL((big_kernel<GATED, false>), grid, threads, 0, s, a);
+  else hipLaunchKernelGGL((big_kernel<GATED, true>), grid, threads, 0, s, a);
+  return hipGetLastError();
+}
+
 template <bool GATED>
 hipError_t launch_sized(const GemmArgs& a, hipStream_t s) {
   if (a.M <= 16) return launch_skinny<1, GATED>(a, s);
   if (a.M <= 32) return launch_skinny<2, GATED>(a, s);
   if (a.M <= 512) return launch_ring<64, 1, 4, 4, GATED>(a, s);
+  if (a.x_ld <= kBigMaxLd && a.K > (kBigMinChunks - 1) * kKC) return launch_big<GATED>(a, s);
   return launch_ring<128, 4, 2, 3, GATED>(a, s);
 }
 

@@ -9,10 +9,12 @@
 // unrounded z).  The mean of squared distances is taken around each wave's own mean and moved
 // to the row's (Chan's pairwise formula: n_w (mean_w - mean)^2 more), so a row whose mean is
 // far above its spread loses nothing, and a LAYER norm costs one barrier as an RMS norm does.
+#include <algorithm>
 #include <type_traits>
 
 #include "device_common.h"
 #include "launchers.h"
+#include "wave_ops.h"
 
 namespace moe {
 
@@ -43,7 +45,7 @@ struct Raw<true> {
 __device__ __forceinline__ void store_bf16(uint16_t* p, const float (&v)[8]) {
   u32x4 u;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) u[q] = pack_bf16x2(v[2 * q], v[2 * q + 1]);
+  for (int q = 0; q < 4; ++q) u[q] = cvt_bf16x2(v[2 * q], v[2 * q + 1]);
   st16(p, u);
 }
 __device__ __forceinline__ void store_f32(float* p, const float (&v)[8]) {
@@ -68,8 +70,8 @@ __device__ __forceinline__ float2 row_moments(const float (&v)[NC][8], const boo
         for (int j = 0; j < 8; ++j) sum += v[i][j];
         n += 8.0f;
       }
-    n_w = wave_sum(n);
-    mean_w = n_w > 0.0f ? wave_sum(sum) / n_w : 0.0f;
+    n_w = wave_sum_f32(n);
+    mean_w = n_w > 0.0f ? wave_sum_f32(sum) / n_w : 0.0f;
   }
   float sq = 0.0f;
 #pragma unroll
@@ -78,7 +80,7 @@ __device__ __forceinline__ float2 row_moments(const float (&v)[NC][8], const boo
 #pragma unroll
       for (int j = 0; j < 8; ++j) sq += (v[i][j] - mean_w) * (v[i][j] - mean_w);
     }
-  sq = wave_sum(sq);
+  sq = wave_sum_f32(sq);
   const float inv = 1.0f / (float)H;
   if (ONE) return make_float2(mean_w, sq * inv);
   // each wave's values in order, n_w from the wave's place: chunks wave * 64 + threads * i on
@@ -102,87 +104,144 @@ __device__ __forceinline__ float2 row_moments(const float (&v)[NC][8], const boo
   return make_float2(mean, total * inv);
 }
 
-// A thread holds chunks (8 values) lane + threads * i of its row, i < NC.  ONE: a wave per row,
-// else a workgroup per row.
+// A thread holds chunks (8 values) lane + threads * i of its row, i < NC, and walks rows; the next
+// row's values are in flight while a row is reduced.  What belongs to the channels is read once:
+//   p = (offset + post_w) * channel gate * block_scale,  q = offset + pre_w
+// ONE: a wave per row (no barriers), else a workgroup per row.
 template <int NC, bool YF32, bool RF32, bool ONE>
-__global__ __launch_bounds__(1024) void block_norm_kernel(BlockNormArgs p) {
+__global__ __launch_bounds__(ONE ? 256 : NC == 1 ? 1024 : 512) void block_norm_kernel(BlockNormArgs a) {
   __shared__ float2 red[2][kMaxWaves + kMaxWaves / 2];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int waves = blockDim.x >> 6;
   const int tid = ONE ? lane : threadIdx.x, threads = ONE ? kWave : blockDim.x;
-  const int row0 = ONE ? blockIdx.x * waves + wave : blockIdx.x;
   const int stride = ONE ? gridDim.x * waves : gridDim.x;
-  const int chunks = p.H >> 3;
+  const int chunks = a.H >> 3;
+  int row = ONE ? blockIdx.x * waves + wave : blockIdx.x;
+  if (row >= a.M) return;
   bool in[NC];
   int at[NC];
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int c = tid + threads * i;
     in[i] = c < chunks;
-    at[i] = 8 * (in[i] ? c : 0);
+    at[i] = 8 * c;
   }
-  for (int row = row0; row < p.M; row += stride) {
-    Raw<YF32> y[NC];
-    Raw<RF32> r[NC];
-    Raw<false> g[NC];
+  Raw<YF32> y[NC];
+  Raw<RF32> r[NC];
+  auto fetch = [&](int t) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      y[i].zero();
-      r[i].zero();
-      if (in[i]) {
-        if (p.y) y[i].load(p.y, (size_t)row * p.y_ld + at[i]);
-        if (p.residual) r[i].load(p.residual, (size_t)row * p.residual_ld + at[i]);
-        if (p.gate && p.gate_cols > 1) g[i].load(p.gate, (size_t)row * p.gate_ld + at[i]);
-      }
+      if (a.y && in[i]) y[i].load(a.y, (size_t)t * a.y_ld + at[i]);
+      if (a.residual && in[i]) r[i].load(a.residual, (size_t)t * a.residual_ld + at[i]);
     }
-    const float token_gate =
-        p.gate && p.gate_cols == 1 ? bf16_to_f32(p.gate[(size_t)row * p.gate_ld]) : 1.0f;
-    float v[NC][8];
-    auto normalize = [&](int kind, const uint16_t* w, const uint16_t* b, float2* slot) {
-      const float2 m = row_moments<NC, ONE>(v, in, kind == kNormLayer, p.H, wave, waves, lane, slot);
-      const float f = 1.0f / sqrtf(m.y + p.eps);
+  };
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        if (!in[i]) continue;
-        Raw<false> wv, bv;
-        if (w) wv.load(w, at[i]);
-        if (b) bv.load(b, at[i]);
+  for (int i = 0; i < NC; ++i) {
+    y[i].zero();
+    r[i].zero();
+  }
+  fetch(row);
+  const bool token_gate = a.gate && a.gate_cols == 1;
+  const bool full_gate = a.gate && a.gate_cols > 1 && a.gate_ld != 0;
+  const bool channel_gate = a.gate && a.gate_cols > 1 && a.gate_ld == 0;
+  float p[NC][8], q[NC][8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          v[i][j] = (v[i][j] - m.x) * f;
-          if (w) v[i][j] *= p.weight_offset + wv.get(j);
-          if (b) v[i][j] += bv.get(j);
-        }
-      }
-    };
+  for (int i = 0; i < NC; ++i) {
+    Raw<false> wp, wg, wq;
+    wp.zero();
+    wg.zero();
+    wq.zero();
+    if (a.post_w && in[i]) wp.load(a.post_w, at[i]);
+    if (channel_gate && in[i]) wg.load(a.gate, at[i]);
+    if (a.pre_w && in[i]) wq.load(a.pre_w, at[i]);
 #pragma unroll
-    for (int i = 0; i < NC; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = y[i].get(j);
-    if (p.post != kNormNone) normalize(p.post, p.post_w, p.post_b, red[0]);
+    for (int j = 0; j < 8; ++j) {
+      p[i][j] = a.post != kNormNone && a.post_w ? a.weight_offset + wp.get(j) : 1.0f;
+      if (channel_gate) p[i][j] *= wg.get(j);
+      p[i][j] *= a.block_scale;
+      q[i][j] = a.pre_w ? a.weight_offset + wq.get(j) : 1.0f;
+    }
+  }
+  for (;;) {
+    float v[NC][8], w[NC][8];   // y, later z; residual
 #pragma unroll
     for (int i = 0; i < NC; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        float u = v[i][j] * p.block_scale;
-        if (p.gate) u *= p.gate_cols > 1 ? g[i].get(j) : token_gate;
-        v[i][j] = r[i].get(j) * p.residual_scale + u;
+        v[i][j] = y[i].get(j);
+        w[i][j] = r[i].get(j) * a.residual_scale;
       }
-    if (p.z_out) {
+    const int next = row + stride;
+    if (next < a.M) fetch(next);
+    const float tg = token_gate ? bf16_to_f32(a.gate[(size_t)row * a.gate_ld]) : 1.0f;
+    float f = 1.0f;
+    if (a.post != kNormNone) {
+      const float2 m = row_moments<NC, ONE>(v, in, a.post == kNormLayer, a.H, wave, waves, lane, red[0]);
+      f = 1.0f / sqrtf(m.y + a.eps);
+      if (a.post == kNormLayer) {
 #pragma unroll
-      for (int i = 0; i < NC; ++i)
-        if (in[i]) {
-          const size_t o = (size_t)row * p.z_ld + at[i];
-          if (RF32) store_f32(static_cast<float*>(p.z_out) + o, v[i]);
-          else store_bf16(static_cast<uint16_t*>(p.z_out) + o, v[i]);
+        for (int i = 0; i < NC; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[i][j] -= m.x;
+      }
+    }
+    f *= tg;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      if (!in[i]) continue;
+      if (full_gate) {
+        Raw<false> g;
+        g.load(a.gate, (size_t)row * a.gate_ld + at[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] *= g.get(j);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = fmaf(v[i][j] * f, p[i][j], w[i][j]);
+      if (a.post != kNormNone && a.post_b) {   // + b gate block_scale
+        Raw<false> b, g;
+        b.load(a.post_b, at[i]);
+        g.zero();
+        if (full_gate || channel_gate) g.load(a.gate, (full_gate ? (size_t)row * a.gate_ld : 0) + at[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          v[i][j] = fmaf(b.get(j) * (full_gate || channel_gate ? g.get(j) : tg), a.block_scale, v[i][j]);
+      }
+      if (a.z_out) {
+        const size_t o = (size_t)row * a.z_ld + at[i];
+        if (RF32) store_f32(static_cast<float*>(a.z_out) + o, v[i]);
+        else store_bf16(static_cast<uint16_t*>(a.z_out) + o, v[i]);
+      }
+    }
+    if (a.out) {
+      f = 1.0f;
+      if (a.pre != kNormNone) {
+        const float2 m = row_moments<NC, ONE>(v, in, a.pre == kNormLayer, a.H, wave, waves, lane, red[1]);
+        f = 1.0f / sqrtf(m.y + a.eps);
+        if (a.pre == kNormLayer) {
+#pragma unroll
+          for (int i = 0; i < NC; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] -= m.x;
         }
-    }
-    if (p.pre != kNormNone) normalize(p.pre, p.pre_w, p.pre_b, red[1]);
-    if (p.out) {
+      }
 #pragma unroll
-      for (int i = 0; i < NC; ++i)
-        if (in[i]) store_bf16(p.out + (size_t)row * p.out_ld + at[i], v[i]);
+      for (int i = 0; i < NC; ++i) {
+        if (!in[i]) continue;
+        if (a.pre != kNormNone) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * f * q[i][j];
+          if (a.pre_b) {
+            Raw<false> b;
+            b.load(a.pre_b, at[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] += b.get(j);
+          }
+        }
+        store_bf16(a.out + (size_t)row * a.out_ld + at[i], v[i]);
+      }
     }
+    if (next >= a.M) return;
+    row = next;
     if (!ONE) __syncthreads();   // the next row's reductions reuse red
   }
 }
@@ -191,25 +250,35 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(BlockNormArgs p) {
 
 hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t s) {
   const int chunks = a.H >> 3;
-  auto go = [&](auto nc, auto one) {
+  int dev = 0, cus = 0;
+  hipError_t err = hipGetDevice(&dev);
+  if (err == hipSuccess) err = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+  if (err != hipSuccess) return err;
+  auto go = [&](auto nc, auto one, int per_cu) {
     constexpr int NC = decltype(nc)::value;
     constexpr bool ONE = decltype(one)::value;
     const int threads = ONE ? 256 : (chunks + NC * kWave - 1) / (NC * kWave) * kWave;
     const int rows = ONE ? threads / kWave : 1;
-    const unsigned grid = (unsigned)((a.M + rows - 1) / rows < (1 << 16) ? (a.M + rows - 1) / rows : 1 << 16);
-    if (a.y_f32 && a.residual_f32)
-      hipLaunchKernelGGL((block_norm_kernel<NC, true, true, ONE>), dim3(grid), dim3(threads), 0, s, a);
-    else if (a.y_f32)
-      hipLaunchKernelGGL((block_norm_kernel<NC, true, false, ONE>), dim3(grid), dim3(threads), 0, s, a);
-    else if (a.residual_f32)
-      hipLaunchKernelGGL((block_norm_kernel<NC, false, true, ONE>), dim3(grid), dim3(threads), 0, s, a);
-    else
-      hipLaunchKernelGGL((block_norm_kernel<NC, false, false, ONE>), dim3(grid), dim3(threads), 0, s, a);
+    const unsigned grid = (unsigned)std::min((a.M + rows - 1) / rows, cus * per_cu);
+    auto kernel = a.y_f32 ? (a.residual_f32 ? block_norm_kernel<NC, true, true, ONE>
+                                            : block_norm_kernel<NC, true, false, ONE>)
+                          : (a.residual_f32 ? block_norm_kernel<NC, false, true, ONE>
+                                            : block_norm_kernel<NC, false, false, ONE>);
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(threads), 0, s, a);
     return hipGetLastError();
   };
-  if (chunks <= kWave) return go(std::integral_constant<int, 1>{}, std::true_type{});
-  if (chunks <= 1024) return go(std::integral_constant<int, 1>{}, std::false_type{});
-  return go(std::integral_constant<int, 2>{}, std::false_type{});
+  using std::integral_constant;
+  const std::true_type wave{};
+  const std::false_type group{};
+  if (chunks <= kWave) return go(integral_constant<int, 1>{}, wave, 8);
+  if (a.M <= 2 * cus) {   // one or two rows a CU: as many threads as it takes
+    if (chunks <= 1024) return go(integral_constant<int, 1>{}, group, 2);
+    return go(integral_constant<int, 4>{}, group, 2);
+  }
+  if (chunks <= 2 * kWave) return go(integral_constant<int, 2>{}, wave, 4);
+  // 16 waves a CU, twice over
+  if (chunks <= 1024) return go(integral_constant<int, 2>{}, group, 32 / ((chunks + 127) / 128));
+  return go(integral_constant<int, 4>{}, group, 4);
 }
 
 }  // namespace moe

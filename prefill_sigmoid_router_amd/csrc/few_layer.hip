@@ -30,7 +30,7 @@
 
 #include "device_common.h"
 #include "launchers.h"
-#include "route_select.h"
+#include "wave_ops.h"
 
 namespace moe {
 
@@ -44,8 +44,6 @@ constexpr int kGroupRows = 8;         // rows of an expert that an item takes, a
 // Counters, cleared by few_logits_kernel.
 constexpr int kTicket = 0, kDownDone = 1, kUpDone = 2;
 constexpr int kCounters = kUpDone + kFewMaxPicks;
-
-typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
 
 // Two products of bf16 pairs added to c.
 __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
@@ -473,12 +471,12 @@ __device__ __forceinline__ void join_item(const FewArgs& p, FewShared& s, int t,
       b += bf16hi(r);
     }
     if (p.residual_out)
-      *reinterpret_cast<uint32_t*>(p.residual_out + (size_t)t * p.H + h) = pack_bf16x2(a, b);
+      *reinterpret_cast<uint32_t*>(p.residual_out + (size_t)t * p.H + h) = cvt_bf16x2(a, b);
     *reinterpret_cast<float2*>(z + h) = make_float2(a, b);   // read by this thread only
     sq += a * a + b * b;
   }
   if (!p.out) return;
-  sq = wave_sum(sq);
+  sq = wave_sum_f32(sq);
   if (lane == 0) s.sum[wave] = sq;
   __syncthreads();
   float total = 0.0f;
@@ -489,7 +487,7 @@ __device__ __forceinline__ void join_item(const FewArgs& p, FewShared& s, int t,
     const float2 v = *reinterpret_cast<const float2*>(z + h);
     const uint32_t g = *reinterpret_cast<const uint32_t*>(p.norm_w + h);
     *reinterpret_cast<uint32_t*>(p.out + (size_t)t * p.H + h) =
-        pack_bf16x2(v.x * f * bf16lo(g), v.y * f * bf16hi(g));
+        cvt_bf16x2(v.x * f * bf16lo(g), v.y * f * bf16hi(g));
   }
 }
 

@@ -20,43 +20,14 @@
 
 #include "device_common.h"
 #include "launchers.h"
-#include "route_select.h"
 #include "tiled_common.h"
+#include "wave_ops.h"
 
 namespace moe {
 
 namespace {
 
 constexpr int kSelWaves = 4;   // tokens per workgroup: one wave each, no barriers
-
-// The same for floats: largest and sum.
-#define MOE_DPP_F32(v, old, ctrl, rows)                                                       \
-  __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp((int)__float_as_uint(old),            \
-                                                        (int)__float_as_uint(v), ctrl, rows, \
-                                                        0xf, false))
-__device__ __forceinline__ float scan_max_f32(float v) {
-  v = fmaxf(v, MOE_DPP_F32(v, -INFINITY, 0x111, 0xf));
-  v = fmaxf(v, MOE_DPP_F32(v, -INFINITY, 0x112, 0xf));
-  v = fmaxf(v, MOE_DPP_F32(v, -INFINITY, 0x114, 0xf));
-  v = fmaxf(v, MOE_DPP_F32(v, -INFINITY, 0x118, 0xf));
-  v = fmaxf(v, MOE_DPP_F32(v, -INFINITY, 0x142, 0xa));
-  v = fmaxf(v, MOE_DPP_F32(v, -INFINITY, 0x143, 0xc));
-  return v;   // largest of the lanes up to this one
-}
-__device__ __forceinline__ float lane63(float v) {
-  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
-}
-__device__ __forceinline__ float wave_max_f32(float v) { return lane63(scan_max_f32(v)); }
-__device__ __forceinline__ float wave_sum_f32(float v) {
-  v += MOE_DPP_F32(v, 0.0f, 0x111, 0xf);
-  v += MOE_DPP_F32(v, 0.0f, 0x112, 0xf);
-  v += MOE_DPP_F32(v, 0.0f, 0x114, 0xf);
-  v += MOE_DPP_F32(v, 0.0f, 0x118, 0xf);
-  v += MOE_DPP_F32(v, 0.0f, 0x142, 0xa);
-  v += MOE_DPP_F32(v, 0.0f, 0x143, 0xc);
-  return lane63(v);
-}
-#undef MOE_DPP_F32
 
 // fp32 logits with a bound, for many tokens.
 //
