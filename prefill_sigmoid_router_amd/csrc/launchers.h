@@ -255,7 +255,7 @@ struct FewArgs {
   float* w_out;
   // filled in by the launcher
   double* keys;     // logits [M, E]
-  int* sync;        // counters
+  int* ticket;      // of the next work item
   float *act, *y;   // [M top_k, I], [M top_k, H]
   int up_tiles, down_tiles, group_rows;
 };
