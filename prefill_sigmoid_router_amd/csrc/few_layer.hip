@@ -675,6 +675,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   for (int e = tid; e < E; e += kThreads) s.mask[e] = 0;
   lds_barrier();
   for (int t = wave; t < p.M; t += kWaves) {
+    const int lane = thread_here() & 63;
     double* c = reinterpret_cast<double*>(s.stage) + (size_t)wave * E;
     int* ids = s.ids + t * p.top_k;
     if (E <= 64) select_token<1>(p, t, lane, c, ids);
