@@ -526,7 +526,8 @@ int moe_block_norm(const void* y, int32_t y_f32, int64_t y_ld,
  * 16 bytes at a time where N, out_ld and residual_ld are multiples of 8, else one by one.
  * K % 8 == 0, 8 <= K <= 2^20, 1 <= N <= 2^24, 0 <= M <= 2^24, M * N below 2^38 (larger:
  * MOE_ERR_UNSUPPORTED).  workspace of moe_matmul_workspace_bytes bytes (0 for many sizes, then it
- * may be NULL, and for invalid ones), 16-byte aligned.
+ * may be NULL, and for invalid ones), 16-byte aligned.  Few rows with a long K need it, for sums of
+ * parts of K: a smaller M can need more than a larger one.
  */
 enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3, MOE_ACT_GELU_TANH = 4 };
 size_t moe_matmul_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t gated);

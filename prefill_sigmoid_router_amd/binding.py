@@ -728,7 +728,7 @@ def _device_of(t, name: str) -> int:
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device (GPU) tensor")
-    return torch.cuda.current_device()
+    return torch._C._cuda_getDevice()
 
 
 def _arg(device: int, t, name: str, dtype, shape=None):
@@ -894,9 +894,12 @@ FEW_MAX_TOKENS, FEW_MAX_PICKS = 16, 512                                         
 
 def _rows_arg(device: int, t, name: str, dtypes, shape):
     """Address and row stride of a matrix on the current device whose rows may lie apart (a
-    slice of the columns of a wider tensor); 0, 0 for None."""
+    slice of the columns of a wider tensor); None, 0 for None."""
     if t is None:
         return None, 0
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.get_device() == device
+            and t.shape == shape and t.is_contiguous()):
+        return t.data_ptr(), shape[1]
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
@@ -912,7 +915,7 @@ def _rows_arg(device: int, t, name: str, dtypes, shape):
     ld, step = t.stride()
     if (n > 1 and step != 1) or (M > 1 and ld < n):
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
-    return t.data_ptr(), ld if M > 1 else (n + 7) // 8 * 8
+    return t.data_ptr(), ld if M > 1 else n
 
 
 _BF16, _ANY_FLOAT = (torch.bfloat16,), (torch.bfloat16, torch.float32)
@@ -953,7 +956,11 @@ def moe_block_norm(y, residual, out, z_out=None, gate=None, post: int = NORM_NON
         g_at, g_ld = _rows_arg(dev, rows, "gate", _BF16, tuple(rows.shape))
         if rows.shape[0] == 1:
             g_ld = 0
-    vec = lambda t, name: _opt_arg(dev, t, name, torch.bfloat16, (H,))  # noqa: E731
+    row = (H,)
+
+    def vec(t, name):
+        return None if t is None else _arg(dev, t, name, torch.bfloat16, row)
+
     _check("moe_block_norm", load_library().moe_block_norm(
         y_at, _is_f32(y), y_ld, r_at, 1 if rtype is torch.float32 else 0, r_ld, g_at, g_cols, g_ld,
         post, vec(post_w, "post_w"), vec(post_b, "post_b"), pre, vec(pre_w, "pre_w"),

@@ -207,8 +207,13 @@ __device__ __forceinline__ int weight_swizzle(int r) {
 
 // Tiles of BM tokens x 64 WN weight rows (GATED: 32 WN gate and as many up rows), K in chunks
 // of 64.  Both operands are copied global -> LDS in 1 KiB pieces of 8 rows x one line.  A ring of
-// S stages keeps S - 1 chunks in flight; each wave waits for its own copies and a bare barrier
-// publishes them.  Only a partial last chunk goes through registers (zero-filled).
+// S stages keeps S chunks in flight; each wave waits for its own copies and a bare barrier
+// publishes them.  Only a partial last chunk goes through registers (zero-filled).  A chunk's
+// fragments are read while the one before is multiplied (without that a chunk of a 64 x 64 tile took
+// 0.40 us, most of it LDS latency).
+// SPLIT: an item is a tile and one of p.splits parts of K, whose fp32 sums go to p.partial
+// [splits][M][p.partial_ld] (GATED: the up rows' columns behind the gate rows'), where join_kernel
+// adds them in order.
 template <int BM, int WN, int WM>
 struct RingCfg {
   static constexpr int WT = 4 * WN;              // weight row tiles of 16
@@ -230,10 +235,10 @@ __device__ __forceinline__ void wait_after(int after) {
   }
 }
 
-template <int BM, int WN, int WM, int S, bool GATED>
+template <int BM, int WN, int WM, int S, bool GATED, bool SPLIT>
 __global__ __launch_bounds__(64 * WN * WM) void ring_kernel(GemmArgs p) {
   using C = RingCfg<BM, WN, WM>;
-  static_assert((S - 2) * C::PPW <= 63, "the copies in flight must fit the vmcnt counter");
+  static_assert((S - 1) * C::PPW <= 63, "the copies in flight must fit the vmcnt counter");
   static_assert(S * C::PIECES * 1024 <= 160 * 1024, "the ring must fit the LDS");
   __shared__ __align__(16) unsigned char lds[S * C::PIECES * 1024];
   constexpr int SPAN = GATED ? 8 : 16, COLS = GATED ? 32 * WN : 64 * WN;
@@ -241,9 +246,15 @@ __global__ __launch_bounds__(64 * WN * WM) void ring_kernel(GemmArgs p) {
   const int li = lane & 15, lg = lane >> 4;
   const int wn = wave % WN, wm = wave / WN;
   const int K = p.K;
-  TiledWalk walk((p.M + BM - 1) / BM, (p.N + COLS - 1) / COLS);
+  const int all = (K + kKC - 1) / kKC, ndma = K / kKC;   // chunks, whole ones
+  const int ntiles = (p.N + COLS - 1) / COLS;
+  TiledWalk walk((p.M + BM - 1) / BM, SPLIT ? ntiles * p.splits : ntiles);
   int ntile, ti;
   while (walk.next(ntile, ti)) {
+    const int split = SPLIT ? ntile % p.splits : 0;
+    if (SPLIT) ntile /= p.splits;
+    const int first = SPLIT ? (int)((int64_t)all * split / p.splits) : 0;
+    const int nch = SPLIT ? (int)((int64_t)all * (split + 1) / p.splits) : all;
     const int start = ti * BM, nlive = min(BM, p.M - start), col0 = ntile * COLS;
     const int mt_active = (nlive + 15) >> 4;
     // piece f of a chunk: LDS rows 8f .. 8f + 7 (weight rows first); lane l copies slot l % 8
@@ -257,71 +268,121 @@ __global__ __launch_bounds__(64 * WN * WM) void ring_kernel(GemmArgs p) {
         koff[i] = 8 * ((lane & 7) ^ weight_swizzle<SPAN>(lr));
         const bool up = GATED && lr >= 32 * WN;
         const int col = min(col0 + (up ? lr - 32 * WN : lr), p.N - 1);
-        src[i] = p.w + (size_t)(up ? p.N + col : col) * K + koff[i];
+        src[i] = p.w + (size_t)(up ? p.N + col : col) * K + koff[i] + (size_t)first * kKC;
       } else {
         const int r = lr - 64 * WN;
         koff[i] = 8 * ((lane & 7) ^ token_swizzle(r));
-        src[i] = p.x + (size_t)(start + min(r, nlive - 1)) * p.x_ld + koff[i];
+        src[i] = p.x + (size_t)(start + min(r, nlive - 1)) * p.x_ld + koff[i] + (size_t)first * kKC;
       }
     }
-    const int nch = (K + kKC - 1) / kKC, ndma = K / kKC;   // chunks, whole ones
-    auto issue = [&](int c) {
-      unsigned char* base = lds + (size_t)(c % S) * C::PIECES * 1024 + wave * C::PPW * 1024;
-      if (c < ndma) {
+    constexpr int STAGE = C::PIECES * 1024;
+    int put = 0, get = 0;   // stages that the next copy fills, that the next chunk is read from
+    auto copy = [&] {   // the next chunk, a whole one
+      unsigned char* base = lds + put * STAGE + wave * C::PPW * 1024;
+      put = put == S - 1 ? 0 : put + 1;
 #pragma unroll
-        for (int i = 0; i < C::PPW; ++i)
-          __builtin_amdgcn_global_load_lds((global_void*)(src[i] + (size_t)c * kKC),
-                                           (lds_void*)(base + i * 1024), 16, 0, 0);
-      } else {
-#pragma unroll
-        for (int i = 0; i < C::PPW; ++i)
-          *reinterpret_cast<u32x4*>(base + i * 1024 + lane * 16) =
-              c * kKC + koff[i] < K ? ld16(src[i] + (size_t)c * kKC) : u32x4{0, 0, 0, 0};
+      for (int i = 0; i < C::PPW; ++i) {
+        __builtin_amdgcn_global_load_lds((global_void*)src[i], (lds_void*)(base + i * 1024), 16, 0, 0);
+        src[i] += kKC;
       }
     };
+    auto issue = [&](int c) {   // the next chunk, c
+      if (c < ndma) {
+        copy();
+        return;
+      }
+      unsigned char* base = lds + put * STAGE + wave * C::PPW * 1024;
+      put = put == S - 1 ? 0 : put + 1;
+#pragma unroll
+      for (int i = 0; i < C::PPW; ++i)
+        *reinterpret_cast<u32x4*>(base + i * 1024 + lane * 16) =
+            c * kKC + koff[i] < K ? ld16(src[i]) : u32x4{0, 0, 0, 0};
+    };
+    const int my_active = mt_active - wm * C::MTW;
     const int wrow = (GATED ? 32 : 64) * wn + SPAN * (li >> 2) + (li & 3);
-    const int wslot = weight_swizzle<SPAN>(wrow), tslot = token_swizzle(li);
-    auto frag = [&](int c, int row, int slot) -> u32x4 {
-      return *reinterpret_cast<const u32x4*>(lds + (size_t)(c % S) * C::PIECES * 1024 + row * 128 +
-                                             slot * 16);
+    const int waddr = wrow * 128 + 16 * (lg ^ weight_swizzle<SPAN>(wrow));
+    const int taddr = (64 * WN + 16 * C::MTW * wm + li) * 128 + 16 * (lg ^ token_swizzle(li));
+    u32x4 wa[2][2][4], xb[2][2][C::MTW];   // fragments of even and odd chunks, both halves of K
+    auto read = [&](int set) {   // of the next chunk
+      const unsigned char* base = lds + get * STAGE;
+      get = get == S - 1 ? 0 : get + 1;
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {   // half ks: slot lg + 4 ks, that is byte 64 ks flipped
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          wa[set][ks][j] = *reinterpret_cast<const u32x4*>(
+              base + (waddr ^ 64 * ks) + 512 * (GATED ? j & 1 : j) + (GATED ? (j >> 1) * 32 * WN * 128 : 0));
+#pragma unroll
+        for (int s = 0; s < C::MTW; ++s)
+          xb[set][ks][s] = *reinterpret_cast<const u32x4*>(base + (taddr ^ 64 * ks) + 2048 * s);
+      }
     };
     f32x4 acc[4][C::MTW];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int s = 0; s < C::MTW; ++s) acc[j][s] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const int my_active = mt_active - wm * C::MTW;
-#pragma unroll
-    for (int q = 0; q < S - 1; ++q)
-      if (q < nch) issue(q);
-    for (int c = 0; c < nch; ++c) {
-      // this wave's whole chunks issued after c (the tail chunk's loads are complete when
-      // they are stored)
-      wait_after<C::PPW, S - 2>(c < ndma ? min(S - 2, ndma - 1 - c) : 0);
+    // Chunk c has landed, and chunk c - 1 has been read: this wave's whole chunks issued after c
+    // may be in flight (the tail chunk's loads are complete when they are stored).
+    auto landed = [&](int c, int after) {
+      wait_after<C::PPW, S - 1>(c < ndma ? min(after, min(ndma, nch) - 1 - c) : 0);
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      if (c + S - 1 < nch) issue(c + S - 1);
-      if (my_active > 0) {
+    };
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          u32x4 wa[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            wa[j] = frag(c, GATED ? wrow + 4 * (j & 1) + (j >> 1) * 32 * WN : wrow + 4 * j,
-                         (lg + 4 * ks) ^ wslot);
-#pragma unroll
-          for (int s = 0; s < C::MTW; ++s) {
-            if (s < my_active) {
-              const u32x4 xb = frag(c, 64 * WN + 16 * (wm * C::MTW + s) + li, (lg + 4 * ks) ^ tslot);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) acc[j][s] = mfma16x16x32(wa[j], xb, acc[j][s]);
-            }
-          }
-        }
+    for (int q = 0; q < S; ++q)
+      if (first + q < nch) issue(first + q);
+    landed(first, S - 1);
+    read(0);
+    // Chunk c is multiplied while the next one's fragments are read and chunk c + S is copied into
+    // the stage that c has left.  ON: those exist and are whole.
+    auto step = [&](int c, auto parity, auto on) {
+      constexpr int set = decltype(parity)::value;
+      constexpr bool ON = decltype(on)::value;
+      if (ON) {
+        wait_vmcnt<(S - 2) * C::PPW>();
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        copy();
+        read(set ^ 1);
+      } else if (c + 1 < nch) {
+        landed(c + 1, S - 2);
+        if (c + S < nch) issue(c + S);
+        read(set ^ 1);
       }
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int s = 0; s < C::MTW; ++s)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[j][s] = mfma16x16x32(wa[set][ks][j], xb[set][ks][s], acc[j][s]);
+    };
+    const std::integral_constant<int, 0> even{};
+    const std::integral_constant<int, 1> odd{};
+    int c = first;
+#pragma unroll 1
+    for (; c + 1 + S < min(nch, ndma); c += 2) {
+      step(c, even, std::true_type{});
+      step(c + 1, odd, std::true_type{});
+    }
+#pragma unroll 1
+    for (; c < nch; c += 2) {
+      step(c, even, std::false_type{});
+      if (c + 1 < nch) step(c + 1, odd, std::false_type{});
     }
     // lane (li, lg) holds token row li of each token tile and SPAN columns from n0 on
     const int n0 = col0 + (GATED ? 32 : 64) * wn + SPAN * lg;
-    if (n0 < p.N && my_active > 0) {
+    if constexpr (SPLIT) {
+#pragma unroll
+      for (int s = 0; s < C::MTW; ++s) {
+        const int r = 16 * (wm * C::MTW + s) + li;
+        if (r >= nlive || n0 >= p.N) continue;
+        float* dst = p.partial + ((size_t)split * p.M + start + r) * p.partial_ld + n0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float* at = !GATED ? dst + 4 * j : dst + (j >> 1) * (p.partial_ld / 2) + 4 * (j & 1);
+          *reinterpret_cast<f32x4*>(at) = acc[j][s];   // (rows are whole numbers of tiles' columns)
+        }
+      }
+    } else if (n0 < p.N && my_active > 0) {
       float bh[SPAN], bu[SPAN];
       load_bias(p, n0, 0, bh);
       if (GATED) load_bias(p, n0, p.N, bu);
@@ -349,13 +410,67 @@ __global__ __launch_bounds__(64 * WN * WM) void ring_kernel(GemmArgs p) {
   }
 }
 
+// Sums of the parts of K, in order, and the epilogue: 8 columns of a token per thread.
+template <bool GATED>
+__global__ __launch_bounds__(256) void join_kernel(GemmArgs p) {
+  const int groups = (p.N + 7) / 8;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (int64_t)p.M * groups) return;
+  const int m[1] = {(int)(i / groups)}, n = (int)(i % groups) * 8;
+  float h[1][8], u[1][8], bh[8], bu[8];
+  Residual<8> res[1];
+  if (p.residual) res[0].load(p, m[0], n);
+  load_bias(p, n, 0, bh);
+  if (GATED) load_bias(p, n, p.N, bu);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) h[0][q] = u[0][q] = 0.0f;
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s) {
+    const float* src = p.partial + ((size_t)s * p.M + m[0]) * p.partial_ld + n;
+#pragma unroll
+    for (int q = 0; q < 8; q += 4) {
+      const f32x4 a = *reinterpret_cast<const f32x4*>(src + q);
+      f32x4 b = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (GATED) b = *reinterpret_cast<const f32x4*>(src + p.partial_ld / 2 + q);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        h[0][q + e] += a[e];
+        u[0][q + e] += b[e];
+      }
+    }
+  }
+  finish<GATED>(p, m, n, h, u, bh, bu, res);
+}
+
 template <int BM, int WN, int WM, int S, bool GATED>
 hipError_t launch_ring(const GemmArgs& a, hipStream_t s) {
   const int cols = GATED ? 32 * WN : 64 * WN;
   const long items = (long)((a.M + BM - 1) / BM) * ((a.N + cols - 1) / cols);
   const long grid = walk_grid(items, S * RingCfg<BM, WN, WM>::PIECES * 1024);
-  hipLaunchKernelGGL((ring_kernel<BM, WN, WM, S, GATED>), dim3((unsigned)grid), dim3(64 * WN * WM), 0,
-                     s, a);
+  hipLaunchKernelGGL((ring_kernel<BM, WN, WM, S, GATED, false>), dim3((unsigned)grid), dim3(64 * WN * WM),
+                     0, s, a);
+  return hipGetLastError();
+}
+
+// 64 x 64 tiles with K in parts.
+constexpr int kSplitLd = 64;   // rows of partial sums are a multiple of a tile's columns
+int partial_ld(int N, bool gated) {
+  const int cols = gated ? kSplitLd / 2 : kSplitLd;
+  return (N + cols - 1) / cols * kSplitLd;
+}
+template <bool GATED>
+hipError_t launch_split(GemmArgs a, int splits, float* partial, hipStream_t s) {
+  const int cols = GATED ? 32 : 64;
+  a.splits = splits;
+  a.partial = partial;
+  a.partial_ld = partial_ld(a.N, GATED);
+  const long items = (long)((a.M + 63) / 64) * ((a.N + cols - 1) / cols) * splits;
+  const long grid = walk_grid(items, 4 * RingCfg<64, 1, 4>::PIECES * 1024);
+  hipLaunchKernelGGL((ring_kernel<64, 1, 4, 4, GATED, true>), dim3((unsigned)grid), dim3(256), 0, s, a);
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  const int64_t threads = (int64_t)a.M * ((a.N + 7) / 8);
+  hipLaunchKernelGGL((join_kernel<GATED>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -365,7 +480,7 @@ hipError_t launch_ring(const GemmArgs& a, hipStream_t s) {
 // flight.
 template <int MT, bool GATED>
 __global__ __launch_bounds__(512) void skinny_kernel(GemmArgs p, int n_ntiles, int mblocks, int per_xcd) {
-  constexpr int WAVES = 8, BATCH = MT == 1 ? 4 : MT == 2 ? 2 : 1, COLS = GATED ? 8 : 16;
+  constexpr int WAVES = 8, BATCH = MT == 1 ? 4 : 2, COLS = GATED ? 8 : 16;
   __shared__ float part[WAVES][MT][4][kWave];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int li = lane & 15, lg = lane >> 4;
@@ -409,8 +524,8 @@ __global__ __launch_bounds__(512) void skinny_kernel(GemmArgs p, int n_ntiles, i
 #pragma unroll
     for (int q = 0; q < 4; ++q) part[wave][t][q][lane] = acc[t][q];
   __syncthreads();
-  // thread -> token r, column c, with the residual in flight beside the sums: weight row c is result c % 4 of lane 16 (c / 4) + r % 16 of
-  // token tile r / 16
+  // thread -> token r, column c, with the residual in flight beside the sums: weight row c is
+  // result c % 4 of lane 16 (c / 4) + r % 16 of token tile r / 16
   for (int i = threadIdx.x; i < COLS * 16 * MT; i += 64 * WAVES) {
     const int r = i / COLS, c = i % COLS;
     if (m0 + r >= p.M || n0 + c >= p.N) continue;
@@ -721,19 +836,78 @@ hipError_t launch_big(const GemmArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// The variant of a product: the one that these estimates (us, fitted to bf16 results without an
+// epilogue) make the fastest.  A chunk of all the tiles that the 256 CUs hold at once takes
+//   64 x 64      0.20 (one tile per CU), 0.39 (two), 0.45 (two, the operands from HBM)
+//   128 x 128    0.39 (half of the CUs), 0.50, 0.68 (past two rounds of tiles)
+//   256 x 256    1.25 (few tiles) .. 1.60 (all CUs)
+// K in parts fills idle CUs with 64 x 64 tiles, at the price of another launch and of fp32 sums
+// that are written and read.  Measured, 64 x 64 / the best split of it / 128 x 128 / 256 x 256:
+//   M     N     K
+//   40    512   7168    24.3    9.4   43.8    141
+//   160   1024  2048     9.4    8.8   16.5     49
+//   640   2048  2048    14.1   20.3   17.3     50
+//   640   4096  7168    66.7   70.8   47.7    142
+//   2048  2048  2048    38.2   55.2   21.4     52
+//   2048  7168  2048   115.7    187   77.6     60
+//   8192  4096  7168    1052      -    570    371
+// Up to 32 tokens the weights' bytes bound a product, and a workgroup of the few-token variant
+// takes 16 of their rows, so that all CUs read (M = 8, N = 7168, K = 2048: 9 us; 64 x 64: 9.5; at
+// M = 33 13 and 9.4).  Sizes alone decide: a call's workspace does not change its result.
+enum Variant { kSkinny, kTile64, kTile128, kTile256 };
+struct Choice {
+  Variant variant;
+  int splits;   // kTile64: parts of K
+};
+constexpr int kMaxSplits = 16;
+Choice choose(int M, int N, int K, bool gated) {
+  if (M <= 32) return Choice{kSkinny, 1};
+  const double rows = gated ? 2.0 * N : N, chunks = (K + kKC - 1) / kKC;
+  auto tiles = [&](int m, int w) { return ceil((double)M / m) * ceil(rows / w); };
+  Choice best{kTile64, 1};
+  double cost = 1e30;
+  auto offer = [&](Variant v, int splits, double us) {
+    if (us < cost) {
+      cost = us;
+      best = Choice{v, splits};
+    }
+  };
+  const double t64 = tiles(64, 64), t128 = tiles(128, 128), t256 = tiles(256, 256);
+  auto time64 = [&](double items) {   // of a chunk of all of them
+    return items <= 256 ? 0.2 : items <= 512 ? 0.39 : 0.45 * ceil(items / 512);
+  };
+  offer(kTile64, 1, 3.0 + chunks * time64(t64));
+  for (int splits = 2; splits <= kMaxSplits && chunks / splits >= 4; splits *= 2)
+    offer(kTile64, splits, 5.5 + ceil(chunks / splits) * time64(t64 * splits) +
+                               8.0 * splits * M * rows / 3.5e6);   // bytes, at 3.5 TB/s
+  offer(kTile128, 1, 3.0 + chunks * (t128 <= 128 ? 0.39 : (t128 <= 512 ? 0.5 : 0.68) * ceil(t128 / 256)));
+  if (K > kKC) {   // (the stream needs 2 chunks per item)
+    const double full = t256 < 256 ? t256 / 256 : 1.0;
+    offer(kTile256, 1, 5.0 + ceil(t256 / 256) * (chunks * (1.25 + 0.35 * full)) + 12.0 * full);
+  }
+  return best;
+}
+
 template <bool GATED>
-hipError_t launch_sized(const GemmArgs& a, hipStream_t s) {
-  if (a.M <= 16) return launch_skinny<1, GATED>(a, s);
-  if (a.M <= 32) return launch_skinny<2, GATED>(a, s);
-  if (a.M <= 512) return launch_ring<64, 1, 4, 4, GATED>(a, s);
-  if (a.x_ld <= kBigMaxLd && a.K > (kBigMinChunks - 1) * kKC) return launch_big<GATED>(a, s);
-  return launch_ring<128, 4, 2, 3, GATED>(a, s);
+hipError_t launch_sized(const GemmArgs& a, float* partial, hipStream_t s) {
+  const Choice c = choose(a.M, a.N, a.K, GATED);
+  if (c.splits > 1) return launch_split<GATED>(a, c.splits, partial, s);
+  if (c.variant == kSkinny) return a.M <= 16 ? launch_skinny<1, GATED>(a, s) : launch_skinny<2, GATED>(a, s);
+  if (c.variant == kTile64) return launch_ring<64, 1, 4, 4, GATED>(a, s);
+  if (c.variant == kTile256 && a.x_ld <= kBigMaxLd) return launch_big<GATED>(a, s);
+  return launch_ring<128, 2, 4, 5, GATED>(a, s);
 }
 
 }  // namespace
 
-hipError_t launch_bf16_matmul(const GemmArgs& a, hipStream_t s) {
-  return a.gated ? launch_sized<true>(a, s) : launch_sized<false>(a, s);
+size_t bf16_matmul_scratch_bytes(int M, int N, int K, bool gated) {
+  const int splits = choose(M, N, K, gated).splits;
+  return splits > 1 ? (size_t)splits * M * partial_ld(N, gated) * sizeof(float) : 0;
+}
+
+hipError_t launch_bf16_matmul(const GemmArgs& a, void* scratch, hipStream_t s) {
+  float* partial = static_cast<float*>(scratch);
+  return a.gated ? launch_sized<true>(a, partial, s) : launch_sized<false>(a, partial, s);
 }
 
 }  // namespace moe

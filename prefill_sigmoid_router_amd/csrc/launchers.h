@@ -239,8 +239,12 @@ struct GemmArgs {
   int64_t x_ld, residual_ld, out_ld;
   int M, N, K, act, gated, residual_f32, out_f32;
   int wide;   // N, residual_ld and out_ld are multiples of 8: columns 16 bytes at a time
+  // filled in by the launcher: parts of K, and where their sums go
+  int splits, partial_ld;
+  float* partial;
 };
-hipError_t launch_bf16_matmul(const GemmArgs& a, hipStream_t s);
+size_t bf16_matmul_scratch_bytes(int M, int N, int K, bool gated);   // 16-byte aligned
+hipError_t launch_bf16_matmul(const GemmArgs& a, void* scratch, hipStream_t s);
 
 // The layer for a few tokens (few_layer.hip).
 constexpr int kFewMaxTokens = 16, kFewMaxPicks = 512;

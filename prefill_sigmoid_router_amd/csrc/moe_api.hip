@@ -1009,8 +1009,7 @@ int moe_block_norm(const void* y, int32_t y_f32, int64_t y_ld, const void* resid
 }
 
 size_t moe_matmul_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t gated) {
-  if (!gemm_sizes_ok(M, N, K, gated)) return 0;
-  return 0;
+  return gemm_sizes_ok(M, N, K, gated) ? moe::bf16_matmul_scratch_bytes(M, N, K, gated) : 0;
 }
 
 int moe_matmul(const uint16_t* x, int64_t x_ld, const uint16_t* w, const uint16_t* bias, int32_t M,
@@ -1046,7 +1045,7 @@ int moe_matmul(const uint16_t* x, int64_t x_ld, const uint16_t* w, const uint16_
   a.residual_f32 = residual_f32;
   a.out_f32 = out_f32;
   a.wide = N % 8 == 0 && out_ld % 8 == 0 && (!residual || residual_ld % 8 == 0);
-  return hip_status(moe::launch_bf16_matmul(a, (hipStream_t)stream));
+  return hip_status(moe::launch_bf16_matmul(a, workspace, (hipStream_t)stream));
 }
 
 size_t moe_few_workspace_bytes(int32_t M, int32_t H, int32_t E, int32_t I, int32_t top_k) {

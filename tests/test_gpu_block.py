@@ -303,6 +303,49 @@ def test_product_large(B, dev, M, N, K, gated):
     _check_product(B, dev, M, N, K, gated=gated, act="silu" if gated else "none", ot=F32, pad=8)
 
 
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("M,N,K", [(33, 40, 4096), (40, 512, 7168), (77, 65, 2056), (130, 24, 4104), (200, 300, 8256),
+                                   (64, 1, 2048), (1000, 33, 6144)])
+def test_product_in_parts_of_k(B, dev, M, N, K, gated):
+    """Few tiles and a long K: the sums of its parts meet in the workspace (filled with NaN here)."""
+    assert B.moe_matmul_workspace_bytes(M, N, K, gated) > 0
+    _check_product(B, dev, M, N, K, gated=gated)
+    _check_product(B, dev, M, N, K, gated=gated, act="gelu", bias=True, res=BF16, pad=8)
+    _check_product(B, dev, M, N, K, gated=gated, act="silu", bias=True, res=F32, ot=F32, pad=24)
+
+
+def test_product_in_parts_of_k_on_two_streams(B, dev):
+    """Two streams with a workspace each, and graphs that share one and are replayed in turn."""
+    M, N, K = 77, 520, 4104
+    g = _gen(dev, 11)
+    x = [_randn(g, (M, K)) for _ in range(2)]
+    w = [_randn(g, (N, K), 0.05) for _ in range(2)]
+    need = B.moe_matmul_workspace_bytes(M, N, K, False)
+    ws = [torch.full((need,), 0xFF, dtype=torch.uint8, device=dev) for _ in range(2)]
+    want = [torch.empty(M, N, dtype=BF16, device=dev) for _ in range(2)]
+    for i in range(2):
+        B.moe_matmul(x[i], w[i], want[i], workspace=ws[0])
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [torch.zeros_like(t) for t in want]
+    for _ in range(10):
+        for i in range(2):
+            B.moe_matmul(x[i], w[i], got[i], workspace=ws[i], stream=streams[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for i in range(2):
+        with torch.cuda.graph(graphs[i]):
+            B.moe_matmul(x[i], w[i], got[i], workspace=ws[0])
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        ws[0].fill_(0xFF)
+        for q in graphs:
+            q.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 @pytest.mark.parametrize("M,N,K", [(4, 64, 256), (100, 128, 256), (1100, 512, 512)])
 def test_product_onto_the_residual(B, dev, M, N, K):
     g = _gen(dev, 3)
