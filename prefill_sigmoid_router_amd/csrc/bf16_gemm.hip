@@ -474,51 +474,112 @@ hipError_t launch_split(GemmArgs a, int splits, float* partial, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Few tokens: 16 weight rows (GATED: 8 gate and 8 up rows) x 16 MT tokens per workgroup, the
-// 64-wide units of K dealt over its 8 waves, whose sums meet in LDS in a fixed order.  Fragments
-// come straight from memory (a weight row's line is read by one wave), BATCH units at a time in
-// flight.
-template <int MT, bool GATED>
+// Few tokens: 16 weight rows (GATED: 8 gate and 8 up rows) x 8 XP tokens per workgroup, the
+// 64-wide units of K dealt over its 8 waves, whose sums meet in LDS in a fixed order.  A wave copies
+// its units global -> LDS in 1 KiB pieces of 8 rows x one line, two at a time in flight (three to six
+// were no faster: the LDS then holds fewer workgroups), and waits for nobody else's.  Bound by the
+// weights: M = 8, N = 4096, K = 7168 10.8 us (5.4 TB/s), M = 32 11.9.  (Fragments straight from
+// memory, each lane its row's 16 bytes, took 13.5 and 21.4: 64 lines to look up per load.)
+template <int XP, bool GATED>
 __global__ __launch_bounds__(512) void skinny_kernel(GemmArgs p, int n_ntiles, int mblocks, int per_xcd) {
-  constexpr int WAVES = 8, BATCH = MT == 1 ? 4 : 2, COLS = GATED ? 8 : 16;
-  __shared__ float part[WAVES][MT][4][kWave];
+  constexpr int WAVES = 8, AHEAD = 2, COLS = GATED ? 8 : 16, MT = (XP + 1) / 2, PIECES = 2 + XP;
+  constexpr int UNIT = PIECES * 1024;
+  static_assert(WAVES * AHEAD * UNIT <= 160 * 1024, "the units in flight must fit the LDS");
+  static_assert(AHEAD * UNIT >= MT * 1024, "the sums take the units' place");
+  __shared__ __align__(16) unsigned char lds[WAVES * AHEAD * UNIT];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int li = lane & 15, lg = lane >> 4;
   // the token blocks of a weight tile run on one XCD
   const int slot = blockIdx.x / kXcds, item = (blockIdx.x % kXcds) * per_xcd + slot;
   if (slot >= per_xcd || item >= n_ntiles * mblocks) return;
-  const int n0 = item / mblocks * COLS, m0 = item % mblocks * (16 * MT);
+  const int n0 = item / mblocks * COLS, m0 = item % mblocks * (8 * XP);
   const int K = p.K, units = (K + kKC - 1) / kKC, whole = K / kKC;
-  const int col = min(n0 + (GATED ? li & 7 : li), p.N - 1);
-  const uint16_t* wrow = p.w + (size_t)(GATED && li >= 8 ? p.N + col : col) * K + 8 * lg;
-  const uint16_t* trow[MT];
+  // piece f: rows 8f .. 8f + 7 (weight rows first); lane l copies slot l % 8 of row l / 8.  Rows past
+  // the last repeat it; their results are not stored.
+  const uint16_t* src[PIECES];
+  int koff[2];   // of pieces with an even and an odd number
 #pragma unroll
-  for (int t = 0; t < MT; ++t) trow[t] = p.x + (size_t)min(m0 + 16 * t + li, p.M - 1) * p.x_ld + 8 * lg;
+  for (int f = 0; f < 2; ++f) koff[f] = 8 * ((lane & 7) ^ token_swizzle(8 * f + (lane >> 3)));
+#pragma unroll
+  for (int f = 0; f < PIECES; ++f) {
+    const int r = 8 * f + (lane >> 3);
+    if (f < 2) {
+      const bool up = GATED && f == 1;
+      const int col = min(n0 + (up ? r - 8 : r), p.N - 1);
+      src[f] = p.w + (size_t)(up ? p.N + col : col) * K;
+    } else {
+      src[f] = p.x + (size_t)min(m0 + r - 16, p.M - 1) * p.x_ld;
+    }
+    src[f] += koff[f & 1] + wave * kKC;
+  }
+  unsigned char* const ring = lds + wave * AHEAD * UNIT;
+  const int mine = (units - wave + WAVES - 1) / WAVES;         // units wave, wave + WAVES, ...
+  const int mine_whole = (whole - wave + WAVES - 1) / WAVES;   // (0 or 1 fewer)
+  int put = 0, get = 0;
+  auto copy = [&] {   // the next unit, a whole one
+    unsigned char* base = ring + put * UNIT;
+    put = put == AHEAD - 1 ? 0 : put + 1;
+#pragma unroll
+    for (int f = 0; f < PIECES; ++f) {
+      __builtin_amdgcn_global_load_lds((global_void*)src[f], (lds_void*)(base + f * 1024), 16, 0, 0);
+      src[f] += WAVES * kKC;
+    }
+  };
+  auto issue = [&](int i) {   // this wave's unit i
+    if (i < mine_whole) {
+      copy();
+      return;
+    }
+    unsigned char* base = ring + put * UNIT;
+    put = put == AHEAD - 1 ? 0 : put + 1;
+#pragma unroll
+    for (int f = 0; f < PIECES; ++f)
+      *reinterpret_cast<u32x4*>(base + f * 1024 + lane * 16) =
+          whole * kKC + koff[f & 1] < K ? ld16(src[f]) : u32x4{0, 0, 0, 0};
+  };
+  const int row = XP == 1 ? li & 7 : li;
+  const int waddr = li * 128 + 16 * (lg ^ token_swizzle(li));
+  const int xaddr = 2048 + row * 128 + 16 * (lg ^ token_swizzle(row));
   f32x4 acc[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int u0 = wave; u0 < units; u0 += WAVES * BATCH) {
-    u32x4 w[BATCH][2], x[BATCH][MT][2];
+  u32x4 w[2], x[2][MT];
+  auto read = [&] {
+    const unsigned char* base = ring + get * UNIT;
+    get = get == AHEAD - 1 ? 0 : get + 1;
 #pragma unroll
-    for (int b = 0; b < BATCH; ++b) {
-      const int u = u0 + WAVES * b;
+    for (int h = 0; h < 2; ++h) {
+      w[h] = *reinterpret_cast<const u32x4*>(base + (waddr ^ 64 * h));
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        // behind column K zeros meet zeros
-        const bool in = u < whole || (u < units && u * kKC + 32 * h + 8 * lg < K);
-        const size_t off = (size_t)u * kKC + 32 * h;
-        w[b][h] = in ? ld16(wrow + off) : u32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int t = 0; t < MT; ++t) x[b][t][h] = in ? ld16(trow[t] + off) : u32x4{0, 0, 0, 0};
-      }
+      for (int t = 0; t < MT; ++t) x[h][t] = *reinterpret_cast<const u32x4*>(base + (xaddr ^ 64 * h) + 2048 * t);
     }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the slot can be filled again
+  };
+  auto multiply = [&] {
 #pragma unroll
-    for (int b = 0; b < BATCH; ++b)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int t = 0; t < MT; ++t) acc[t] = mfma16x16x32(w[h], x[h][t], acc[t]);
+  };
 #pragma unroll
-        for (int t = 0; t < MT; ++t) acc[t] = mfma16x16x32(w[b][h], x[b][t][h], acc[t]);
+  for (int q = 0; q < AHEAD; ++q)
+    if (q < mine) issue(q);
+  int i = 0;
+  for (; i + AHEAD < mine_whole; ++i) {
+    wait_vmcnt<(AHEAD - 1) * PIECES>();
+    read();
+    copy();
+    multiply();
   }
+  for (; i < mine; ++i) {   // (a partial unit's loads are complete when they are stored)
+    wait_after<PIECES, AHEAD - 1>(i < mine_whole ? min(AHEAD, mine_whole - i) - 1 : 0);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    read();
+    if (i + AHEAD < mine) issue(i + AHEAD);
+    multiply();
+  }
+  __syncthreads();
+  auto part = reinterpret_cast<float(*)[MT][4][kWave]>(lds);
 #pragma unroll
   for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -526,7 +587,7 @@ __global__ __launch_bounds__(512) void skinny_kernel(GemmArgs p, int n_ntiles, i
   __syncthreads();
   // thread -> token r, column c, with the residual in flight beside the sums: weight row c is
   // result c % 4 of lane 16 (c / 4) + r % 16 of token tile r / 16
-  for (int i = threadIdx.x; i < COLS * 16 * MT; i += 64 * WAVES) {
+  for (int i = threadIdx.x; i < COLS * 8 * XP; i += 64 * WAVES) {
     const int r = i / COLS, c = i % COLS;
     if (m0 + r >= p.M || n0 + c >= p.N) continue;
     const int n = n0 + c;
@@ -548,12 +609,12 @@ __global__ __launch_bounds__(512) void skinny_kernel(GemmArgs p, int n_ntiles, i
   }
 }
 
-template <int MT, bool GATED>
+template <int XP, bool GATED>
 hipError_t launch_skinny(const GemmArgs& a, hipStream_t s) {
   const int n_ntiles = (a.N + (GATED ? 7 : 15)) / (GATED ? 8 : 16);
-  const int mblocks = (a.M + 16 * MT - 1) / (16 * MT);
+  const int mblocks = (a.M + 8 * XP - 1) / (8 * XP);
   const int64_t per_xcd = ((int64_t)n_ntiles * mblocks + kXcds - 1) / kXcds;
-  hipLaunchKernelGGL((skinny_kernel<MT, GATED>), dim3((unsigned)(per_xcd * kXcds)), dim3(512), 0, s, a,
+  hipLaunchKernelGGL((skinny_kernel<XP, GATED>), dim3((unsigned)(per_xcd * kXcds)), dim3(512), 0, s, a,
                      n_ntiles, mblocks, (int)per_xcd);
   return hipGetLastError();
 }
@@ -841,19 +902,22 @@ hipError_t launch_big(const GemmArgs& a, hipStream_t s) {
 //   64 x 64      0.20 (one tile per CU), 0.39 (two), 0.45 (two, the operands from HBM)
 //   128 x 128    0.39 (half of the CUs), 0.50, 0.68 (past two rounds of tiles)
 //   256 x 256    1.25 (few tiles) .. 1.60 (all CUs)
+//   32 x 16      0.07 (the few-token variant)
 // K in parts fills idle CUs with 64 x 64 tiles, at the price of another launch and of fp32 sums
-// that are written and read.  Measured, 64 x 64 / the best split of it / 128 x 128 / 256 x 256:
+// that are written and read.  Measured, 32 x 16 / 64 x 64 / the best split of it / 128 x 128 /
+// 256 x 256:
 //   M     N     K
-//   40    512   7168    24.3    9.4   43.8    141
-//   160   1024  2048     9.4    8.8   16.5     49
-//   640   2048  2048    14.1   20.3   17.3     50
-//   640   4096  7168    66.7   70.8   47.7    142
-//   2048  2048  2048    38.2   55.2   21.4     52
-//   2048  7168  2048   115.7    187   77.6     60
-//   8192  4096  7168    1052      -    570    371
-// Up to 32 tokens the weights' bytes bound a product, and a workgroup of the few-token variant
-// takes 16 of their rows, so that all CUs read (M = 8, N = 7168, K = 2048: 9 us; 64 x 64: 9.5; at
-// M = 33 13 and 9.4).  Sizes alone decide: a call's workspace does not change its result.
+//   33    1024  2048     4.2    9.2    7.1   15.8     48
+//   64    512   7168     9.6   24.2    9.6   43.9    141
+//   40    4096  7168    18.5   24.5   15.4   43.5    141
+//   160   1024  2048     7.3    9.3    8.8   16.4     49
+//   640   2048  2048    35.9   13.8   20.1   17.2     50
+//   640   4096  7168     218   64.4   69.8   47.0    142
+//   2048  2048  2048     152   37.8   54.6   22.1     51
+//   2048  7168  2048     504    116    187   77.7     61
+//   8192  4096  7168    3845   1040   1118    567    373
+// Up to 32 tokens the few-token variant takes one block of tokens, and no other was faster by more
+// than 5 %.  Sizes alone decide: a call's workspace does not change its result.
 enum Variant { kSkinny, kTile64, kTile128, kTile256 };
 struct Choice {
   Variant variant;
@@ -872,6 +936,7 @@ Choice choose(int M, int N, int K, bool gated) {
       best = Choice{v, splits};
     }
   };
+  offer(kSkinny, 1, 1.3 + ceil(tiles(32, 16) / 256) * (1.0 + 0.07 * chunks));
   const double t64 = tiles(64, 64), t128 = tiles(128, 128), t256 = tiles(256, 256);
   auto time64 = [&](double items) {   // of a chunk of all of them
     return items <= 256 ? 0.2 : items <= 512 ? 0.39 : 0.45 * ceil(items / 512);
@@ -892,7 +957,10 @@ template <bool GATED>
 hipError_t launch_sized(const GemmArgs& a, float* partial, hipStream_t s) {
   const Choice c = choose(a.M, a.N, a.K, GATED);
   if (c.splits > 1) return launch_split<GATED>(a, c.splits, partial, s);
-  if (c.variant == kSkinny) return a.M <= 16 ? launch_skinny<1, GATED>(a, s) : launch_skinny<2, GATED>(a, s);
+  if (c.variant == kSkinny)
+    return a.M <= 8    ? launch_skinny<1, GATED>(a, s)
+           : a.M <= 16 ? launch_skinny<2, GATED>(a, s)
+                       : launch_skinny<4, GATED>(a, s);
   if (c.variant == kTile64) return launch_ring<64, 1, 4, 4, GATED>(a, s);
   if (c.variant == kTile256 && a.x_ld <= kBigMaxLd) return launch_big<GATED>(a, s);
   return launch_ring<128, 2, 4, 5, GATED>(a, s);

@@ -305,10 +305,9 @@ def test_product_large(B, dev, M, N, K, gated):
 
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("M,N,K", [(33, 40, 4096), (40, 512, 7168), (77, 65, 2056), (130, 24, 4104), (200, 300, 8256),
-                                   (64, 1, 2048), (1000, 33, 6144)])
+                                   (64, 1, 2048), (1000, 33, 6144), (77, 4099, 7168), (200, 1024, 8192)])
 def test_product_in_parts_of_k(B, dev, M, N, K, gated):
     """Few tiles and a long K: the sums of its parts meet in the workspace (filled with NaN here)."""
-    assert B.moe_matmul_workspace_bytes(M, N, K, gated) > 0
     _check_product(B, dev, M, N, K, gated=gated)
     _check_product(B, dev, M, N, K, gated=gated, act="gelu", bias=True, res=BF16, pad=8)
     _check_product(B, dev, M, N, K, gated=gated, act="silu", bias=True, res=F32, ot=F32, pad=24)
@@ -316,7 +315,8 @@ def test_product_in_parts_of_k(B, dev, M, N, K, gated):
 
 def test_product_in_parts_of_k_on_two_streams(B, dev):
     """Two streams with a workspace each, and graphs that share one and are replayed in turn."""
-    M, N, K = 77, 520, 4104
+    M, N, K = 200, 1024, 8200
+    assert B.moe_matmul_workspace_bytes(M, N, K, False) > 0
     g = _gen(dev, 11)
     x = [_randn(g, (M, K)) for _ in range(2)]
     w = [_randn(g, (N, K), 0.05) for _ in range(2)]
