@@ -137,11 +137,12 @@ struct Residual {
 };
 
 // C results each of R tokens m (those from p.M on are left out), columns n ..: sums h (of the gate
-// rows) and u (of the up rows, GATED), and what is added to them.
-template <bool GATED, int R, int C>
+// rows) and u (of the up rows, GATED), and what is added to them.  before_stores issues loads for
+// later: issued behind the stores they would wait for them.
+template <bool GATED, int R, int C, class F>
 __device__ __forceinline__ void finish(const GemmArgs& p, const int (&m)[R], int n, float (&h)[R][C],
                                        float (&u)[R][C], const float (&bh)[C], const float (&bu)[C],
-                                       const Residual<C> (&res)[R]) {
+                                       const Residual<C> (&res)[R], F before_stores) {
   if (p.bias) {
 #pragma unroll
     for (int k = 0; k < R; ++k)
@@ -162,6 +163,7 @@ __device__ __forceinline__ void finish(const GemmArgs& p, const int (&m)[R], int
 #pragma unroll
     for (int k = 0; k < R; ++k) res[k].add(p, n, h[k]);
   }
+  before_stores();
   if (wide_at<C>(p, n)) {
 #pragma unroll
     for (int k = 0; k < R; ++k) {
@@ -404,7 +406,7 @@ __global__ __launch_bounds__(64 * WN * WM) void ring_kernel(GemmArgs p) {
           u[s][q] = GATED ? acc[2 + (q >> 2 & 1)][s][q & 3] : 0.0f;
         }
       }
-      finish<GATED>(p, m, n0, h, u, bh, bu, res);
+      finish<GATED>(p, m, n0, h, u, bh, bu, res, [] {});
     }
     __syncthreads();   // the next item's first copies reuse the ring
   }
@@ -439,7 +441,7 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs p) {
       }
     }
   }
-  finish<GATED>(p, m, n, h, u, bh, bu, res);
+  finish<GATED>(p, m, n, h, u, bh, bu, res, [] {});
 }
 
 template <int BM, int WN, int WM, int S, bool GATED>
@@ -747,6 +749,7 @@ __device__ __forceinline__ void big_products(const GemmArgs& p, unsigned char* l
   // 16-byte slots XORed with the row; then 8 columns of a row per thread, whole lines of a row
   // together, the residuals of the next four rows in flight.
   constexpr int G = GATED ? 16 : 32, ROWS = 256 / G, PASSES = 64 / ROWS;   // threads of a row, rows of a pass
+  constexpr int R = 4;   // rows of a thread at a time
   auto barrier = [&] { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
   auto results = [&](unsigned char* low, unsigned char* high, int m0, int n0) {
     int tid = threadIdx.x;   // (addresses are computed here, not held through the item's loop)
@@ -758,15 +761,15 @@ __device__ __forceinline__ void big_products(const GemmArgs& p, unsigned char* l
     load_bias(p, min(n, p.N - 1), 0, bh);
     if (GATED) load_bias(p, min(n, p.N - 1), p.N, bu);
     auto token = [&](int g, int k) {   // row k of this thread's four in group g of passes
-      const int lr = (g * 4 + k) % PASSES * ROWS + row0;
-      return m0 + 128 * (lr >> 5) + 32 * (g * 4 / PASSES) + (lr & 31);
+      const int lr = (g * R + k) % PASSES * ROWS + row0;
+      return m0 + 128 * (lr >> 5) + 32 * (g * R / PASSES) + (lr & 31);
     };
-    Residual<8> res[4];
+    Residual<8> res[R];
     auto fetch = [&](int g, int k) {
       if (p.residual && on && token(g, k) < p.M) res[k].load(p, token(g, k), n);
     };
 #pragma unroll
-    for (int k = 0; k < 4; ++k) fetch(0, k);
+    for (int k = 0; k < R; ++k) fetch(0, k);
 #pragma unroll
     for (int ph = 0; ph < 4; ++ph) {
       unsigned char* const mine = (wm ? high : low) + r * 1024;
@@ -783,11 +786,11 @@ __device__ __forceinline__ void big_products(const GemmArgs& p, unsigned char* l
       }
       barrier();
 #pragma unroll 1
-      for (int g = ph * (PASSES / 4); g < (ph + 1) * (PASSES / 4); ++g) {
-        float v[4][8], u[4][8];
+      for (int g = ph * (PASSES / R); g < (ph + 1) * (PASSES / R); ++g) {
+        float v[R][8], u[R][8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int lr = (g * 4 + k) % PASSES * ROWS + row0;
+        for (int k = 0; k < R; ++k) {
+          const int lr = (g * R + k) % PASSES * ROWS + row0;
           const unsigned char* src = (lr & 32 ? high : low) + (lr & 31) * 1024;
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
@@ -801,14 +804,15 @@ __device__ __forceinline__ void big_products(const GemmArgs& p, unsigned char* l
             }
           }
         }
-        int m[4];
+        int m[R];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) m[k] = on ? token(g, k) : p.M;
-        finish<GATED>(p, m, n, v, u, bh, bu, res);
-        if (g + 1 < PASSES) {
+        for (int k = 0; k < R; ++k) m[k] = on ? token(g, k) : p.M;
+        finish<GATED>(p, m, n, v, u, bh, bu, res, [&] {
+          if (g + 1 < 4 * PASSES / R) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) fetch(g + 1, k);
-        }
+            for (int k = 0; k < R; ++k) fetch(g + 1, k);
+          }
+        });
       }
       barrier();
     }

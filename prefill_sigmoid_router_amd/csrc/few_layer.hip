@@ -802,11 +802,8 @@ hipError_t launch_few_layer(FewArgs a, void* scratch, hipStream_t s) {
   const long groups = std::min((long)a.M * a.top_k, (long)a.E);
   auto up = [&](int rg) { return (a.I + 32 * rg - 1) / (32 * rg); };
   auto down = [&](int rg) { return (a.H + 64 * rg - 1) / (64 * rg); };
-#ifndef DOWN_PER
-#define DOWN_PER 2
-#endif
   const int urg = groups * up(4) >= cus ? 4 : groups * up(2) >= cus ? 2 : 1;
-  const int drg = groups * down(4) >= DOWN_PER * cus ? 4 : groups * down(2) >= DOWN_PER * cus ? 2 : 1;
+  const int drg = groups * down(4) >= 2 * cus ? 4 : groups * down(2) >= 2 * cus ? 2 : 1;
   a.up_tiles = up(urg);
   a.down_tiles = down(drg);
   const long most = (long)a.M * a.top_k * std::max(a.up_tiles, a.down_tiles);
