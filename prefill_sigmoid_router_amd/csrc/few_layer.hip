@@ -7,8 +7,8 @@
 // from by a ticket: all up items, then all down items, then one item per token that joins its
 // picks.  Every workgroup first selects the experts of all tokens for itself (a wave per token)
 // and lists the touched experts with their rows; that costs less than a hand-over would.
-//   up    act[i, c] = silu(x . W13[e, c]) * (x . W13[e, I + c]) for 32 URG columns of an expert
-//   down  y[i, h] = act[i] . W2[e, h] for 64 DRG of its rows
+//   up    act[i, c] = silu(x . W13[e, c]) * (x . W13[e, I + c]) for 32 columns of an expert (URG = 2: 64)
+//   down  y[i, h] = act[i] . W2[e, h] for 64 of its rows (DRG = 2: 128)
 //   join  z = sum_j w_j y[t k + j] + residual, out = z * (mean z^2 + eps)^-1/2 * norm_w
 // At a few tokens an expert has few rows, so the layer is a stream of its weights (M=8, H=7168,
 // I=2048, k=16: 9 GB) and the arithmetic is small: no LDS ring and no MFMA tile, but dot
@@ -385,7 +385,7 @@ __device__ __forceinline__ void weigh_token(const FewArgs& p, int t, int lane, c
 // exact.  UB units are in flight.
 template <int RG, int TT, bool F32>
 struct Stream {
-  static constexpr int UB = F32 ? (RG == 4 ? 4 : RG == 2 ? 8 : 16) : (RG == 4 ? 6 : RG == 2 ? 12 : 16);
+  static constexpr int UB = RG == 1 ? 16 : F32 ? 8 : 12;
   const uint16_t* row[RG];
   u32x4 w[UB][RG];
   int K, part;
@@ -798,19 +798,24 @@ hipError_t launch_few_layer(FewArgs a, void* scratch, hipStream_t s) {
   err = hipGetDevice(&dev);
   if (err == hipSuccess) err = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
   if (err != hipSuccess) return err;
-  // the widest items that leave every CU some
+  // Two groups of 8 rows per wave where an expert has several rows (4 picks per expert on average) and
+  // every CU still gets an item: each read of a token's values from LDS then serves both.  16 tokens,
+  // 8 of 16 experts, H = 7168, I = 2048: 351 us, one group 410; 2 of 4 experts, H = I = 4096: 136 and
+  // 150.  With few rows per expert small items spread better: 3 tokens, 6 of 64 experts, H = 4096,
+  // I = 1536: 105 us, two groups 114; one token, 4 of 60, H = 2048, I = 1408: 26.6 and 33.4.  (Four
+  // groups were never faster.)
   const long groups = std::min((long)a.M * a.top_k, (long)a.E);
+  const bool shared = (long)a.M * a.top_k >= 4L * a.E;
   auto up = [&](int rg) { return (a.I + 32 * rg - 1) / (32 * rg); };
   auto down = [&](int rg) { return (a.H + 64 * rg - 1) / (64 * rg); };
-  const int urg = groups * up(4) >= cus ? 4 : groups * up(2) >= cus ? 2 : 1;
-  const int drg = groups * down(4) >= 2 * cus ? 4 : groups * down(2) >= 2 * cus ? 2 : 1;
+  const int urg = shared && groups * up(2) >= cus ? 2 : 1;
+  const int drg = shared && groups * down(2) >= cus ? 2 : 1;
   a.up_tiles = up(urg);
   a.down_tiles = down(drg);
   const long most = (long)a.M * a.top_k * std::max(a.up_tiles, a.down_tiles);
   const dim3 grid((unsigned)std::min<long>(cus, std::max<long>(most, a.M))), t(kThreads);
-  auto kernel = urg == 4   ? (drg == 4 ? few_layer_kernel<4, 4> : drg == 2 ? few_layer_kernel<4, 2> : few_layer_kernel<4, 1>)
-                : urg == 2 ? (drg == 4 ? few_layer_kernel<2, 4> : drg == 2 ? few_layer_kernel<2, 2> : few_layer_kernel<2, 1>)
-                           : (drg == 4 ? few_layer_kernel<1, 4> : drg == 2 ? few_layer_kernel<1, 2> : few_layer_kernel<1, 1>);
+  auto kernel = urg == 2 ? (drg == 2 ? few_layer_kernel<2, 2> : few_layer_kernel<2, 1>)
+                         : (drg == 2 ? few_layer_kernel<1, 2> : few_layer_kernel<1, 1>);
   hipLaunchKernelGGL(kernel, grid, t, 0, s, a);
   return hipGetLastError();
 }
