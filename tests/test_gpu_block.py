@@ -359,6 +359,38 @@ def test_product_onto_the_residual(B, dev, M, N, K):
         assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("M,N,K,ld", [(3, 64, 72, (1 << 31) + 64), (40, 512, 2056, 1 << 27), (300, 1024, 328, 1 << 24),
+                                      (1000, 4104, 1032, (1 << 23) + 8), (2048, 7168, 520, 1 << 23),
+                                      (2048, 7168, 520, (1 << 23) + 8)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_product_offsets_past_32_bits(B, dev, M, N, K, ld, gated):
+    """Rows of x, residual and out whose offsets in values pass 2^32 (out over the residual).  The stride
+    may choose another order of sums, so both results are within a product's bound of the exact one."""
+    g = _gen(dev, 9)
+    rows = 2 * N if gated else N
+    x, w, r = _randn(g, (M, K)), _randn(g, (rows, K), 0.05), _randn(g, (M, N))
+    want = torch.empty(M, N, dtype=BF16, device=dev)
+    ws = torch.empty(max(1, B.moe_matmul_workspace_bytes(M, N, K, gated)), dtype=torch.uint8, device=dev)
+    act = dict(act=B.ACT_RELU, gated=True) if gated else {}
+    B.moe_matmul(x, w, want, residual=r, workspace=ws, **act)
+    flat = torch.empty(M * ld, dtype=BF16, device=dev)
+    far_x, far_r = flat.as_strided((M, K), (ld, 1)), flat.as_strided((M, N), (ld, 1), 4096)
+    far_x.copy_(x)
+    far_r.copy_(r)
+    B.moe_matmul(far_x, w, far_r, residual=far_r, workspace=ws, **act)
+    torch.cuda.synchronize()
+    xs, wd = x.double(), w.double().T.contiguous()
+    err = (40 + K / 32) * 2 * U * (xs.abs() @ wd.abs())
+    if gated:
+        h = xs @ wd
+        a, ea, u, eu = h[:, :N].clamp(min=0.0), err[:, :N], h[:, N:], err[:, N:]
+        err = ea * u.abs() + a * eu + ea * eu + 2 * U * (a * u).abs()
+    err = 2 * (err + U * (want.double().abs() + r.double().abs() + err))
+    top = torch.maximum(want.double().abs(), far_r.double().abs()) + err
+    assert ((want.double() - far_r.double()).abs() <= err + 2 * _round(BF16) * top).all()
+    assert torch.equal(far_x, x)
+
+
 @pytest.mark.parametrize("M,N,K", [(5, 72, 264), (70, 200, 328), (1100, 520, 1096)])
 def test_product_keeps_rows_apart(B, dev, M, N, K):
     """A token or a weight row that is not finite changes its own row or column only."""
