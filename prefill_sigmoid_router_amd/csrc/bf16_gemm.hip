@@ -626,6 +626,8 @@ hipError_t launch_skinny(const GemmArgs& a, hipStream_t s) {
 // accumulation registers: fragment reads then take half of the LDS's rate (8 waves of 64 x 128:
 // three quarters, and with the copies' writes all of it).
 //
+// 8192 x 2 x 2048 x 7168, gated: 377 us (1.28 PFLOP/s; a library product of the same sizes without
+// the epilogue 375), MFMAs busy 62 % of the time at 1.9 GHz.
 // K in chunks of 64, a panel of 256 weight rows and one of 256 token rows each, in a ring of five
 // LDS slots of 32 KiB: two of the present chunk, two of the next, one more.  A chunk is 4 steps of
 // 16 values; a step's 16 MFMAs run on one of two sets of fragment registers while the next step's

@@ -9,6 +9,9 @@
 // unrounded z).  The mean of squared distances is taken around each wave's own mean and moved
 // to the row's (Chan's pairwise formula: n_w (mean_w - mean)^2 more), so a row whose mean is
 // far above its spread loses nothing, and a LAYER norm costs one barrier as an RMS norm does.
+// Bound by memory where there are many rows: 8192 x 7168, bf16, RMS twice and a gate per channel (470
+// MB) takes 91 to 97 us, 4.8 to 5.1 TB/s, where a large copy reaches 4.9.  One row of 7168 takes 4.4
+// us: a launch, a load and two reductions.
 #include <algorithm>
 #include <type_traits>
 
@@ -270,15 +273,19 @@ hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t s) {
   using std::integral_constant;
   const std::true_type wave{};
   const std::false_type group{};
+  // Measured with RMS twice and a channel gate, us.  A wave per row, no barriers, where it holds the
+  // row: H = 512, M = 8192 9.4 (a workgroup per row 11.5); H = 1024, M = 8192 13.1 (15.8).
   if (chunks <= kWave) return go(integral_constant<int, 1>{}, wave, 8);
-  if (a.M <= 2 * cus) {   // one or two rows a CU: as many threads as it takes
-    if (chunks <= 1024) return go(integral_constant<int, 1>{}, group, 2);
-    return go(integral_constant<int, 4>{}, group, 2);
-  }
+  // Long rows, two workgroups a CU: H = 16384, M = 1024 31.4 (four 40.6), M = 8192 203 (200).
+  if (chunks > 1024) return go(integral_constant<int, 4>{}, group, 2);
+  // One or two rows a CU, as many threads as it takes: H = 2048, M = 256 3.7 (two chunks a thread
+  // 4.3); H = 7168, M = 8 4.5 (4.8).
+  if (a.M <= 2 * cus) return go(integral_constant<int, 1>{}, group, 2);
+  // Many rows, two chunks a thread, 16 waves a CU twice over: H = 2048, M = 8192 28.7 (one chunk
+  // 33.6); H = 7168, M = 1024 16.7 (18.0), M = 8192 91 to 97 (95; a workgroup for each row that reads
+  // what belongs to the channels anew 190).
   if (chunks <= 2 * kWave) return go(integral_constant<int, 2>{}, wave, 4);
-  // 16 waves a CU, twice over
-  if (chunks <= 1024) return go(integral_constant<int, 2>{}, group, 32 / ((chunks + 127) / 128));
-  return go(integral_constant<int, 4>{}, group, 4);
+  return go(integral_constant<int, 2>{}, group, 32 / ((chunks + 127) / 128));
 }
 
 }  // namespace moe

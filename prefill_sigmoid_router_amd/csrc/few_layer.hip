@@ -14,7 +14,9 @@
 // I=2048, k=16: 9 GB) and the arithmetic is small: no LDS ring and no MFMA tile, but dot
 // products straight from the load registers.  A load is 8 weight rows x one 128-byte line,
 // nontemporal; a wave keeps 16 to 24 KiB of them in flight and runs on by itself, without a
-// barrier, to the end of its rows.  The tokens' rows (x in bf16, act in fp32) lie in LDS.  act and
+// barrier, to the end of its rows: M=8 1.25 to 1.39 ms from box to box (6.5 to 7.3 TB/s, the rate of
+// a plain read), M=1 224 us (6.3).  Small layers are a chain of latencies: H=2048, I=1408, 4 of 60
+// experts, one token 26.5 us, of which 10 are its bytes.  The tokens' rows (x in bf16, act in fp32) lie in LDS.  act and
 // y stay in fp32 at all times, so the layer rounds only its outputs.
 //
 // Hand-overs: act and y are written and read past the XCDs' L2s (agent-scope accesses) and carry
