@@ -426,7 +426,7 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs p) {
   if (GATED) load_bias(p, n, p.N, bu);
 #pragma unroll
   for (int q = 0; q < 8; ++q) h[0][q] = u[0][q] = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
   for (int s = 0; s < p.splits; ++s) {
     const float* src = p.partial + ((size_t)s * p.M + m[0]) * p.partial_ld + n;
 #pragma unroll
@@ -905,7 +905,7 @@ hipError_t launch_big(const GemmArgs& a, hipStream_t s) {
 
 // The variant of a product: the one that these estimates (us, fitted to bf16 results without an
 // epilogue) make the fastest.  A chunk of all the tiles that the 256 CUs hold at once takes
-//   64 x 64      0.20 (one tile per CU), 0.39 (two), 0.45 (two, the operands from HBM)
+//   64 x 64      0.20 (one tile per CU), 0.42 (two), more by the tile
 //   128 x 128    0.39 (half of the CUs), 0.50, 0.68 (past two rounds of tiles)
 //   256 x 256    1.25 (few tiles) .. 1.60 (all CUs)
 //   32 x 16      0.07 (the few-token variant)
@@ -922,8 +922,9 @@ hipError_t launch_big(const GemmArgs& a, hipStream_t s) {
 //   2048  2048  2048     152   37.8   54.6   22.1     51
 //   2048  7168  2048     504    116    187   77.7     61
 //   8192  4096  7168    3845   1040   1118    567    373
-// Up to 32 tokens the few-token variant takes one block of tokens, and no other was faster by more
-// than 5 %.  Sizes alone decide: a call's workspace does not change its result.
+// At 128 sizes (M 40 to 8192, N 64 to 7168, K 768 to 7168, gated and not) the pick was within 10 % of
+// the fastest at all but five, the worst 22 %.  Up to 32 tokens the few-token variant takes one block
+// of tokens, and no other was faster by more than 5 %.  Sizes alone decide: a call's workspace does not change its result.
 enum Variant { kSkinny, kTile64, kTile128, kTile256 };
 struct Choice {
   Variant variant;
@@ -942,19 +943,19 @@ Choice choose(int M, int N, int K, bool gated) {
       best = Choice{v, splits};
     }
   };
-  offer(kSkinny, 1, 1.3 + ceil(tiles(32, 16) / 256) * (1.0 + 0.07 * chunks));
+  offer(kSkinny, 1, ceil(tiles(32, 16) / 256) * (2.1 + 0.07 * chunks));
   const double t64 = tiles(64, 64), t128 = tiles(128, 128), t256 = tiles(256, 256);
   auto time64 = [&](double items) {   // of a chunk of all of them
-    return items <= 256 ? 0.2 : items <= 512 ? 0.39 : 0.45 * ceil(items / 512);
+    return items <= 256 ? 0.2 : items <= 512 ? 0.42 : 0.00108 * items;
   };
   offer(kTile64, 1, 3.0 + chunks * time64(t64));
   for (int splits = 2; splits <= kMaxSplits && chunks / splits >= 4; splits *= 2)
-    offer(kTile64, splits, 5.5 + ceil(chunks / splits) * time64(t64 * splits) +
-                               8.0 * splits * M * rows / 3.5e6);   // bytes, at 3.5 TB/s
-  offer(kTile128, 1, 3.0 + chunks * (t128 <= 128 ? 0.39 : (t128 <= 512 ? 0.5 : 0.68) * ceil(t128 / 256)));
+    offer(kTile64, splits, (gated ? 7.5 : 5.5) + 0.15 * splits + ceil(chunks / splits) * time64(t64 * splits) +
+                               8.0 * splits * M * rows / 3.5e6);   // (bytes, at 3.5 TB/s)
+  offer(kTile128, 1, 3.0 + ceil(t128 / 256) * (2.0 + chunks * (t128 <= 128 ? 0.39 : t128 <= 512 ? 0.5 : 0.68)));
   if (K > kKC) {   // (the stream needs 2 chunks per item)
     const double full = t256 < 256 ? t256 / 256 : 1.0;
-    offer(kTile256, 1, 5.0 + ceil(t256 / 256) * (chunks * (1.25 + 0.35 * full)) + 12.0 * full);
+    offer(kTile256, 1, 5.0 + ceil(t256 / 256) * chunks * (1.25 + 0.35 * full * full * full) + 12.0 * full);
   }
   return best;
 }
