@@ -728,7 +728,7 @@ def _device_of(t, name: str) -> int:
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device (GPU) tensor")
-    return torch._C._cuda_getDevice()
+    return torch.cuda.current_device()
 
 
 def _arg(device: int, t, name: str, dtype, shape=None):
