@@ -496,6 +496,13 @@ def test_few_sizes(B, dev, M, H, E, I, k):
     _check_few(B, dev, M, H, E, I, k)
 
 
+@pytest.mark.parametrize("M,H,E,I,k", [(16, 4104, 8, 2064, 8), (16, 520, 8, 2064, 8), (16, 4104, 8, 528, 8),
+                                       (13, 4168, 8, 2080, 5), (16, 8200, 4, 4112, 3)])
+def test_few_with_several_rows_per_expert(B, dev, M, H, E, I, k):
+    """Enough picks per expert for items of two row groups, in both products, in one, in the other."""
+    _check_few(B, dev, M, H, E, I, k)
+
+
 @pytest.mark.parametrize("rule", [
     dict(softmax=True), dict(softmax=True, renormalize=False, scale=2.5), dict(renormalize=False),
     dict(n_group=4, topk_group=2, group_top=2), dict(n_group=8, topk_group=3, group_top=1, scale=0.5),
