@@ -760,7 +760,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 
 inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Rows of a group: as many as the stage holds of both kinds, a power of two.
+// Rows of a group: as many as the stage holds of both kinds, a power of two.  I up to kMaxI (a larger
+// row's bytes need not fit an int).
+constexpr int kMaxI = kStage / (int)sizeof(float);
 int group_rows(int H, int I) {
   const int row = std::max((H + kUnit - 1) / kUnit * kUnit * 2, (I + kUnit - 1) / kUnit * kUnit * 4);
   int g = kGroupRows;
@@ -770,7 +772,7 @@ int group_rows(int H, int I) {
 
 }  // namespace
 
-bool few_sizes_ok(int H, int I) { return group_rows(H, I) > 0; }
+bool few_sizes_ok(int H, int I) { return I <= kMaxI && group_rows(H, I) > 0; }
 
 size_t few_scratch_bytes(int M, int H, int E, int I, int top_k) {
   return up256((size_t)M * E * sizeof(double)) + up256(sizeof(int)) +

@@ -126,6 +126,13 @@ def test_few_sizes(B):
     assert (B.FEW_MAX_TOKENS, B.FEW_MAX_PICKS) == (16, 512)
 
 
+@pytest.mark.parametrize("I", [32784, 65536, 1 << 24, 1 << 29, 1 << 30, (1 << 31) - 16])
+def test_few_refuses_wide_experts(B, I):
+    """I past what the call takes, also where the bytes of a row of act pass 32 bits."""
+    assert B.moe_few_workspace_bytes(1, 8, 1, I, 1) == 0
+    assert _few(B.load_library(), M=1, H=8, E=1, I=I, k=1, wsb=1 << 62) == -2
+
+
 def test_binding_refuses_host_tensors_and_wrong_types(B):
     bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
     with pytest.raises(ValueError, match="device"):
