@@ -548,7 +548,9 @@ int moe_matmul(const uint16_t* x, int64_t x_ld, const uint16_t* w, const uint16_
  *   out          may be NULL if residual_out is not (norm_w and eps are not looked at then)
  * Any I % 16 == 0 up to 32768 (larger: MOE_ERR_UNSUPPORTED).  workspace of
  * moe_few_workspace_bytes bytes (0 for sizes that are refused), 256-byte aligned; it needs no
- * clearing.  Results do not depend on the number of CUs or on the order of events.
+ * clearing.  It serves one call at a time: calls that share one at once end after some seconds, with
+ * results that mean nothing (NaN among them).  Results do not depend on the number of CUs or on the
+ * order of events.
  */
 #define MOE_FEW_MAX_TOKENS 16
 #define MOE_FEW_MAX_PICKS 512

@@ -26,8 +26,10 @@
 // items of lower tickets, tickets are handed out in order, and a workgroup holds at most the item
 // that it works on and the next one: the unfinished item with the lowest ticket is always being
 // worked on and never waits, so every wait ends, however many workgroups run at once and whatever
-// else runs on the GPU.  A wait is bounded all the same, so that calls that share a workspace at
-// the same time end too (with results that mean nothing).
+// else runs on the GPU.  A wave's polls in a call are bounded all the same, so that calls that share a
+// workspace at the same time end too (with results that mean nothing, NaN among them).  They are
+// counted and not timed: a clock runs on while the queue is suspended, and a wait that it ends may have
+// had its producer suspended with it.
 #include <algorithm>
 #include <type_traits>
 
@@ -45,6 +47,9 @@ constexpr int kStage = 128 * 1024;    // LDS for the tokens' rows
 constexpr int kGroupRows = 8;         // rows of an expert that an item takes, at most
 
 constexpr uint32_t kNotThere = 0xffffffffu;
+// Polls of a wave in a call, a sleep of 512 cycles and a trip past the L2s each: seconds of the wave's
+// own time, where no call takes one.
+constexpr int kPolls = 1 << 22;
 
 // Two products of bf16 pairs added to c.
 __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
@@ -67,10 +72,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const float* base) {
   return __builtin_amdgcn_make_buffer_rsrc((void*)((uint64_t)hi << 32 | lo), 0, -1, 0x00020000);
 }
 // N times 4 values that other workgroups hand over, at byte offsets off[]; -1: none (zeros).  All
-// are asked for at once, and those with a word that is not there again, for at most two seconds.
+// are asked for at once, and those with a word that is not there again, as long as the wave has polls
+// left.
 constexpr int kAgentScope = 16;   // cache policy bit SC1
 template <int N>
-__device__ __forceinline__ void take(__amdgpu_buffer_rsrc_t from, const int (&off)[N], f32x4 (&v)[N]) {
+__device__ __forceinline__ void take(__amdgpu_buffer_rsrc_t from, const int (&off)[N], f32x4 (&v)[N],
+                                     int& polls) {
   u32x4 w[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -84,7 +91,6 @@ __device__ __forceinline__ void take(__amdgpu_buffer_rsrc_t from, const int (&of
 #pragma unroll
   for (int i = 0; i < N; ++i) some |= missing(w[i]);
   if (__any(some)) {
-    const uint64_t end = __builtin_amdgcn_s_memrealtime() + 200000000ull;   // of 100 MHz
     do {
       __builtin_amdgcn_s_sleep(8);
       some = false;
@@ -93,7 +99,7 @@ __device__ __forceinline__ void take(__amdgpu_buffer_rsrc_t from, const int (&of
         if (missing(w[i])) w[i] = __builtin_amdgcn_raw_buffer_load_b128(from, off[i], 0, kAgentScope);
         some |= missing(w[i]);
       }
-    } while (__any(some) && __builtin_amdgcn_s_memrealtime() < end);
+    } while (__any(some) && --polls > 0);
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = __builtin_bit_cast(f32x4, w[i]);
@@ -532,7 +538,7 @@ __device__ __forceinline__ void up_item(const FewArgs& p, FewShared& s, int u, i
 }
 
 template <int RG, int TT>
-__device__ __forceinline__ void down_item(const FewArgs& p, FewShared& s, int u, int tile) {
+__device__ __forceinline__ void down_item(const FewArgs& p, FewShared& s, int u, int tile, int& polls) {
   const int tid = thread_here(), wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int r = lane >> 3, part = lane & 7;
   const int e = s.gexp[u], first = s.gfirst[u], count = s.gcount[u];
@@ -555,7 +561,7 @@ __device__ __forceinline__ void down_item(const FewArgs& p, FewShared& s, int u,
       const int i = i0 + q * kThreads, t = i / per, c = i % per * 4;
       off[q] = i < count * per && c < p.I ? (s.rows[first + t] * p.I + c) * 4 : -1;
     }
-    take(act, off, v);
+    take(act, off, v, polls);
 #pragma unroll
     for (int q = 0; q < 2; ++q)
       if (i0 + q * kThreads < count * per)
@@ -583,7 +589,7 @@ __device__ __forceinline__ void down_item(const FewArgs& p, FewShared& s, int u,
   }
 }
 
-__device__ __forceinline__ void join_item(const FewArgs& p, FewShared& s, int t) {
+__device__ __forceinline__ void join_item(const FewArgs& p, FewShared& s, int t, int& polls) {
   const int tid = thread_here(), wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int k = p.top_k;
   if (wave == 0) {
@@ -616,7 +622,7 @@ __device__ __forceinline__ void join_item(const FewArgs& p, FewShared& s, int t)
           const int h = h0 + c * 4 * kThreads;
           off[j * C + c] = j0 + j < k && h < p.H ? ((j0 + j) * p.H + h) * 4 : -1;
         }
-      take(y, off, v);
+      take(y, off, v, polls);
 #pragma unroll
       for (int j = 0; j < B; ++j) {
         if (j0 + j >= k) break;
@@ -732,6 +738,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   lds_barrier();
   const int groups = all >> 16;
   const int ups = groups * p.up_tiles, downs = groups * p.down_tiles;
+  int polls = kPolls;
   for (;;) {
     const int item = s.ticket;
     lds_barrier();   // read by all, and the stage is free
@@ -746,12 +753,12 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
       else up_item<URG, 8>(p, s, u, tile);
     } else if (item < ups + downs) {
       const int d = item - ups, u = d / p.down_tiles, tile = d % p.down_tiles, c = s.gcount[u];
-      if (c <= 1) down_item<DRG, 1>(p, s, u, tile);
-      else if (c <= 2) down_item<DRG, 2>(p, s, u, tile);
-      else if (c <= 4) down_item<DRG, 4>(p, s, u, tile);
-      else down_item<DRG, 8>(p, s, u, tile);
+      if (c <= 1) down_item<DRG, 1>(p, s, u, tile, polls);
+      else if (c <= 2) down_item<DRG, 2>(p, s, u, tile, polls);
+      else if (c <= 4) down_item<DRG, 4>(p, s, u, tile, polls);
+      else down_item<DRG, 8>(p, s, u, tile, polls);
     } else {
-      join_item(p, s, item - ups - downs);
+      join_item(p, s, item - ups - downs, polls);
     }
     if (draws) s.ticket = next;
     lds_barrier();
