@@ -531,6 +531,11 @@ int moe_block_norm(const void* y, int32_t y_f32, int64_t y_ld,
  */
 enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3, MOE_ACT_GELU_TANH = 4 };
 size_t moe_matmul_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t gated);
+/* Token-tile height that moe_matmul uses at these sizes: 8, 16 or 32 (few tokens, or few results of a
+ * long K), 64 (with K in parts where a workspace is needed), 128 or 256; rows of x more than 2^23
+ * values apart take 128 in the place of 256.  Tiles differ in the order of their sums.  Host-only; 0
+ * for sizes or a stride that moe_matmul refuses. */
+int32_t moe_matmul_tile_rows(int32_t M, int32_t N, int32_t K, int32_t gated, int64_t x_ld);
 int moe_matmul(const uint16_t* x, int64_t x_ld, const uint16_t* w, const uint16_t* bias,
                int32_t M, int32_t N, int32_t K, int32_t act, int32_t gated,
                const void* residual, int32_t residual_f32, int64_t residual_ld,

@@ -28,7 +28,7 @@ __all__ = [
     "SCORE_SIGMOID", "SCORE_SOFTMAX", "moe_i8_quantize", "moe_i8_matmul_workspace_bytes",
     "moe_i8_matmul", "moe_i8_workspace_bytes", "moe_forward_i8",
     "moe_block_norm", "NORM_NONE", "NORM_RMS", "NORM_LAYER",
-    "moe_matmul_workspace_bytes", "moe_matmul", "ACT_NONE", "ACT_RELU", "ACT_SILU", "ACT_GELU",
+    "moe_matmul_workspace_bytes", "moe_matmul_tile_rows", "moe_matmul", "ACT_NONE", "ACT_RELU", "ACT_SILU", "ACT_GELU",
     "ACT_GELU_TANH", "moe_few_workspace_bytes", "moe_forward_few", "FEW_MAX_TOKENS",
     "FEW_MAX_PICKS",
     "HipEvent",
@@ -116,6 +116,7 @@ _PROTOS = {
                                       ctypes.c_float, ctypes.c_float, ctypes.c_float,
                                       ctypes.c_float, _i32, _i32, _p, _i64, _p, _i64, _p]),
     "moe_matmul_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32]),
+    "moe_matmul_tile_rows": (_i32, [_i32, _i32, _i32, _i32, _i64]),
     "moe_matmul": (ctypes.c_int, [_p, _i64, _p, _p, _i32, _i32, _i32, _i32, _i32,
                                   _p, _i32, _i64, _p, _i32, _i64, _p, _sz, _p]),
     "moe_few_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32]),
@@ -970,6 +971,11 @@ def moe_block_norm(y, residual, out, z_out=None, gate=None, post: int = NORM_NON
 
 def moe_matmul_workspace_bytes(M: int, N: int, K: int, gated: bool = False) -> int:
     return int(load_library().moe_matmul_workspace_bytes(M, N, K, 1 if gated else 0))
+
+
+def moe_matmul_tile_rows(M: int, N: int, K: int, gated: bool = False, x_ld: Optional[int] = None) -> int:
+    """x_ld: the stride of x's rows, K by default."""
+    return int(load_library().moe_matmul_tile_rows(M, N, K, 1 if gated else 0, K if x_ld is None else x_ld))
 
 
 def moe_matmul(x, w, out, bias=None, act: int = ACT_NONE, gated: bool = False, residual=None,

@@ -924,14 +924,16 @@ hipError_t launch_big(const GemmArgs& a, hipStream_t s) {
 //   8192  4096  7168    3845   1040   1118    567    373
 // At 128 sizes (M 40 to 8192, N 64 to 7168, K 768 to 7168, gated and not) the pick was within 10 % of
 // the fastest at all but five, the worst 22 %.  Up to 32 tokens the few-token variant takes one block
-// of tokens, and no other was faster by more than 5 %.  Sizes alone decide: a call's workspace does not change its result.
+// of tokens, and no other was faster by more than 5 %.  Sizes decide, and whether 64 rows of x lie within
+// the 32-bit byte offsets of the 256 x 256 variant (else 128 x 128, whose sums have another order); a
+// call's workspace does not change its result.
 enum Variant { kSkinny, kTile64, kTile128, kTile256 };
 struct Choice {
   Variant variant;
   int splits;   // kTile64: parts of K
 };
 constexpr int kMaxSplits = 16;
-Choice choose(int M, int N, int K, bool gated) {
+Choice choose(int M, int N, int K, bool gated, int64_t x_ld) {
   if (M <= 32) return Choice{kSkinny, 1};
   const double rows = gated ? 2.0 * N : N, chunks = (K + kKC - 1) / kKC;
   auto tiles = [&](int m, int w) { return ceil((double)M / m) * ceil(rows / w); };
@@ -957,27 +959,36 @@ Choice choose(int M, int N, int K, bool gated) {
     const double full = t256 < 256 ? t256 / 256 : 1.0;
     offer(kTile256, 1, 5.0 + ceil(t256 / 256) * chunks * (1.25 + 0.35 * full * full * full) + 12.0 * full);
   }
+  if (best.variant == kTile256 && x_ld > kBigMaxLd) best.variant = kTile128;
   return best;
 }
+int skinny_tokens(int M) { return M <= 8 ? 8 : M <= 16 ? 16 : 32; }
 
 template <bool GATED>
 hipError_t launch_sized(const GemmArgs& a, float* partial, hipStream_t s) {
-  const Choice c = choose(a.M, a.N, a.K, GATED);
+  const Choice c = choose(a.M, a.N, a.K, GATED, a.x_ld);
   if (c.splits > 1) return launch_split<GATED>(a, c.splits, partial, s);
-  if (c.variant == kSkinny)
-    return a.M <= 8    ? launch_skinny<1, GATED>(a, s)
-           : a.M <= 16 ? launch_skinny<2, GATED>(a, s)
-                       : launch_skinny<4, GATED>(a, s);
+  if (c.variant == kSkinny) {
+    const int tokens = skinny_tokens(a.M);
+    return tokens == 8    ? launch_skinny<1, GATED>(a, s)
+           : tokens == 16 ? launch_skinny<2, GATED>(a, s)
+                          : launch_skinny<4, GATED>(a, s);
+  }
   if (c.variant == kTile64) return launch_ring<64, 1, 4, 4, GATED>(a, s);
-  if (c.variant == kTile256 && a.x_ld <= kBigMaxLd) return launch_big<GATED>(a, s);
+  if (c.variant == kTile256) return launch_big<GATED>(a, s);
   return launch_ring<128, 2, 4, 5, GATED>(a, s);
 }
 
 }  // namespace
 
 size_t bf16_matmul_scratch_bytes(int M, int N, int K, bool gated) {
-  const int splits = choose(M, N, K, gated).splits;
+  const int splits = choose(M, N, K, gated, K).splits;   // (the same for every stride)
   return splits > 1 ? (size_t)splits * M * partial_ld(N, gated) * sizeof(float) : 0;
+}
+
+int bf16_matmul_tile_rows(int M, int N, int K, bool gated, int64_t x_ld) {
+  const Variant v = choose(M, N, K, gated, x_ld).variant;
+  return v == kSkinny ? skinny_tokens(M) : v == kTile64 ? 64 : v == kTile128 ? 128 : 256;
 }
 
 hipError_t launch_bf16_matmul(const GemmArgs& a, void* scratch, hipStream_t s) {

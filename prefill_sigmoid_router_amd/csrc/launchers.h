@@ -244,6 +244,7 @@ struct GemmArgs {
   float* partial;
 };
 size_t bf16_matmul_scratch_bytes(int M, int N, int K, bool gated);   // 16-byte aligned
+int bf16_matmul_tile_rows(int M, int N, int K, bool gated, int64_t x_ld);
 hipError_t launch_bf16_matmul(const GemmArgs& a, void* scratch, hipStream_t s);
 
 // The layer for a few tokens (few_layer.hip).

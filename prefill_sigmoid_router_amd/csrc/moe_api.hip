@@ -929,6 +929,7 @@ namespace {
 
 constexpr int32_t kMaxNormRows = 1 << 30;
 constexpr int32_t kMaxGemmRows = 1 << 24, kMaxGemmK = 1 << 20;
+constexpr int64_t kMaxGemmResults = (int64_t)1 << 38;
 
 bool row_ld_ok(int64_t ld, int32_t H) { return ld >= H && ld % 8 == 0; }
 bool flag_ok(int32_t f) { return f == 0 || f == 1; }
@@ -1012,6 +1013,11 @@ size_t moe_matmul_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t gated
   return gemm_sizes_ok(M, N, K, gated) ? moe::bf16_matmul_scratch_bytes(M, N, K, gated) : 0;
 }
 
+int32_t moe_matmul_tile_rows(int32_t M, int32_t N, int32_t K, int32_t gated, int64_t x_ld) {
+  if (!gemm_sizes_ok(M, N, K, gated) || (int64_t)M * N >= kMaxGemmResults || !row_ld_ok(x_ld, K)) return 0;
+  return moe::bf16_matmul_tile_rows(M, N, K, gated, x_ld);
+}
+
 int moe_matmul(const uint16_t* x, int64_t x_ld, const uint16_t* w, const uint16_t* bias, int32_t M,
                int32_t N, int32_t K, int32_t act, int32_t gated, const void* residual,
                int32_t residual_f32, int64_t residual_ld, void* out, int32_t out_f32,
@@ -1019,7 +1025,7 @@ int moe_matmul(const uint16_t* x, int64_t x_ld, const uint16_t* w, const uint16_
   if (!gemm_sizes_ok(M, N, K, gated) || act < MOE_ACT_NONE || act > MOE_ACT_GELU_TANH ||
       !flag_ok(residual_f32) || !flag_ok(out_f32))
     return MOE_ERR_INVALID_ARG;
-  if ((int64_t)M * N >= (int64_t)1 << 38) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)M * N >= kMaxGemmResults) return MOE_ERR_UNSUPPORTED;
   if (M == 0) return MOE_OK;
   if (!x || !w || !out || x_ld < K || x_ld % 8 != 0 || out_ld < N || (residual && residual_ld < N) ||
       !aligned(x, 16) || !aligned(w, 16) || !aligned(out, 16) || (bias && !aligned(bias, 16)) ||

@@ -85,6 +85,22 @@ def test_matmul_workspace(B):
                 assert _matmul(B.load_library(), ws=ws, wsb=wsb, **ok) == -3
 
 
+def test_matmul_tile_rows(B):
+    rows = B.moe_matmul_tile_rows
+    assert [rows(M, 7168, 2048) for M in (1, 8, 9, 16, 17, 32)] == [8, 8, 16, 16, 32, 32]
+    assert (rows(640, 2048, 2048), rows(640, 4096, 7168), rows(2048, 7168, 2048)) == (64, 128, 256)
+    assert (rows(640, 4096, 7168, True), rows(8192, 2048, 7168, True)) == (128, 256)
+    # K in parts: on tiles of 64 rows only
+    assert B.moe_matmul_workspace_bytes(200, 1024, 8200) > 0 and rows(200, 1024, 8200) == 64
+    # one chunk of K is too short for the largest tiles
+    assert rows(8192, 8192, 72) == 256 and rows(8192, 8192, 64) < 256
+    # rows of x too far apart for them
+    assert rows(2048, 7168, 2048, x_ld=1 << 23) == 256 and rows(2048, 7168, 2048, x_ld=(1 << 23) + 8) == 128
+    for bad in ((-1, 32, 64), (4, 0, 64), (4, 32, 60), (1 << 24, 1 << 14, 64)):
+        assert rows(*bad) == 0
+    assert rows(4, 32, 64, x_ld=56) == 0 and rows(4, 32, 64, x_ld=68) == 0
+
+
 def _few(lib, **kw):
     a = dict(x=256, rw=256, rb=None, sb=None, w13=256, w2=256, res=256, g=256, eps=1e-5, M=4, H=256, E=8,
              I=512, k=2, score=0, n_group=1, topk_group=1, group_top=1, renorm=1, scale=1.0, out=256,
