@@ -162,3 +162,39 @@ def test_tiles_of_64_and_128(B, dev, tile, M, N, K, gated):
     _check(B, dev, tile, M, N, K, gated=gated, act="silu" if gated else "none")
     _check(B, dev, tile, M, N, K, "gelu", gated, bias=True, res=F32, ot=F32, pad=8)
     _check(B, dev, tile, M, N, K, "gelu_tanh", gated, res=BF16, pad=24, in_place=True)
+
+
+# Parts: 2, 4, 8 and 16 of them; K % 64 != 0, where a part ends with a partial chunk, and whole chunks
+PARTS = [(200, 1024, 8200, False), (77, 4099, 7176, False), (40, 512, 7112, False), (200, 300, 8264, False),
+         (100, 256, 16392, False), (130, 520, 9000, False), (33, 257, 16440, False), (300, 140, 12040, False),
+         (77, 4099, 7168, False), (65, 64, 65544, False), (200, 1024, 8200, True), (77, 4099, 7176, True),
+         (200, 300, 8264, True), (33, 1030, 4104, True), (100, 256, 16392, True), (33, 257, 16440, True),
+         (500, 130, 8008, True), (300, 140, 12040, True), (36, 2000, 7168, True), (65, 64, 65544, True)]
+
+
+@pytest.mark.parametrize("M,N,K,gated", PARTS)
+def test_parts_of_k(B, dev, M, N, K, gated):
+    """The sums of K's parts meet in the workspace (filled with NaN here)."""
+    _check(B, dev, 64, M, N, K, gated=gated, parts=True)
+    _check(B, dev, 64, M, N, K, "gelu", gated, bias=True, res=BF16, pad=8, parts=True)
+    _check(B, dev, 64, M, N, K, "silu", gated, bias=True, res=F32, ot=F32, pad=24, parts=True, in_place=True)
+
+
+def test_parts_of_k_keep_rows_apart(B, dev):
+    """A token or a weight row that is not finite, in the last, partial chunk, changes its own row or column
+    only."""
+    for M, N, K, gated in PARTS[:4] + PARTS[10:13]:
+        need = B.moe_matmul_workspace_bytes(M, N, K, gated)
+        assert need > 0
+        g = _gen(dev, 4)
+        x, w = _randn(g, (M, K)), _randn(g, (2 * N if gated else N, K), 0.05)
+        ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=dev)
+        want, got = (torch.empty(M, N, dtype=BF16, device=dev) for _ in range(2))
+        B.moe_matmul(x, w, want, gated=gated, workspace=ws)
+        x[M - 1, K - 1], w[N // 2, K - 3] = float("nan"), float("inf")
+        B.moe_matmul(x, w, got, gated=gated, workspace=ws)
+        torch.cuda.synchronize()
+        assert not torch.isfinite(got[M - 1]).any() and not torch.isfinite(got[:, N // 2]).any()
+        keep = torch.ones(M, N, dtype=torch.bool, device=dev)
+        keep[M - 1], keep[:, N // 2] = False, False
+        assert torch.equal(got[keep], want[keep])
