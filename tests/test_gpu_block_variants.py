@@ -1,7 +1,10 @@
-"""Each variant of the bf16 product on the GPU against 64 bits, at sizes that are known to take it.
+"""Each variant of the bf16 product on the GPU against 64 bits, at sizes that are known to take it, and
+the block norm where its workgroups or waves walk several rows.
 
 Bounds count roundings: u = 2^-24 for one in fp32, 2^-8 for the last one to bf16 (2^-24 to fp32).
 """
+import math
+
 import pytest
 import torch
 
@@ -198,3 +201,133 @@ def test_parts_of_k_keep_rows_apart(B, dev):
         keep = torch.ones(M, N, dtype=torch.bool, device=dev)
         keep[M - 1], keep[:, N // 2] = False, False
         assert torch.equal(got[keep], want[keep])
+
+
+# ---------------------------------------------------------------------------------------
+# Block norm: more rows than run at once, in each variant
+# ---------------------------------------------------------------------------------------
+NONE, RMS, LAYER = 0, 1, 2
+
+
+def _norm(v, err, kind, w, b, offset, eps):
+    """N(v) in 64 bits, and a bound of the kernel's error where its v is off by up to err.
+
+    A sum over a row is a chain of at most 32 values a thread, 6 steps in the wave and 16 waves, 54
+    roundings, and a term of it rounds twice.  The mean is off by dm = 57 u mean |v| and the mean of err.
+    A difference d from it then is off by err + dm + u |d|, the mean of squares m2 by 58 u of itself and
+    2 rms(d) (rms(err) + dm) and the square of those errors, its root by half of that relative to m2 + eps,
+    and root and quotient round (4 u).  d f (offset + w) + b: 5 roundings more."""
+    if kind == NONE:
+        return v, err
+    dm = torch.zeros_like(v[:, :1])
+    d = v
+    if kind == LAYER:
+        dm = 57 * U * v.abs().mean(dim=1, keepdim=True) + err.mean(dim=1, keepdim=True)
+        d = v - v.mean(dim=1, keepdim=True)
+    m2 = (d * d).mean(dim=1, keepdim=True)
+    f = 1.0 / torch.sqrt(m2 + eps)
+    r = (err * err).mean(dim=1, keepdim=True).sqrt() + dm
+    rel = (29 + 4) * U + r * f + 0.5 * (r * f) ** 2
+    g = torch.ones_like(v[:1]) if w is None else (offset + w.double())[None, :]
+    out = d * f * g
+    off = ((err + dm) * f * (1 + rel) + (d * f).abs() * (rel + 6 * U)) * g.abs()
+    if b is not None:
+        out = out + b.double()
+        off = off + U * (out.abs() + off)
+    return out, off
+
+
+def _norm_inputs(dev, M, H, post, pre, gate, yt, rt, weights, bias, offset, pad, y_mean=0.0):
+    g = _gen(dev, M * 7 + H)
+    s = dict(y=Rows(M, H, yt, dev, pad, _randn(g, (M, H), 1.0, y_mean, yt)),
+             r=Rows(M, H, rt, dev, 2 * pad, _randn(g, (M, H), 3.0, 0.0, rt)))
+    for n, kind in (("post", post), ("pre", pre)):
+        s[n + "_w"] = _randn(g, (H,), 0.05, 1.0 - offset) if weights and kind else None
+        s[n + "_b"] = _randn(g, (H,), 0.1) if bias and kind else None
+    shape = {"none": None, "channel": (H,), "full": (M, H), "token": (M, 1), "one": (1, 1)}[gate]
+    s["gate"] = None if shape is None else _randn(g, shape, 0.3, 0.7)
+    return s
+
+
+def _call(B, s, y, r, out, z, post, pre, offset, a, b):
+    B.moe_block_norm(y, r, out, z_out=z, gate=s["gate"], post=post, post_w=s["post_w"], post_b=s["post_b"],
+                     pre=pre, pre_w=s["pre_w"], pre_b=s["pre_b"], eps=1e-5, weight_offset=offset,
+                     residual_scale=a, block_scale=b)
+
+
+def _check_norm(B, dev, M, H, post=RMS, pre=RMS, gate="none", yt=BF16, rt=BF16, weights=True, bias=False,
+                offset=0.0, a=1.0, b=1.0, pad=0, y_mean=0.0):
+    s = _norm_inputs(dev, M, H, post, pre, gate, yt, rt, weights, bias, offset, pad, y_mean)
+    z, out = Rows(M, H, rt, dev, pad), Rows(M, H, BF16, dev, 3 * pad)
+    _call(B, s, s["y"].t, s["r"].t, out.t, z.t, post, pre, offset, a, b)
+    torch.cuda.synchronize()
+    yd = s["y"].t.double()
+    want, err = _norm(yd, torch.zeros_like(yd), post, s["post_w"], s["post_b"], offset, 1e-5)
+    scale = torch.tensor(b, dtype=torch.float64, device=dev)
+    if s["gate"] is not None:
+        gd = s["gate"].double()
+        scale = scale * (gd if gd.dim() == 2 else gd[None, :])
+    want, err = scale * want, scale.abs() * (err + 4 * U * want.abs())      # products in any order, sums of two
+    rd = a * s["r"].t.double()
+    err = err + U * rd.abs() + 2 * U * ((want + rd).abs() + want.abs() + err)
+    want = want + rd
+    for rows in (s["y"], s["r"], z, out):
+        assert rows.untouched()
+    off = (z.t.double() - want).abs()
+    assert (off <= err + _round(rt) * (want.abs() + err)).all(), off.max().item()
+    w2, e2 = _norm(want, err, pre, s["pre_w"], s["pre_b"], offset, 1e-5)
+    off = (out.t.double() - w2).abs()
+    assert (off <= e2 + _round(BF16) * (w2.abs() + e2)).all(), off.max().item()
+
+
+# rows of each variant, more than twice as many as 256 CUs hold at once: a wave per row with one chunk
+# a lane (8192 rows at once) or two (4096), a workgroup per row with two (4096 at H = 1032, 2560 at
+# 2056, 1024 at 7168 and 8192) or four (512)
+WALKS = [(17000, 264), (17000, 512), (9001, 520), (9001, 1000), (9001, 1024), (9001, 1032), (6001, 2056),
+         (2300, 7168), (2300, 8192), (1300, 8200), (1300, 12296), (1300, 16384)]
+
+
+@pytest.mark.parametrize("M,H", WALKS)
+def test_norm_walks_rows(B, dev, M, H):
+    _check_norm(B, dev, M, H, gate="channel", offset=1.0, b=0.25)
+    _check_norm(B, dev, M, H, LAYER, LAYER, "full", F32, F32, bias=True, a=0.5, b=1.5, pad=8)
+    _check_norm(B, dev, M, H, LAYER, RMS, "token", F32, BF16, bias=True, pad=16)
+    _check_norm(B, dev, M, H, RMS, LAYER, "channel", BF16, F32, bias=True, offset=1.0)
+    _check_norm(B, dev, M, H, NONE, LAYER, "full", BF16, BF16, weights=False, a=-1.0, pad=8)
+    _check_norm(B, dev, M, H, LAYER, NONE, "one", F32, F32, b=0.5)
+    _check_norm(B, dev, M, H, LAYER, LAYER, "none", F32, F32, y_mean=64.0)
+
+
+@pytest.mark.parametrize("M,H", [(9001, 1000), (9001, 264), (2300, 7168), (9001, 1032), (1300, 16384), (600, 2056)])
+@pytest.mark.parametrize("yt,rt,gate", [(BF16, BF16, "channel"), (BF16, F32, "full"), (BF16, F32, "none")])
+def test_norm_walks_rows_in_place(B, dev, M, H, yt, rt, gate):
+    """out over y and z over the residual: the next row is read before this one is written."""
+    s = _norm_inputs(dev, M, H, LAYER, RMS, gate, yt, rt, True, True, 0.0, 8)
+    z, out = Rows(M, H, rt, dev, 8), Rows(M, H, BF16, dev, 8)
+    args = (LAYER, RMS, 0.0, 0.5, 2.0)
+    _call(B, s, s["y"].t, s["r"].t, out.t, z.t, *args)
+    _call(B, s, s["y"].t, s["r"].t, s["y"].t, s["r"].t, *args)
+    torch.cuda.synchronize()
+    assert torch.equal(s["y"].t, out.t) and torch.equal(s["r"].t, z.t)
+    assert s["y"].untouched() and s["r"].untouched()
+
+
+@pytest.mark.parametrize("M,H", WALKS)
+def test_norm_walks_past_rows_that_are_not_finite(B, dev, M, H):
+    """A row with a NaN or an infinity leaves the others as they were, those that its workgroup takes after
+    it among them; a row of zeros is one."""
+    s = _norm_inputs(dev, M, H, LAYER, RMS, "token", BF16, F32, True, True, 0.0, 0)
+    z, out, z2, out2 = Rows(M, H, F32, dev), Rows(M, H, BF16, dev), Rows(M, H, F32, dev), Rows(M, H, BF16, dev)
+    args = (LAYER, RMS, 0.0, 1.0, 1.0)
+    _call(B, s, s["y"].t, s["r"].t, out.t, z.t, *args)
+    rows = torch.arange(0, M, 7, device=dev)
+    s["y"].t[rows[0::3], H // 2] = math.nan
+    s["r"].t[rows[1::3], H - 1] = math.inf
+    s["y"].t[rows[2::3]] = 0.0
+    _call(B, s, s["y"].t, s["r"].t, out2.t, z2.t, *args)
+    torch.cuda.synchronize()
+    keep = torch.ones(M, dtype=torch.bool, device=dev)
+    keep[rows] = False
+    assert torch.equal(out.t[keep], out2.t[keep]) and torch.equal(z.t[keep], z2.t[keep])
+    assert not torch.isfinite(out2.t[rows[0::3]]).any() and torch.isfinite(out2.t[rows[2::3]]).all()
+    assert not torch.isfinite(out2.t[rows[1::3], H - 1]).any()
