@@ -19,7 +19,7 @@ namespace {
 constexpr int kKC = 64;   // K values per chunk: one 128-byte line per row
 
 // __expf is exp2 of a rounded product: within about (1.5 |z| + 2) 2^-24 of itself; the reciprocal
-// within 2^-23.
+// within 2^-23.  Where it would be subnormal (z < -87) it may be 0.
 __device__ __forceinline__ float sigmoid_fast(float z) {
   return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
 }
@@ -626,8 +626,9 @@ hipError_t launch_skinny(const GemmArgs& a, hipStream_t s) {
 // accumulation registers: fragment reads then take half of the LDS's rate (8 waves of 64 x 128:
 // three quarters, and with the copies' writes all of it).
 //
-// 8192 x 2 x 2048 x 7168, gated: 377 us (1.28 PFLOP/s; a library product of the same sizes without
-// the epilogue 375), MFMAs busy 62 % of the time at 1.9 GHz.
+// 8192 x 2 x 2048 x 7168, gated: 379 us (1.27 PFLOP/s; a library product of the same sizes without
+// the epilogue 309), MFMAs busy 62 % of the time at 1.9 GHz.  That is from some 100 calls in a row on;
+// the first 40 after a pause, while the clock settles, take 390 to 530 (the library's 310 to 520).
 // K in chunks of 64, a panel of 256 weight rows and one of 256 token rows each, in a ring of five
 // LDS slots of 32 KiB: two of the present chunk, two of the next, one more.  A chunk is 4 steps of
 // 16 values; a step's 16 MFMAs run on one of two sets of fragment registers while the next step's

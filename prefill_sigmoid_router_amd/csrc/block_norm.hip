@@ -8,10 +8,14 @@
 // Everything between the loads and the two stores is fp32 in registers (out comes from the
 // unrounded z).  The mean of squared distances is taken around each wave's own mean and moved
 // to the row's (Chan's pairwise formula: n_w (mean_w - mean)^2 more), so a row whose mean is
-// far above its spread loses nothing, and a LAYER norm costs one barrier as an RMS norm does.
+// far above its spread loses no more than the mean's own fp32 roundings, and a LAYER norm costs one
+// barrier as an RMS norm does.
 // Bound by memory where there are many rows: 8192 x 7168, bf16, RMS twice and a gate per channel (470
-// MB) takes 91 to 97 us, 4.8 to 5.1 TB/s, where a large copy reaches 4.9.  One row of 7168 takes 4.4
-// us: a launch, a load and two reductions.
+// MB) takes 91 to 97 us, 4.8 to 5.1 TB/s, where a large copy reaches 4.9; with a gate value for every
+// token and channel 113 (5.2).  Gates of the tokens and biases are loaded for each row, behind the next
+// row's values, which a wave then waits for: token gate and biases 103 us (4.6 TB/s), LAYER norms twice
+// with biases 109 (4.3), those and a full gate 141 (4.2).  One row of 7168 takes 4.4 us: a launch, a
+// load and two reductions.
 #include <algorithm>
 #include <type_traits>
 
@@ -281,8 +285,8 @@ hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t s) {
   // One or two rows a CU, as many threads as it takes: H = 2048, M = 256 3.7 (two chunks a thread
   // 4.3); H = 7168, M = 8 4.5 (4.8).
   if (a.M <= 2 * cus) return go(integral_constant<int, 1>{}, group, 2);
-  // Many rows, two chunks a thread, 16 waves a CU twice over: H = 2048, M = 8192 28.7 (one chunk
-  // 33.6); H = 7168, M = 1024 16.7 (18.0), M = 8192 91 to 97 (95; a workgroup for each row that reads
+  // Many rows, two chunks a thread, 16 waves a CU twice over: H = 2048, M = 8192 24.5 (one chunk
+  // 31.0); H = 7168, M = 1024 15.9 (16.9), M = 8192 93.0 (91.4; a workgroup for each row that reads
   // what belongs to the channels anew 190).
   if (chunks <= 2 * kWave) return go(integral_constant<int, 2>{}, wave, 4);
   return go(integral_constant<int, 2>{}, group, 32 / ((chunks + 127) / 128));

@@ -11,13 +11,19 @@
 //   down  y[i, h] = act[i] . W2[e, h] for 64 of its rows (DRG = 2: 128)
 //   join  z = sum_j w_j y[t k + j] + residual, out = z * (mean z^2 + eps)^-1/2 * norm_w
 // At a few tokens an expert has few rows, so the layer is a stream of its weights (M=8, H=7168,
-// I=2048, k=16: 9 GB) and the arithmetic is small: no LDS ring and no MFMA tile, but dot
+// I=2048, k=16: 8 to 9 GB) and the arithmetic is small: no LDS ring and no MFMA tile, but dot
 // products straight from the load registers.  A load is 8 weight rows x one 128-byte line,
 // nontemporal; a wave keeps 16 to 24 KiB of them in flight and runs on by itself, without a
-// barrier, to the end of its rows: M=8 1.25 to 1.39 ms from box to box (6.5 to 7.3 TB/s, the rate of
-// a plain read), M=1 224 us (6.3).  Small layers are a chain of latencies: H=2048, I=1408, 4 of 60
-// experts, one token 26.5 us, of which 10 are its bytes.  The tokens' rows (x in bf16, act in fp32) lie in LDS.  act and
-// y stay in fp32 at all times, so the layer rounds only its outputs.
+// barrier, to the end of its rows: M=8 1.24 to 1.38 ms for the 92 to 101 experts that it touches
+// (6.2 to 6.6 TB/s; a plain read reaches 7.1), M=1 222 us (6.4).  Small layers are a chain of
+// latencies and too few items for the CUs: H=2048, I=1408, 4 of 60 experts, one token 26.5 us, of which
+// 10 are its bytes.  The tokens' rows (x in bf16, act in fp32) lie in LDS.  act and y stay in fp32 at all
+// times, so the layer rounds only its outputs.
+//
+// An expert's weights are read once for each group of up to 8 of its rows (fewer where the LDS does not
+// hold 8: from H > 8192 or I > 4096 on), so several tokens per expert cost more than the bytes: 16
+// tokens, 8 of 16 experts, H=7168, I=2048 read 2.0 GB for 1.4 (380 us, where 199 would do), 2 of 8,
+// H=4096, I=14336 6.3 for 2.8 (953 us and 397).
 //
 // Hand-overs: act and y are written and read past the XCDs' L2s (agent-scope accesses) and carry
 // their own flag: a word that has not been written holds kNotThere, a NaN that no result is stored
@@ -811,8 +817,8 @@ hipError_t launch_few_layer(FewArgs a, void* scratch, hipStream_t s) {
   if (err != hipSuccess) return err;
   // Two groups of 8 rows per wave where an expert has several rows (4 picks per expert on average) and
   // every CU still gets an item: each read of a token's values from LDS then serves both.  16 tokens,
-  // 8 of 16 experts, H = 7168, I = 2048: 351 us, one group 410; 2 of 4 experts, H = I = 4096: 136 and
-  // 150.  With few rows per expert small items spread better: 3 tokens, 6 of 64 experts, H = 4096,
+  // 8 of 16 experts, H = 7168, I = 2048: 351 us (to 380 from box to box), one group 410; 2 of 4 experts,
+  // H = I = 4096: 136 and 150.  With few rows per expert small items spread better: 3 tokens, 6 of 64 experts, H = 4096,
   // I = 1536: 105 us, two groups 114; one token, 4 of 60, H = 2048, I = 1408: 26.6 and 33.4.  (Four
   // groups were never faster.)
   const long groups = std::min((long)a.M * a.top_k, (long)a.E);
